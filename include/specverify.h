@@ -36,6 +36,10 @@
  *   - spec_kv_compact: after verification, keep the accepted entries of the
  *     KV cache at consecutive positions and cut the length after them
  *     (lotook.com, KV-cache section; SubSpec review, step "Update KV").
+ *   - spec_kv8_append, spec_kv8_attention, spec_kv8_compact: the target's (or
+ *     a drafter's) KV cache in 8 bits and pages around a verification step:
+ *     rotate and append the K+1 draft positions or tree nodes, attend over the
+ *     cache under the chain's or the merged tree's mask, keep the accepted path.
  *
  * Conventions shared by every call.
  *   - Pointers marked "device" are device pointers owned by the caller (only
@@ -72,8 +76,9 @@
 extern "C" {
 #endif
 
-/* Element type of logit buffers. */
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
+/* Element type of logit buffers (fp32, bf16) and of the spec_kv8_* calls'
+ * activations (these calls alone also take fp16). */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype;
 
 /* Return codes. */
 enum {
@@ -97,6 +102,9 @@ enum {
 #define SPEC_ROW_MASK 16  /* a retrieve row that contradicts tree_mask */
 #define SPEC_ROW_WARP 32  /* spec_tree_expand: more than 4096 tokens of one frontier node tie at its M-th
                              largest logit (never set by the chain calls) */
+
+#define SPEC_ROW_CACHE 64 /* spec_kv8_*: a sequence's lengths, or the id of a cache block it uses, are out of range */
+#define SPEC_ROW_TIMEOUT 128 /* spec_kv8_attention: a wait inside the kernel ran out (never seen in a sound run) */
 
 /* Limits: 1 <= B <= 65535; 0 <= K <= 255; 2 <= V <= 2^24; for trees
  * 1 <= N <= 1024, 1 <= D <= 64, 1 <= R <= 4096. */
@@ -395,6 +403,129 @@ int spec_tree_expand(const void* draft_logits, int dtype, float temperature, con
 int spec_kv_compact(void* kv, int elem_bytes, int n_planes, int B, int S, int W, long long stride_plane,
                     long long stride_batch, long long stride_pos, const int32_t* base_pos, const int32_t* path, int D,
                     const int32_t* accept_len, int32_t* new_len, int32_t* row_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A paged KV cache in 8 bits (one layer).
+ *
+ * The cache is a pool of num_blocks blocks of `block` tokens. Block i, KV head
+ * h, slot s holds head_dim e4m3 codes of the key, and as many of the value, at
+ * byte i * stride_block + h * stride_head + s * stride_slot of k and of v. Every
+ * block and head has one scale for its keys and one for its values, a power of
+ * two stored as an e8m0 byte (2^(byte - 127)) at element i * kv_heads + h of
+ * k_scale and v_scale. An entry's value is code * scale. Scales lie in
+ * [2^-40, 2^40]; another byte is read as the nearest of the two bounds.
+ * block_table[b] lists the blocks of sequence b: its token at position t lies
+ * in slot t mod block of block block_table[b][t / block]. Entries behind the
+ * blocks in use are not read. cache_len[b] is the number of tokens sequence b
+ * holds before the step.
+ * Powers of two: code * scale is exact, a block whose scale grows keeps its
+ * values but for those that leave the codes' normal range, and scores and
+ * weights take the scale as an exponent.
+ *
+ * Limits: block 16, 32, 64 or 128; head_dim 64 or 128; 1 <= kv_heads <= 1024;
+ * 1 <= B <= 65535; num_blocks, max_blocks >= 1, num_blocks * kv_heads < 2^31.
+ * Alignment: k and v 16 bytes and the three strides (bytes) multiples of 16;
+ * stride_slot >= head_dim. Blocks, heads and slots may lie in any order. */
+typedef struct {
+  void* k;                    /* device, codes */
+  void* v;                    /* device, codes */
+  uint8_t* k_scale;           /* device [num_blocks][kv_heads] */
+  uint8_t* v_scale;           /* device [num_blocks][kv_heads] */
+  const int32_t* block_table; /* device [B][max_blocks] */
+  const int32_t* cache_len;   /* device [B] */
+  int32_t B, num_blocks, max_blocks, block, kv_heads, head_dim;
+  int64_t stride_block, stride_head, stride_slot; /* bytes, multiples of 16 */
+} spec_kv8_cache;
+
+/* Append the step's keys and values, rotated, to the cache; optionally rotate
+ * its queries in the same launch.
+ *   keys, values  device, `dtype` (SPEC_F32, SPEC_BF16 or SPEC_F16): token t of
+ *       the T packed tokens, head h starts at element t * stride_token +
+ *       h * stride_head of its tensor (any strides; head_dim innermost,
+ *       contiguous). Rows on 16-byte boundaries are read 16 bytes at a time.
+ *   cu_tokens     device [B + 1] int32: sequence b has tokens cu_tokens[b] to
+ *       cu_tokens[b + 1] - 1 (none is allowed); its i-th goes to position
+ *       cache_len[b] + i. cache_len itself is not changed.
+ *   positions     device [T] int32 or NULL: the position that token t is
+ *       rotated by (a tree node's: cache_len + its depth); NULL: the position
+ *       it is stored at.
+ *   inv_freq      HOST [rot_dim / 2] fp64 or NULL (no rotation; rot_dim 0): pair
+ *       i of the first rot_dim dimensions turns by positions * inv_freq[i]
+ *       radians. The angle is reduced in 64-bit integer turns, so it is as good
+ *       at position 2^31 as at 1. rot_dim: a multiple of 16 up to head_dim.
+ *   interleaved   0: pair i is (i, i + rot_dim / 2); 1: (2 i, 2 i + 1)
+ *   queries, queries_out  device or NULL: [T][q_heads] rows of the same dtype
+ *       and strides of their own, rotated alike (queries_out may be queries).
+ * Scales: a token needs the least 2^e in range with max |x| <= 448 * 2^e over
+ * its finite entries. A block whose first slot this call writes gets the
+ * largest need of its tokens; a block that already holds tokens keeps its
+ * scale, or takes the largest need where that is larger, and its other codes
+ * are then rounded to the new scale. Codes: nearest even, magnitudes over 448
+ * (only at scale 2^40) give 448; NaN and infinities give the NaN code.
+ * Rotation and quantisation are computed in fp32.
+ * Output: row_status [B] int32: SPEC_ROW_CACHE where cu_tokens or cache_len of a
+ * sequence is invalid or the table too short (nothing of it is written), or
+ * where the id of a block it writes is outside the pool (that block is not
+ * written). Two sequences must not write the same block.
+ * Errors: SPEC_ERR_ARG for NULL pointers, sizes, dtype or strides outside the
+ * above; SPEC_ERR_UNSUPPORTED beyond the limits (T * kv_heads < 2^26). */
+int spec_kv8_append(const spec_kv8_cache* cache, const void* keys, int64_t k_stride_token, int64_t k_stride_head,
+                    const void* values, int64_t v_stride_token, int64_t v_stride_head, int dtype, int T,
+                    const int32_t* cu_tokens, const int32_t* positions, const double* inv_freq, int rot_dim,
+                    int interleaved, const void* queries, int64_t q_stride_token, int64_t q_stride_head,
+                    void* queries_out, int64_t qo_stride_token, int64_t qo_stride_head, int q_heads,
+                    int32_t* row_status, void* stream);
+
+/* Attention of the step's queries over the cache: for sequence b, its token i
+ * and query head a of KV head h = a / (q_heads / kv_heads),
+ *     out = sum_t softmax_t(sm_scale * q . k_t) v_t
+ * over the cache_len[b] tokens of the context and those of the step's tokens
+ * (positions cache_len[b] + j, appended before) that token i sees: j <= i, or
+ * with tree_mask those with tree_mask[b][i][j] != 0. A row that sees nothing is
+ * 0. Entries that a row does not see do not reach it, NaN or not.
+ *   queries, out  device, dtype SPEC_BF16 or SPEC_F16: token t, head a at element
+ *       t * stride_token + a * stride_head (any strides; head_dim contiguous)
+ *   cu_tokens     as in spec_kv8_append
+ *   max_tokens    no sequence has more step tokens than this
+ *   tree_mask     device [B][max_tokens][max_tokens] uint8 or NULL (as written by
+ *       spec_merge_trees with N = max_tokens)
+ *   sm_scale      finite
+ *   q_heads       a multiple of kv_heads, at most 64 * kv_heads
+ * Scores, maxima, sums and the accumulated output are fp32; queries and
+ * softmax weights enter the products as two (bf16) or three (fp16) e4m3 terms.
+ * The keys' and values' codes enter the tensor cores as they are.
+ * Outputs: out; row_status [B] int32: SPEC_ROW_CACHE where the sequence's lengths
+ * are invalid (cu_tokens not rising or outside [0, T], more than max_tokens,
+ * cache_len negative or beyond the table) or one of its blocks' ids is outside
+ * the pool: its rows are NaN where its cu_tokens are valid. Tokens of no
+ * sequence are not written.
+ * workspace: spec_kv8_workspace_bytes(...) bytes, 256-byte aligned, needing no
+ * initialisation. Errors: SPEC_ERR_ARG, SPEC_ERR_WORKSPACE as usual;
+ * SPEC_ERR_UNSUPPORTED beyond the limits (T * q_heads < 2^31; with tree_mask
+ * max_tokens <= 1024). */
+size_t spec_kv8_workspace_bytes(const spec_kv8_cache* cache, int q_heads, int max_tokens, int dtype);
+int spec_kv8_attention(const spec_kv8_cache* cache, const void* queries, int64_t q_stride_token,
+                       int64_t q_stride_head, int dtype, int T, int q_heads, const int32_t* cu_tokens, int max_tokens,
+                       const uint8_t* tree_mask, float sm_scale, void* out, int64_t o_stride_token,
+                       int64_t o_stride_head, int32_t* row_status, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* spec_kv_compact for this cache: after verification of a tree, position
+ * cache_len[b] + t receives the entry of position cache_len[b] + path[b][t],
+ * t = 0 .. accept_len[b], in every one of n_planes caches (layers) that share
+ * the block table: codes stride_plane bytes, scales scale_stride_plane bytes
+ * apart. Entries are moved as values: a block that receives some takes the
+ * largest of its scale and the needs (see spec_kv8_append) of the entries moved
+ * into it, and when its scale grows its other codes are rounded to it. Scales
+ * never shrink here. In place.
+ * path NULL: chain verification, nothing moves. Rows are checked as by
+ * spec_kv_compact (SPEC_ROW_TREE, new_len -1; accept_len < 0: new_len -1,
+ * status 0), plus SPEC_ROW_CACHE (new_len -1, nothing moved) for an invalid
+ * cache_len or block id. D <= 64. n_planes >= 1; 1 <= n_planes * B * kv_heads
+ * < 2^30. */
+int spec_kv8_compact(const spec_kv8_cache* cache, int n_planes, int64_t stride_plane, int64_t scale_stride_plane,
+                     const int32_t* path, int D, const int32_t* accept_len, int32_t* new_len, int32_t* row_status,
+                     void* stream);
 
 /* Static description of a return code. */
 const char* spec_status_string(int status);

@@ -19,6 +19,10 @@ __all__ = [
     "spec_tree_entropy",
     "spec_tree_expand",
     "spec_kv_compact",
+    "spec_kv8_append",
+    "spec_kv8_attention",
+    "spec_kv8_compact",
+    "kv8_workspace_bytes",
     "workspace_bytes",
     "warped_workspace_bytes",
     "host_workspace_bytes",

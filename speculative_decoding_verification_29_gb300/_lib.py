@@ -13,15 +13,25 @@ import threading
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libspecverify.so")
 
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_F16 = 0, 1, 2
 SPEC_OK, SPEC_ERR_ARG, SPEC_ERR_ALIGN, SPEC_ERR_CUDA, SPEC_ERR_TIMEOUT, SPEC_ERR_UNIMPLEMENTED = 0, -1, -2, -3, -4, -5
 SPEC_ERR_WORKSPACE, SPEC_ERR_UNSUPPORTED = SPEC_ERR_ALIGN, SPEC_ERR_UNIMPLEMENTED  # older names of the same codes
 SPEC_ROW_TOKEN, SPEC_ROW_TARGET, SPEC_ROW_DRAFT, SPEC_ROW_TREE, SPEC_ROW_MASK, SPEC_ROW_WARP = 1, 2, 4, 8, 16, 32
+SPEC_ROW_CACHE, SPEC_ROW_TIMEOUT = 64, 128
 
 P = ctypes.c_void_p
 I = ctypes.c_int
 F = ctypes.c_float
 Z = ctypes.c_size_t
+L = ctypes.c_int64
+
+
+class Kv8Cache(ctypes.Structure):
+    """spec_kv8_cache of include/specverify.h."""
+
+    _fields_ = ([(n, P) for n in ("k", "v", "k_scale", "v_scale", "block_table", "cache_len")] +
+                [(n, ctypes.c_int32) for n in ("B", "num_blocks", "max_blocks", "block", "kv_heads", "head_dim")] +
+                [(n, L) for n in ("stride_block", "stride_head", "stride_slot")])
 
 SIGNATURES = {
     "spec_workspace_bytes": (Z, [I, I, I, I]),
@@ -42,6 +52,10 @@ SIGNATURES = {
     "spec_tree_expand": (I, [P, I, F, P, I, I, I, I, P, P, P, P, P, Z, P]),
     "spec_kv_compact": (I, [P, I, I, I, I, I, ctypes.c_longlong, ctypes.c_longlong, ctypes.c_longlong, P, P, I, P, P, P,
                             P]),
+    "spec_kv8_append": (I, [P, P, L, L, P, L, L, I, I, P, P, P, I, I, P, L, L, P, L, L, I, P, P]),
+    "spec_kv8_workspace_bytes": (Z, [P, I, I, I]),
+    "spec_kv8_attention": (I, [P, P, L, L, I, I, I, P, I, P, F, P, L, L, P, P, Z, P]),
+    "spec_kv8_compact": (I, [P, I, L, L, P, I, P, P, P, P]),
     "spec_status_string": (ctypes.c_char_p, [I]),
 }
 

@@ -10,12 +10,14 @@ buffers uses.
 
 from __future__ import annotations
 
+import ctypes
+import math
 from typing import Dict, Optional
 
 import torch
 
 from . import _lib
-from ._lib import SPEC_BF16, SPEC_F32, check
+from ._lib import SPEC_BF16, SPEC_F16, SPEC_F32, check
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -375,6 +377,226 @@ def spec_kv_compact(kv: torch.Tensor, base_pos, accept_len, path=None, out: Opti
     check("spec_kv_compact", lib.spec_kv_compact(kv.data_ptr(), kv.element_size(), P_, B, S, W, sp, sb, ss,
                                                  _ptr(base), _ptr(pth), D, _ptr(acc), _ptr(out["new_len"]),
                                                  _ptr(out["row_status"]), _stream(stream)))
+    return out
+
+
+# -------------------------------------------------- the 8-bit paged KV cache --
+
+_KV8_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+
+
+def _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len):
+    """The C record of one layer's cache, checked; the tensors stay the caller's."""
+    dev = k_cache.device
+    if not k_cache.is_cuda or v_cache.device != dev:
+        raise ValueError("k_cache and v_cache must be CUDA tensors of one device (the cache lives there)")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must both be [blocks, kv_heads, block, head_dim], with the same strides")
+    if k_cache.element_size() != 1 or v_cache.element_size() != 1 or k_cache.stride(3) != 1:
+        raise ValueError("k_cache and v_cache hold one byte per code (uint8 or float8_e4m3fn), head_dim contiguous")
+    nb, H, bs, D = k_cache.shape
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t.device != dev or t.element_size() != 1 or t.shape != (nb, H) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [blocks, kv_heads] tensor of bytes (uint8 or float8_e8m0fnu)")
+    _int32(block_table, "block_table", dev)
+    _int32(cache_len, "cache_len", dev)
+    if block_table.dim() != 2 or cache_len.shape != block_table.shape[:1]:
+        raise ValueError("block_table must be [B, max_blocks] and cache_len [B]")
+    sb, sh, ss, _ = k_cache.stride()
+    return _lib.Kv8Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                         block_table.data_ptr(), cache_len.data_ptr(), block_table.shape[0], nb, block_table.shape[1], bs,
+                         H, D, sb, sh, ss)
+
+
+def _int32(t, name, dev):
+    if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on {dev}")
+
+
+def _kv8_rows(t, name, D, dev):
+    """A packed [T, heads, head_dim] activation; returns its token and head strides."""
+    if t.device != dev or t.dim() != 3 or t.shape[2] != D or t.stride(2) != 1:
+        raise ValueError(f"{name} must be a [tokens, heads, {D}] tensor on {dev}, head_dim contiguous")
+    if t.dtype not in _KV8_DTYPES:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return t.stride(0), t.stride(1)
+
+
+def _used_on(stream, *tensors):
+    """Tensors allocated here on the current stream but used on `stream`."""
+    if stream is None:
+        return
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
+def spec_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, cu_tokens, *, inv_freq=None,
+                    interleaved: bool = False, positions=None, q=None, q_out=None,
+                    out: Optional[Dict[str, torch.Tensor]] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """Append the step's keys and values to an 8-bit paged cache, keys rotated.
+
+    k, v [T, kv_heads, head_dim] (fp32, bf16 or fp16; any token and head
+    strides): the packed step tokens, sequence b's at cu_tokens[b] ..
+    cu_tokens[b + 1] - 1 (cu_tokens [B + 1] int32), stored at positions
+    cache_len[b] + i. Cache: k_cache, v_cache [blocks, kv_heads, block,
+    head_dim] (uint8 or float8_e4m3fn codes; strides multiples of 16),
+    k_scale, v_scale [blocks, kv_heads] (uint8 or float8_e8m0fnu), block_table
+    [B, max_blocks] int32, cache_len [B] int32 (not changed by the call).
+    inv_freq: the rotation's rot_dim / 2 angular frequencies (a sequence or a
+    CPU float64 tensor; None: no rotation), pairs (i, i + rot_dim / 2) or, with
+    ``interleaved``, (2 i, 2 i + 1); positions [T] int32 where a token is rotated
+    by another position than it is stored at (tree nodes: cache_len + depth).
+    q [T, q_heads, head_dim]: queries, rotated alike into q_out (allocated when
+    None; may be q). Returns row_status [B] and, with q, q_out."""
+    lib = _lib.load()
+    dev = k_cache.device
+    cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len)
+    D = cache.head_dim
+    kst, ksh = _kv8_rows(k, "k", D, dev)
+    vst, vsh = _kv8_rows(v, "v", D, dev)
+    T, H, _ = k.shape
+    if v.shape != k.shape or v.dtype != k.dtype or H != cache.kv_heads:
+        raise ValueError("k and v must have the same type and shape [tokens, kv_heads, head_dim]")
+    _int32(cu_tokens, "cu_tokens", dev)
+    if cu_tokens.numel() != cache.B + 1:
+        raise ValueError("cu_tokens must have B + 1 entries")
+    if positions is not None:
+        _int32(positions, "positions", dev)
+        if positions.numel() != T:
+            raise ValueError("positions must have one entry per token")
+    qst = qsh = ost = osh = hq = 0
+    made = None
+    if q is not None:
+        qst, qsh = _kv8_rows(q, "q", D, dev)
+        if q_out is None:
+            q_out = made = torch.empty_like(q)
+        ost, osh = _kv8_rows(q_out, "q_out", D, dev)
+        if q.dtype != k.dtype or q_out.dtype != q.dtype or q.shape[0] != T or q_out.shape != q.shape:
+            raise ValueError("q and q_out must be [tokens, q_heads, head_dim] of the keys' type")
+        hq = q.shape[1]
+    rot, freq, held = 0, None, None
+    if inv_freq is not None:
+        if isinstance(inv_freq, torch.Tensor):
+            held = inv_freq.detach().to("cpu", torch.float64).contiguous()
+            rot, freq = 2 * held.numel(), held.data_ptr()
+        else:
+            held = (ctypes.c_double * len(inv_freq))(*inv_freq)
+            rot, freq = 2 * len(inv_freq), ctypes.addressof(held)
+    if out is None:
+        out = dict(row_status=torch.empty(cache.B, dtype=torch.int32, device=dev))
+        _used_on(stream, out["row_status"], made)
+    if q is not None:
+        out["q_out"] = q_out
+    check("spec_kv8_append", lib.spec_kv8_append(
+        ctypes.byref(cache), k.data_ptr(), kst, ksh, v.data_ptr(), vst, vsh, _KV8_DTYPES[k.dtype], T, cu_tokens.data_ptr(),
+        _ptr(positions), freq, rot, int(bool(interleaved)), _ptr(q), qst, qsh, None if q is None else q_out.data_ptr(), ost,
+        osh, hq, out["row_status"].data_ptr(), _stream(stream)))
+    return out
+
+
+def kv8_workspace_bytes(k_cache, block_table, q_heads: int, max_tokens: int, dtype) -> int:
+    """Workspace of spec_kv8_attention for a cache's sizes, the query heads and the longest step."""
+    nb, H, bs, D = k_cache.shape
+    sb, sh, ss, _ = k_cache.stride()
+    cache = _lib.Kv8Cache(*[k_cache.data_ptr()] * 6, block_table.shape[0], nb, block_table.shape[1], bs, H, D, sb, sh, ss)
+    code = dtype if isinstance(dtype, int) else _KV8_DTYPES[dtype]
+    return int(_lib.load().spec_kv8_workspace_bytes(ctypes.byref(cache), q_heads, max_tokens, code))
+
+
+def spec_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, cu_tokens, *, max_tokens: int,
+                       sm_scale: Optional[float] = None, tree_mask=None,
+                       out: Optional[Dict[str, torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None,
+                       stream=None) -> Dict[str, torch.Tensor]:
+    """Attention of the step's queries over an 8-bit paged cache that already
+    holds the step's tokens (spec_kv8_append).
+
+    q [T, q_heads, head_dim] (bf16 or fp16; any token and head strides), packed
+    as the tokens of spec_kv8_append, whose cache arguments it shares; query
+    head a reads KV head a // (q_heads // kv_heads). Token i of sequence b sees the
+    cache_len[b] tokens of the context and the step's tokens j <= i, or with
+    tree_mask [B, max_tokens, max_tokens] uint8 (as written by spec_merge_trees)
+    those with tree_mask[b, i, j] != 0. max_tokens: no sequence has more step
+    tokens. sm_scale: head_dim ** -0.5 when None. Returns out (like q) and
+    row_status [B]."""
+    lib = _lib.load()
+    dev = k_cache.device
+    cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len)
+    qst, qsh = _kv8_rows(q, "q", cache.head_dim, dev)
+    if q.dtype == torch.float32:
+        raise TypeError("q must be bfloat16 or float16")
+    T, hq, _ = q.shape
+    _int32(cu_tokens, "cu_tokens", dev)
+    if cu_tokens.numel() != cache.B + 1:
+        raise ValueError("cu_tokens must have B + 1 entries")
+    if tree_mask is not None:
+        if tree_mask.device != dev or tree_mask.element_size() != 1 or not tree_mask.is_contiguous() or \
+                tree_mask.shape != (cache.B, max_tokens, max_tokens):
+            raise ValueError("tree_mask must be a contiguous [B, max_tokens, max_tokens] tensor of bytes")
+    code = _KV8_DTYPES[q.dtype]
+    made = []
+    if out is None:
+        out = dict(out=torch.empty(q.shape, dtype=q.dtype, device=dev),
+                   row_status=torch.empty(cache.B, dtype=torch.int32, device=dev))
+        made += [out["out"], out["row_status"]]
+    o = out["out"]
+    ost, osh = _kv8_rows(o, "out", cache.head_dim, dev)
+    if o.shape != q.shape or o.dtype != q.dtype:
+        raise ValueError("out must have q's shape and type")
+    if workspace is None:
+        workspace = alloc_workspace(lib.spec_kv8_workspace_bytes(ctypes.byref(cache), hq, max_tokens, code), dev)
+        made.append(workspace)
+    _used_on(stream, *made)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(cache.head_dim)
+    check("spec_kv8_attention", lib.spec_kv8_attention(
+        ctypes.byref(cache), q.data_ptr(), qst, qsh, code, T, hq, cu_tokens.data_ptr(), max_tokens, _ptr(tree_mask),
+        sm_scale, o.data_ptr(), ost, osh, out["row_status"].data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _stream(stream)))
+    return out
+
+
+def spec_kv8_compact(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, accept_len, path=None,
+                     out: Optional[Dict[str, torch.Tensor]] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """Compaction of an 8-bit paged cache along the accepted path of a tree
+    verification, in place.
+
+    k_cache, v_cache [blocks, kv_heads, block, head_dim] with k_scale, v_scale
+    [blocks, kv_heads], or, for layers that share the block table, [planes, ...] of
+    each (any plane stride). cache_len [B]: position of node 0; accept_len [B] and
+    path [B, D] (None for chain verification) as returned by the verification
+    call. Returns new_len [B] and row_status [B]."""
+    lib = _lib.load()
+    planes, sp, ssp = 1, 0, 0
+    kc, vc, ks, vs = k_cache, v_cache, k_scale, v_scale
+    if k_cache.dim() == 5:
+        planes = k_cache.shape[0]
+        if v_cache.shape != k_cache.shape or k_scale.shape[:1] != (planes,) or v_scale.shape[:1] != (planes,) or planes < 1:
+            raise ValueError("k_cache, v_cache, k_scale and v_scale must have the same planes")
+        sp, ssp = k_cache.stride(0), k_scale.stride(0)
+        if v_cache.stride(0) != sp or v_scale.stride(0) != ssp:
+            raise ValueError("keys and values must have the same plane strides")
+        kc, vc, ks, vs = k_cache[0], v_cache[0], k_scale[0], v_scale[0]
+    cache = _kv8_cache(kc, vc, ks, vs, block_table, cache_len)
+    dev = kc.device
+    _int32(accept_len, "accept_len", dev)
+    if accept_len.numel() != cache.B:
+        raise ValueError("accept_len must have B entries")
+    D = 0
+    if path is not None:
+        _int32(path, "path", dev)
+        if path.dim() != 2 or path.shape[0] != cache.B:
+            raise ValueError("path must be [B, D]")
+        D = path.shape[1]
+    if out is None:
+        out = dict(new_len=torch.empty(cache.B, dtype=torch.int32, device=dev),
+                   row_status=torch.empty(cache.B, dtype=torch.int32, device=dev))
+        _used_on(stream, *out.values())
+    check("spec_kv8_compact", lib.spec_kv8_compact(ctypes.byref(cache), planes, sp, ssp, _ptr(path), D,
+                                                   accept_len.data_ptr(), out["new_len"].data_ptr(),
+                                                   out["row_status"].data_ptr(), _stream(stream)))
     return out
 
 

@@ -1,0 +1,485 @@
+// kv8_cache.cu -- writing the 8-bit paged KV cache: appending rotated keys and
+// values, and compaction along an accepted tree path.
+//
+// Append. One thread block owns one cache block of one head (or of a few
+// heads) and either its keys or its values, because the block's scale is a
+// maximum over everything the call writes into it: each thread keeps 16
+// elements of up to four rows in registers, the largest magnitude goes over
+// warps and shared memory, and the codes are stored from the same registers,
+// so every input is read once. A cache block that already holds tokens is only
+// rewritten when its scale grows.
+// Which cache blocks a sequence touches is known on the device alone: sequence
+// b gets the candidates cu[b] / block + 2 b .. cu[b + 1] / block + 2 b + 1, at
+// least as many as it can touch for any cache_len, and a thread block finds its
+// sequence with one comparison per sequence, in parallel.
+// Rotation. position * inv_freq in turns is an integer product modulo 2^64
+// (inv_freq / 2 pi as a 64-bit fraction), so the reduced angle loses nothing at
+// far positions and takes no 64-bit floating point.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv8.h"
+#include "internal.h"
+
+namespace specv {
+
+namespace {
+
+constexpr int kAppThreads = 256;
+
+// ------------------------------------------------------------ elements --
+
+template <typename T>
+struct Act;
+template <>
+struct Act<float> {
+  static __device__ __forceinline__ float get(const float* p) { return *p; }
+  static __device__ __forceinline__ void load8(const float* p, float* x) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
+  static __device__ __forceinline__ void store8(float* p, const float* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+  }
+};
+template <>
+struct Act<__nv_bfloat16> {
+  static __device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
+  }
+  static __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+  static __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
+    uint4 u;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = u;
+  }
+};
+template <>
+struct Act<__half> {
+  static __device__ __forceinline__ float get(const __half* p) { return __half2float(*p); }
+  static __device__ __forceinline__ void load8(const __half* p, float* x) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const __half2* h = reinterpret_cast<const __half2*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(h[i]);
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
+  static __device__ __forceinline__ void store8(__half* p, const float* x) {
+    uint4 u;
+    __half2* h = reinterpret_cast<__half2*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = u;
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void load_chunk(const T* p, bool vec, float* x) {
+  if (vec) {
+    Act<T>::load8(p, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = Act<T>::get(p + i);
+  }
+}
+
+// -------------------------------------------------------------- rotation --
+
+// A thread's 16 elements are two chunks of 8. Within the rotated dimensions
+// they are the two halves of eight split pairs (chunk at 8 c and at
+// rot / 2 + 8 c) or eight interleaved pairs (16 c .. 16 c + 15); behind them,
+// two neighbouring chunks.
+__device__ __forceinline__ void chunk_dims(const Kv8Rope& r, int c, int* d0, int* d1) {
+  const bool split = !r.interleaved && 16 * c < r.rot;
+  *d0 = split ? 8 * c : 16 * c;
+  *d1 = split ? r.rot / 2 + 8 * c : 16 * c + 8;
+}
+
+// cos and sin of pairs 8 c .. 8 c + 7 at a position.
+__device__ __forceinline__ void angles(const Kv8Rope& r, int c, int64_t pos, float* cs, float* sn) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t turns = static_cast<uint64_t>(pos) * r.freq[8 * c + i];
+    const int32_t t = static_cast<int32_t>(turns >> 32);  // signed: [-1/2, 1/2) of a turn
+    sincospif(static_cast<float>(t) * 4.656612873077393e-10f, &sn[i], &cs[i]);  // 2 t / 2^32 half turns
+  }
+}
+
+__device__ __forceinline__ void turn(const Kv8Rope& r, float* x, const float* cs, const float* sn) {
+  if (r.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float u = x[2 * i], w = x[2 * i + 1];
+      x[2 * i] = u * cs[i] - w * sn[i];
+      x[2 * i + 1] = w * cs[i] + u * sn[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float u = x[i], w = x[8 + i];
+      x[i] = u * cs[i] - w * sn[i];
+      x[8 + i] = w * cs[i] + u * sn[i];
+    }
+  }
+}
+
+// ------------------------------------------------------------------ append --
+
+template <typename T>
+__device__ __forceinline__ void append_status(const Kv8AppendArgs& a) {  // a warp per sequence
+  const int b = blockIdx.x * (kAppThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (b >= a.c.B) return;
+  const int lo = a.cu[b], hi = a.cu[b + 1], len = a.c.len[b];
+  bool bad = !kv8_seq_ok(a.c, a.T, lo, hi, len);
+  if (!bad && hi > lo) {
+    const int last = (len + (hi - lo) - 1) / a.c.block;
+    for (int j = len / a.c.block + lane; j <= last; j += 32) {
+      const int id = a.c.table[static_cast<int64_t>(b) * a.c.max_blocks + j];
+      bad |= id < 0 || id >= a.c.num_blocks;
+    }
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0) a.row_status[b] = SPEC_ROW_CACHE;
+  else if (lane == 0) a.row_status[b] = 0;
+}
+
+template <typename T>
+__device__ __forceinline__ void append_queries(const Kv8AppendArgs& a) {  // a thread: 16 elements of a query row
+  const int tpr = a.c.D / 16;
+  const int64_t item = static_cast<int64_t>(blockIdx.x - a.status_ctas - a.item_ctas) * kAppThreads + threadIdx.x;
+  const int64_t row = item / tpr;
+  const int c = static_cast<int>(item - row * tpr);
+  const int t = static_cast<int>(row / a.q_heads), h = static_cast<int>(row - static_cast<int64_t>(t) * a.q_heads);
+  if (t >= a.T) return;
+  int64_t pos = 0;
+  if (a.pos) {
+    pos = a.pos[t];
+  } else {  // the token's sequence: the last b with cu[b] <= t
+    int lo = 0, hi = a.c.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.cu[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    pos = static_cast<int64_t>(a.c.len[lo]) + (t - a.cu[lo]);
+  }
+  int d0, d1;
+  chunk_dims(a.rope, c, &d0, &d1);
+  float x[16];
+  const T* src = static_cast<const T*>(a.q) + t * a.qst + h * a.qsh;
+  load_chunk(src + d0, a.vec_q, x);
+  load_chunk(src + d1, a.vec_q, x + 8);
+  if (16 * c < a.rope.rot) {
+    float cs[8], sn[8];
+    angles(a.rope, c, pos, cs, sn);
+    turn(a.rope, x, cs, sn);
+  }
+  T* dst = static_cast<T*>(a.qo) + t * a.ost + h * a.osh;
+  if (a.vec_q) {
+    Act<T>::store8(dst + d0, x);
+    Act<T>::store8(dst + d1, x + 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) Act<T>::put(dst + d0 + i, x[i]), Act<T>::put(dst + d1 + i, x[8 + i]);
+  }
+}
+
+// PASS: rows a thread holds (block * head_dim / 16 <= PASS * kAppThreads).
+template <typename T, int PASS>
+__global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a) {
+  __shared__ int s_seq[4];  // sequence, candidate block of it, first token, tokens
+  __shared__ float s_amax[2][kAppThreads / 32];
+  const int tid = threadIdx.x;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (blockIdx.x < static_cast<unsigned>(a.status_ctas)) return append_status<T>(a);
+  int item = blockIdx.x - a.status_ctas;
+  if (item >= a.item_ctas) return append_queries<T>(a);
+
+  const int part = item % (2 * a.head_groups);
+  item /= 2 * a.head_groups;
+  const bool keys = part < a.head_groups;
+  const int h0 = (keys ? part : part - a.head_groups) * a.heads_per_cta;
+  if (tid == 0) s_seq[0] = -1;
+  __syncthreads();
+  const int bs = a.c.block;
+  for (int b = tid; b < a.c.B; b += kAppThreads) {
+    const int lo = a.cu[b], hi = a.cu[b + 1];
+    if (lo >= 0 && hi >= lo && hi <= a.T && lo / bs + 2 * b <= item && item < hi / bs + 2 * b + 2) {
+      s_seq[0] = b;
+      s_seq[1] = item - (lo / bs + 2 * b);
+      s_seq[2] = lo;
+      s_seq[3] = hi - lo;
+    }
+  }
+  __syncthreads();
+  const int b = s_seq[0];
+  if (b < 0) return;
+  const int first = s_seq[2], n = s_seq[3], len = a.c.len[b];
+  if (!kv8_seq_ok(a.c, a.T, first, first + n, len)) return;
+  const int64_t j = static_cast<int64_t>(len / bs) + s_seq[1];  // the sequence's block
+  const int64_t start = j * bs;
+  if (n == 0 || start >= static_cast<int64_t>(len) + n) return;
+  const int id = a.c.table[static_cast<int64_t>(b) * a.c.max_blocks + j];
+  if (id < 0 || id >= a.c.num_blocks) return;
+  const int s_lo = max(0, static_cast<int>(len - start));  // slots written: [s_lo, s_hi)
+  const int s_hi = static_cast<int>(min(static_cast<int64_t>(bs), static_cast<int64_t>(len) + n - start));
+
+  const int tpr = a.c.D / 16, c = tid % tpr, row0 = tid / tpr, rows = kAppThreads / tpr;
+  int d0 = 16 * c, d1 = 16 * c + 8;
+  if (keys) chunk_dims(a.rope, c, &d0, &d1);
+  const bool rotated = keys && 16 * c < a.rope.rot;
+  const T* src = static_cast<const T*>(keys ? a.k : a.v);
+  const int64_t st = keys ? a.kst : a.vst, sh = keys ? a.ksh : a.vsh;
+  const bool vec = keys ? a.vec_k : a.vec_v;
+  uint8_t* pool = (keys ? a.c.k : a.c.v) + id * a.c.sb;
+  uint8_t* scales = (keys ? a.c.ks : a.c.vs) + static_cast<int64_t>(id) * a.c.H;
+  const int h1 = min(a.c.H, h0 + a.heads_per_cta);
+  for (int h = h0; h < h1; ++h) {
+    float x[PASS][16];
+    float amax = 0.f;
+#pragma unroll
+    for (int p = 0; p < PASS; ++p) {
+      const int s = row0 + p * rows;
+      if (s < s_lo || s >= s_hi) continue;
+      const int64_t t = first + (start + s - len);
+      load_chunk(src + t * st + h * sh + d0, vec, x[p]);
+      load_chunk(src + t * st + h * sh + d1, vec, x[p] + 8);
+    }
+#pragma unroll
+    for (int p = 0; p < PASS; ++p) {
+      const int s = row0 + p * rows;
+      if (s < s_lo || s >= s_hi) continue;
+      if (rotated) {
+        const int64_t t = first + (start + s - len);
+        float cs[8], sn[8];
+        angles(a.rope, c, a.pos ? a.pos[t] : start + s, cs, sn);
+        turn(a.rope, x[p], cs, sn);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float m = fabsf(x[p][i]);
+        if (m < __int_as_float(0x7f800000)) amax = fmaxf(amax, m);
+      }
+    }
+    uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));  // magnitudes order as their bits
+    if ((tid & 31) == 0) s_amax[h & 1][tid >> 5] = __uint_as_float(m);
+    const uint8_t old_byte = scales[h];
+    __syncthreads();
+    amax = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAppThreads / 32; ++w) amax = fmaxf(amax, s_amax[h & 1][w]);
+    const int old = kv8_exp(old_byte);
+    const int need = kv8_need(amax);
+    const int e = s_lo > 0 ? max(old, need) : need;
+    uint8_t* head = pool + h * a.c.sh;
+    const float down = pow2i(-e);
+#pragma unroll
+    for (int p = 0; p < PASS; ++p) {
+      const int s = row0 + p * rows;
+      if (s >= bs) continue;
+      uint8_t* dst = head + s * a.c.ss;
+      if (s >= s_lo && s < s_hi) {
+        *reinterpret_cast<uint2*>(dst + d0) = make_uint2(kv8_codes4(x[p], down), kv8_codes4(x[p] + 4, down));
+        *reinterpret_cast<uint2*>(dst + d1) = make_uint2(kv8_codes4(x[p] + 8, down), kv8_codes4(x[p] + 12, down));
+      } else if (s_lo > 0 && e > old) {  // codes of the block's other entries, rounded to the grown scale
+        const float up = pow2i(old - e);
+        uint4 w = *reinterpret_cast<const uint4*>(dst + 16 * c);
+        uint32_t* q = &w.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float y[4];
+          kv8_values4(q[i], y);
+          q[i] = kv8_codes4(y, up);
+        }
+        *reinterpret_cast<uint4*>(dst + 16 * c) = w;
+      }
+    }
+    // every thread has read the old scale before the barrier above
+    if (tid == 0) scales[h] = static_cast<uint8_t>(e + 127);
+  }
+}
+
+template <typename T>
+cudaError_t launch_append(const Kv8AppendArgs& a, cudaStream_t st) {
+  const int tpr = a.c.D / 16;
+  const int64_t q_items = a.q ? static_cast<int64_t>(a.T) * a.q_heads * tpr : 0;
+  const int64_t ctas = a.status_ctas + static_cast<int64_t>(a.item_ctas) + (q_items + kAppThreads - 1) / kAppThreads;
+  const dim3 grid(static_cast<unsigned>(ctas)), block(kAppThreads);
+  const int pass = (a.c.block * tpr + kAppThreads - 1) / kAppThreads;
+  if (pass == 1) return launch_pdl(kv8_append_kernel<T, 1>, grid, block, st, a);
+  if (pass == 2) return launch_pdl(kv8_append_kernel<T, 2>, grid, block, st, a);
+  return launch_pdl(kv8_append_kernel<T, 4>, grid, block, st, a);
+}
+
+// ----------------------------------------------------------------- compact --
+//
+// One warp owns one head of one plane of one sequence, keys or values, and its
+// whole path: the entries are staged as codes in shared memory first, because
+// a destination block whose scale grows is rewritten and may hold sources.
+
+constexpr int kCompWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kCompWarps * 32) kv8_compact_kernel(const __grid_constant__ Kv8CompactArgs a) {
+  constexpr int kTpr = D / 16, kRows = 32 / kTpr;  // lanes per entry, entries per round
+  __shared__ __align__(16) uint8_t s_codes[kCompWarps][kKv8MaxPath * D];
+  __shared__ int s_path[kKv8MaxPath];
+  __shared__ int s_id[kKv8MaxPath];      // source block of each entry
+  __shared__ int s_dst[kKv8MaxPath];     // destination block of each entry
+  __shared__ int s_state;
+  const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int L = a.acc[b], base = a.c.len[b];
+  const int bs = a.c.block;
+  const int64_t cap = static_cast<int64_t>(a.c.max_blocks) * bs;
+  const int32_t* table = a.c.table + static_cast<int64_t>(b) * a.c.max_blocks;
+  if (warp == 0) {  // 1: move, 2: nothing to move, 0: skipped, else the negated status
+    int state = 1;
+    if (L < 0) {
+      state = 0;
+    } else if (base < 0) {
+      state = -SPEC_ROW_CACHE;
+    } else if (!a.path) {
+      state = static_cast<int64_t>(base) + L >= cap ? -SPEC_ROW_TREE : 2;
+    } else if (L >= a.Dp) {
+      state = -SPEC_ROW_TREE;
+    } else {
+      bool tree = false, cache = false;
+      for (int t = lane; t <= L; t += 32) {
+        const int p = a.path[static_cast<int64_t>(b) * a.Dp + t];
+        const int prev = t ? a.path[static_cast<int64_t>(b) * a.Dp + t - 1] : -1;
+        const bool bad = (t == 0 && p != 0) || p <= prev || static_cast<int64_t>(base) + p >= cap;
+        tree |= bad;
+        if (bad) continue;
+        s_path[t] = p;
+        const int src = table[(base + p) / bs], dst = table[(base + t) / bs];  // t <= p: both in the table
+        cache |= src < 0 || src >= a.c.num_blocks || dst < 0 || dst >= a.c.num_blocks;
+        s_id[t] = src;
+        s_dst[t] = dst;
+      }
+      if (__any_sync(0xffffffffu, tree)) state = -SPEC_ROW_TREE;
+      else if (__any_sync(0xffffffffu, cache)) state = -SPEC_ROW_CACHE;
+      __syncwarp();
+      if (state == 1 && s_path[L] == L) state = 2;
+    }
+    if (lane == 0) s_state = state;
+  }
+  __syncthreads();
+  const int state = s_state;
+  if (blockIdx.x == 0 && tid == 0) {
+    a.new_len[b] = state >= 1 ? base + L + 1 : -1;
+    a.row_status[b] = state < 0 ? -state : 0;
+  }
+  if (state != 1) return;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kCompWarps + warp;  // plane, keys or values, head
+  if (item >= static_cast<int64_t>(a.planes) * 2 * a.c.H) return;
+  const int h = static_cast<int>(item % a.c.H);
+  const int64_t pk = item / a.c.H, plane = pk >> 1;
+  uint8_t* codes = ((pk & 1) ? a.c.v : a.c.k) + plane * a.sp + h * a.c.sh;
+  uint8_t* scales = ((pk & 1) ? a.c.vs : a.c.ks) + plane * a.ssp + h;
+  uint8_t* stage = s_codes[warp];
+  const int c = lane % kTpr, r = lane / kTpr;
+  for (int t = r; t <= L; t += kRows) {
+    const int p = base + s_path[t];
+    *reinterpret_cast<uint4*>(stage + t * D + 16 * c) =
+        *reinterpret_cast<const uint4*>(codes + s_id[t] * a.c.sb + (p % bs) * a.c.ss + 16 * c);
+  }
+  // the scale of a source entry's block, before any is written: lanes hold entries lane and lane + 32
+  int src_e[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = lane + 32 * i;
+    src_e[i] = t <= L ? kv8_exp(scales[static_cast<int64_t>(s_id[t]) * a.c.H]) : 0;
+  }
+  __syncwarp();
+  for (int t0 = 0; t0 <= L;) {  // entries t0 .. t1 - 1 share a destination block
+    const int t1 = min(L + 1, t0 + bs - (base + t0) % bs);
+    const int64_t dst = s_dst[t0];
+    uint8_t* head = codes + dst * a.c.sb;
+    const int old = kv8_exp(scales[dst * a.c.H]);
+    int e = old;
+    for (int t = t0 + r; __any_sync(0xffffffffu, t < t1); t += kRows) {
+      const int e0 = __shfl_sync(0xffffffffu, src_e[0], t & 31), e1 = __shfl_sync(0xffffffffu, src_e[1], t & 31);
+      const int es = t < 32 ? e0 : e1;
+      if (t >= t1) continue;
+      const uint4 w = *reinterpret_cast<const uint4*>(stage + t * D + 16 * c);
+      const uint32_t* q = &w.x;
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float y[4];
+        kv8_values4(q[i], y);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (fabsf(y[k]) <= kKv8Max) amax = fmaxf(amax, fabsf(y[k]));  // NaN codes do not count
+      }
+      e = max(e, kv8_need(amax * pow2i(es)));
+    }
+    e = __reduce_max_sync(0xffffffffu, e);
+    if (e > old) {
+      const float up = pow2i(old - e);
+      for (int s = r; s < bs; s += kRows) {
+        uint4 w = *reinterpret_cast<const uint4*>(head + s * a.c.ss + 16 * c);
+        uint32_t* q = &w.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float y[4];
+          kv8_values4(q[i], y);
+          q[i] = kv8_codes4(y, up);
+        }
+        *reinterpret_cast<uint4*>(head + s * a.c.ss + 16 * c) = w;
+      }
+      __syncwarp();
+      if (lane == 0) scales[dst * a.c.H] = static_cast<uint8_t>(e + 127);
+    }
+    for (int t = t0 + r; __any_sync(0xffffffffu, t < t1); t += kRows) {
+      const int e0 = __shfl_sync(0xffffffffu, src_e[0], t & 31), e1 = __shfl_sync(0xffffffffu, src_e[1], t & 31);
+      const int es = t < 32 ? e0 : e1;
+      if (t >= t1 || (s_path[t] == t && e == old)) continue;
+      uint4 w = *reinterpret_cast<const uint4*>(stage + t * D + 16 * c);
+      uint32_t* q = &w.x;
+      if (es != e) {
+        const float by = pow2i(es - e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float y[4];
+          kv8_values4(q[i], y);
+          q[i] = kv8_codes4(y, by);
+        }
+      }
+      *reinterpret_cast<uint4*>(head + ((base + t) % bs) * a.c.ss + 16 * c) = w;
+    }
+    __syncwarp();
+    t0 = t1;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int dtype, cudaStream_t st) {
+  if (dtype == SPEC_F32) return launch_append<float>(a, st);
+  if (dtype == SPEC_BF16) return launch_append<__nv_bfloat16>(a, st);
+  return launch_append<__half>(a, st);
+}
+
+cudaError_t launch_kv8_compact(const Kv8CompactArgs& a, cudaStream_t st) {
+  const int64_t items = static_cast<int64_t>(a.planes) * 2 * a.c.H;
+  const dim3 grid(static_cast<unsigned>((items + kCompWarps - 1) / kCompWarps), static_cast<unsigned>(a.c.B));
+  const dim3 block(kCompWarps * 32);
+  return a.c.D == 128 ? launch_pdl(kv8_compact_kernel<128>, grid, block, st, a)
+                      : launch_pdl(kv8_compact_kernel<64>, grid, block, st, a);
+}
+
+}  // namespace specv
