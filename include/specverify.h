@@ -497,7 +497,8 @@ int spec_kv8_append(const spec_kv8_cache* cache, const void* keys, int64_t k_str
  * Outputs: out; row_status [B] int32: SPEC_ROW_CACHE where the sequence's lengths
  * are invalid (cu_tokens not rising or outside [0, T], more than max_tokens,
  * cache_len negative or beyond the table) or one of its blocks' ids is outside
- * the pool: its rows are NaN where its cu_tokens are valid. Tokens of no
+ * the pool: rows that would read it, and all rows of a sequence with
+ *       invalid lengths and valid cu_tokens, are NaN. Tokens of no
  * sequence are not written.
  * workspace: spec_kv8_workspace_bytes(...) bytes, 256-byte aligned, needing no
  * initialisation. Errors: SPEC_ERR_ARG, SPEC_ERR_WORKSPACE as usual;

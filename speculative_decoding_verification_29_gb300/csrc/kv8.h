@@ -2,6 +2,7 @@
 // kernels and the C entry points.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -69,8 +70,19 @@ struct Kv8AttnArgs {
   const uint8_t* tree;  // [B][max_tokens][max_tokens] or NULL
   float scale;          // sm_scale * log2(e)
   int32_t* row_status;
+  int row_tiles;        // row tiles a sequence has at most
+  int parts;            // thread blocks the cache is split over
+  int order;            // tensor maps' dimensions 1..3: 2-bit fields naming slot (0), head (1), block (2)
+  int32_t* gave_up;     // workspace [parts]: a wait of the block ran out
+  float2* part_ml;      // workspace [2 parts][rows]: exponent reference, sum of weights
+  float* part_o;        // workspace [2 parts][rows][head_dim]: weighted sums
 };
-cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, int dtype, cudaStream_t st);
+// Variant for the most rows (step tokens x group) a sequence can have, and
+// thread blocks (parts) of its launch.
+int kv8_attention_rows(int64_t max_rows);
+int kv8_attention_parts(int rows);
+cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, int dtype, int rows, const CUtensorMap& k, const CUtensorMap& v,
+                                 cudaStream_t st);
 
 // ---------------------------------------------------------------- device --
 
@@ -82,11 +94,11 @@ __device__ __forceinline__ bool kv8_seq_ok(const Kv8Pool& c, int T, int lo, int 
 
 // Exponent of the least scale in range that holds amax: least e with
 // amax <= 448 * 2^e = 1.75 * 2^(8 + e), read off the bits.
-__device__ __forceinline__ int kv8_need(float amax) {
+__device__ __forceinline__ int kv8_need(float amax, int lo = kKv8ExpLo, int hi = kKv8ExpHi) {
   const uint32_t u = __float_as_uint(amax);
   const int x = static_cast<int>(u >> 23) - 127;
   const int e = (u & 0x7fffffu) <= 0x600000u ? x - 8 : x - 7;
-  return min(max(e, kKv8ExpLo), kKv8ExpHi);  // zero and subnormals: x = -127
+  return min(max(e, lo), hi);  // zero and subnormals: x = -127
 }
 
 __device__ __forceinline__ int kv8_exp(uint8_t byte) {

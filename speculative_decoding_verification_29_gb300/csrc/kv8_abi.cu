@@ -3,6 +3,9 @@
 // include/specverify.h.
 #include <math.h>
 
+#include <algorithm>
+
+
 #include "kv8.h"
 
 using namespace specv;
@@ -67,6 +70,63 @@ uint64_t turn_fraction(double f) {
   lo += hi - ldexp(a, -32);
   const double rest = ldexp(lo, 64);  // below 2^32 in magnitude, may be negative
   return (static_cast<uint64_t>(a) << 32) + static_cast<uint64_t>(static_cast<int64_t>(llrint(rest)));
+}
+
+// The attention's workspace: a flag per part, then each part's two shares of
+// cut items (exponent references and sums, weighted sums).
+struct AttnLayout {
+  size_t ml, o, total;
+};
+AttnLayout attn_layout(int rows, int D) {
+  const size_t parts = kv8_attention_parts(rows);
+  auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
+  AttnLayout l{};
+  l.ml = up(parts * sizeof(int32_t));
+  l.o = l.ml + up(2 * parts * rows * sizeof(float2));
+  l.total = l.o + up(2 * parts * rows * D * sizeof(float));
+  return l;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return static_cast<EncodeTiled>(nullptr);
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// The pool as a tensor of bytes, one block of one head a copy. Its dimensions
+// behind the head's are ordered by their strides; `order` names them.
+bool pool_map(const Kv8Pool& c, void* codes, CUtensorMap* map, int* order) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return false;
+  struct Dim {
+    cuuint64_t size, stride;
+    cuuint32_t box;
+    int name;
+  } d[3] = {{static_cast<cuuint64_t>(c.block), static_cast<cuuint64_t>(c.ss), static_cast<cuuint32_t>(c.block), 0},
+            {static_cast<cuuint64_t>(c.H), static_cast<cuuint64_t>(c.sh), 1, 1},
+            {static_cast<cuuint64_t>(c.num_blocks), static_cast<cuuint64_t>(c.sb), 1, 2}};
+  cuuint64_t far = 16;
+  for (const Dim& x : d)
+    if (x.size > 1) far = std::max(far, x.size * x.stride);
+  for (Dim& x : d)
+    if (x.size == 1) x.stride = far;  // never stepped
+  std::stable_sort(d, d + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+  const cuuint64_t sizes[4] = {static_cast<cuuint64_t>(c.D), d[0].size, d[1].size, d[2].size};
+  const cuuint64_t strides[3] = {d[0].stride, d[1].stride, d[2].stride};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(c.D), d[0].box, d[1].box, d[2].box}, step[4] = {1, 1, 1, 1};
+  *order = d[0].name | d[1].name << 2 | d[2].name << 4;
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, codes, sizes, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                c.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA; }
@@ -134,7 +194,7 @@ size_t spec_kv8_workspace_bytes(const spec_kv8_cache* cache, int q_heads, int ma
   Kv8Pool c;
   if (take_pool(cache, &c) != SPEC_OK || q_heads < 1 || q_heads % c.H != 0 || max_tokens < 1) return 0;
   if (dtype != SPEC_BF16 && dtype != SPEC_F16) return 0;
-  return 256;
+  return attn_layout(kv8_attention_rows(static_cast<int64_t>(max_tokens) * (q_heads / c.H)), c.D).total;
 }
 
 int spec_kv8_attention(const spec_kv8_cache* cache, const void* queries, int64_t q_stride_token,
@@ -169,7 +229,18 @@ int spec_kv8_attention(const spec_kv8_cache* cache, const void* queries, int64_t
   a.tree = tree_mask;
   a.scale = static_cast<float>(sm_scale * 1.4426950408889634);
   a.row_status = row_status;
-  return cuda_status(launch_kv8_attention(a, dtype, static_cast<cudaStream_t>(stream)));
+  const int64_t most = static_cast<int64_t>(std::min(max_tokens, std::max(T, 1))) * a.group;  // no sequence has more than T
+  const int rows = kv8_attention_rows(static_cast<int64_t>(max_tokens) * a.group);
+  a.row_tiles = static_cast<int>((most + rows - 1) / rows);
+  a.parts = kv8_attention_parts(rows);
+  const AttnLayout l = attn_layout(rows, a.c.D);
+  char* ws = static_cast<char*>(workspace);
+  a.gave_up = reinterpret_cast<int32_t*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + l.ml);
+  a.part_o = reinterpret_cast<float*>(ws + l.o);
+  CUtensorMap kmap, vmap;
+  if (!pool_map(a.c, a.c.k, &kmap, &a.order) || !pool_map(a.c, a.c.v, &vmap, &a.order)) return SPEC_ERR_CUDA;
+  return cuda_status(launch_kv8_attention(a, dtype, rows, kmap, vmap, static_cast<cudaStream_t>(stream)));
 }
 
 int spec_kv8_compact(const spec_kv8_cache* cache, int n_planes, int64_t stride_plane, int64_t scale_stride_plane,

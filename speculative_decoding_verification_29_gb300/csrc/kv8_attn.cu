@@ -1,20 +1,51 @@
-// kv8_attn.cu -- attention over the 8-bit paged KV cache.
+// kv8_attn.cu -- attention over the 8-bit paged KV cache on the tensor cores.
 //
-// One thread block per packed token and KV head, all query heads of the group:
-// tiles of 128 cache slots, one slot per thread for the scores, one dimension
-// per thread for the weighted sum, a running maximum and sum per row.
+// Mathematics. With codes c, block exponents ek and ev, and y_t = sm_scale
+// log2(e) 2^ek(t) (q . ck_t) + ev(t), a row's result is
+//     sum_t 2^y_t cv_t / sum_t 2^(y_t - ev(t)),
+// so neither the keys' nor the values' codes are ever converted: the block
+// scales enter as a factor of the score and a summand of the exponent. Over a
+// tile of 128 slots a row takes weights w_t = 2^(y_t - E + 8) with E the tile's
+// largest y rounded up to a whole number; tiles add up with factors 2^(E - ref),
+// exact powers of two, so the accumulators are rescaled only when a tile passes
+// the row's reference by 2^60.
+// Operands. The products are e4m3 x e4m3 -> fp32. A bf16 query element is the sum
+// of two e4m3 terms (4 bits and a sign each), an fp16 one of three, exactly down
+// to 2^-17 of the item's largest; a weight is split likewise, its relative error
+// about 2^-9 rms for bf16 results and 2^-12 for fp16. Because E is the tile's own
+// largest, the codes' floor costs no more than 2^-17 of a weight in the same tile.
+//
+// Orientation. Slots are the 128 rows of both products' first operand: scores
+// are K (128 slots x D) times Q^T (D x N rows), results are V^T (D x 128 slots)
+// times the weights (128 slots x N). A thread owns one slot (so block scales and
+// masks are scalars of a thread) and one dimension of the result, N is the number
+// of rows rounded to 16, and few rows cost little. K, Q enter with their inner
+// dimension contiguous, V and the weights with their outer one, as they lie.
+//
+// Schedule. An item is (sequence, row tile, KV head); its tiles of 128 slots are
+// numbered through all items, and every thread block takes an equal run of that
+// list, found on the device from the lengths. An item cut by a run's end leaves
+// partial sums; a second kernel joins them, in order. One warp copies K and V
+// blocks into a ring of tile slots by bulk tensor copies, one issues the
+// products, four or eight compute the softmax.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "internal.h"
 #include "kv8.h"
+#include "tc.cuh"
 
 namespace specv {
 
 namespace {
 
+using namespace tc;
+
 constexpr int kTile = 128;
-constexpr int kMaxGroup = 64;
+constexpr int kMetaRing = 8;
+constexpr int kMaxPages = kTile / 16;
+constexpr int kBadPage = 1 << 20;
+constexpr float kNegInf = -__builtin_huge_valf();
 
 template <typename T>
 __device__ __forceinline__ float to_f(T v);
@@ -29,102 +60,895 @@ __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat
 template <>
 __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kTile) kv8_attention_rows(const __grid_constant__ Kv8AttnArgs a) {
-  __shared__ float s_p[kTile], s_v[kTile], s_red[2][4];
-  __shared__ int s_id[kTile];
-  const int tid = threadIdx.x, t = blockIdx.x, h = blockIdx.y;
-  griddep_launch_dependents();
-  griddep_wait();
-  const bool report = t >= a.T;  // the last B columns of blocks write row_status
-  int b = report ? t - a.T : 0;
-  for (int hi = report ? b : a.c.B; hi - b > 1;) {
-    const int mid = (b + hi) >> 1;
-    if (a.cu[mid] <= t) b = mid;
-    else hi = mid;
-  }
-  const int lo = a.cu[b], hi = a.cu[b + 1], len = a.c.len[b], bs = a.c.block;
-  bool bad = !kv8_seq_ok(a.c, a.T, lo, hi, len) || hi - lo > a.max_tokens;
-  const int i = t - lo, end = len + (a.tree ? hi - lo : i + 1);
-  const int32_t* table = a.c.table + static_cast<int64_t>(b) * a.c.max_blocks;
-  if (!bad)
-    for (int j = tid; j < (len + hi - lo + bs - 1) / bs; j += kTile) bad |= table[j] < 0 || table[j] >= a.c.num_blocks;
-  bad = __syncthreads_or(bad);
-  if (report) {
-    if (tid == 0 && h == 0) a.row_status[b] = bad ? SPEC_ROW_CACHE : 0;
-    return;
-  }
-  if (t < lo || t >= hi) return;
-  for (int g = 0; g < a.group; ++g) {
-    const int head = h * a.group + g;
-    const T* q = static_cast<const T*>(a.q) + t * a.qst + head * a.qsh;
-    T* out = static_cast<T*>(a.out) + t * a.ost + head * a.osh;
-    if (bad) {
-      if (tid < D) out[tid] = from_f<T>(__int_as_float(0x7fffffff));
-      continue;
-    }
-    float top = -__int_as_float(0x7f800000), sum = 0.f, acc = 0.f;
-    for (int s0 = 0; s0 < end; s0 += kTile) {
-      const int s = s0 + tid;
-      float y = -__int_as_float(0x7f800000), vs = 0.f;
-      int id = 0;
-      if (s < end && (s < len || !a.tree ||
-                      a.tree[(static_cast<int64_t>(b) * a.max_tokens + i) * a.max_tokens + (s - len)])) {
-        id = table[s / bs];
-        const uint8_t* k = a.c.k + id * a.c.sb + h * a.c.sh + (s % bs) * a.c.ss;
-        float dot = 0.f;
-        for (int d = 0; d < D; d += 4) {
-          float x[4];
-          kv8_values4(*reinterpret_cast<const uint32_t*>(k + d), x);
+// -------------------------------------------------------------- schedule --
+
+// One row tile of a sequence, all KV heads alike.
+struct RowTile {
+  int b, rt;
+  int first;  // first packed token of the sequence
+  int n;      // its step tokens
+  int ctx;    // tokens in the cache before the step
+  int rows;   // rows of this tile
+  int end;    // slots that some row of it may see
+  int tiles;  // ceil(end / 128); 0: no such row tile
+};
+
+template <int N>
+__device__ __forceinline__ RowTile row_tile(const Kv8AttnArgs& a, int b, int rt) {
+  RowTile r{};
+  r.b = b;
+  r.rt = rt;
+  const int lo = a.cu[b], hi = a.cu[b + 1], len = a.c.len[b];
+  if (!kv8_seq_ok(a.c, a.T, lo, hi, len) || hi - lo > a.max_tokens) return r;
+  const int64_t rows = static_cast<int64_t>(hi - lo) * a.group, r0 = static_cast<int64_t>(rt) * N;
+  if (r0 >= rows) return r;
+  r.first = lo;
+  r.n = hi - lo;
+  r.ctx = len;
+  r.rows = static_cast<int>(min(rows - r0, static_cast<int64_t>(N)));
+  r.end = len + (a.tree ? r.n : static_cast<int>((r0 + r.rows - 1) / a.group) + 1);
+  r.tiles = (r.end + kTile - 1) / kTile;
+  return r;
+}
+
+// Where a run of tiles begins.
+struct Start {
+  int b, rt, h, t;
+};
+
+// All threads of the block: the run [lo, hi) of part `part` and its first tile.
+// With `last`, the place of tile hi - 1 instead. s_tmp: 34 words of shared memory.
+template <int N>
+__device__ __forceinline__ bool find_run(const Kv8AttnArgs& a, int part, bool last, int64_t* lo, int64_t* hi, Start* s,
+                                         int64_t* all_tiles, int* s_tmp) {
+  const int nthr = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = nthr >> 5;
+  const int64_t cand = static_cast<int64_t>(a.c.B) * a.row_tiles;
+  int64_t total = 0;
+  int v0 = 0, incl0 = 0;  // this thread's candidate of the first round
+  for (int64_t base = 0; base < cand; base += nthr) {
+    const int64_t i = base + tid;
+    int v = 0;
+    if (i < cand) v = row_tile<N>(a, static_cast<int>(i / a.row_tiles), static_cast<int>(i % a.row_tiles)).tiles;
+    int x = v;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) dot = fmaf(to_f(q[d + u]), x[u], dot);
-        }
-        y = dot * a.scale * pow2i(kv8_exp(a.c.ks[static_cast<int64_t>(id) * a.c.H + h]));
-        vs = pow2i(kv8_exp(a.c.vs[static_cast<int64_t>(id) * a.c.H + h]));
-      }
-      float m = y;
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      __syncthreads();
-      if ((tid & 31) == 0) s_red[0][tid >> 5] = m;
-      __syncthreads();
-      m = fmaxf(fmaxf(s_red[0][0], s_red[0][1]), fmaxf(s_red[0][2], s_red[0][3]));
-      const float now = fmaxf(top, m);
-      const float ref = now > -__int_as_float(0x7f800000) ? now : 0.f;
-      const float p = exp2f(y - ref), old = exp2f(top - ref);
-      float l = p;
-      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if ((tid & 31) == 0) s_red[1][tid >> 5] = l;
-      s_p[tid] = p;
-      s_v[tid] = vs;
-      s_id[tid] = id;
-      __syncthreads();
-      sum = sum * old + (s_red[1][0] + s_red[1][1] + s_red[1][2] + s_red[1][3]);
-      acc *= old;
-      top = now;
-      if (tid < D)
-        for (int u = 0; u < min(kTile, end - s0); ++u) {
-          if (s_v[u] == 0.f) continue;  // not seen
-          const uint8_t c = a.c.v[s_id[u] * a.c.sb + h * a.c.sh + ((s0 + u) % bs) * a.c.ss + tid];
-          float x[4];
-          kv8_values4(c, x);
-          acc = fmaf(s_p[u] * s_v[u], x[0], acc);
-        }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
-    if (tid < D) out[tid] = from_f<T>(sum > 0.f || sum != sum ? acc / sum : 0.f);
+    if (lane == 31) s_tmp[warp] = x;
+    __syncthreads();
+    int before = 0, sum = 0;
+    for (int w = 0; w < nw; ++w) {
+      if (w < warp) before += s_tmp[w];
+      sum += s_tmp[w];
+    }
+    __syncthreads();
+    if (base == 0) v0 = v, incl0 = x + before;
+    total += sum;
+  }
+  const int64_t all = total * a.c.H;
+  const int64_t parts = min(static_cast<int64_t>(a.parts), all);
+  *all_tiles = all;
+  *lo = part < parts ? all * part / parts : all;
+  *hi = part < parts ? all * (part + 1) / parts : all;
+  if (*lo >= *hi) return false;
+  const int64_t want = last ? *hi - 1 : *lo;
+  int64_t run = 0;
+  for (int64_t base = 0; base < cand; base += nthr) {
+    const int64_t i = base + tid;
+    int v = v0, incl = incl0, sum = 0;
+    if (base > 0 || cand > nthr) {
+      v = 0;
+      if (i < cand) v = row_tile<N>(a, static_cast<int>(i / a.row_tiles), static_cast<int>(i % a.row_tiles)).tiles;
+      int x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) s_tmp[warp] = x;
+      __syncthreads();
+      int before = 0;
+      for (int w = 0; w < nw; ++w) {
+        if (w < warp) before += s_tmp[w];
+        sum += s_tmp[w];
+      }
+      __syncthreads();
+      incl = x + before;
+    }
+    const int64_t from = (run + incl - v) * a.c.H, to = (run + incl) * a.c.H;
+    if (v > 0 && want >= from && want < to) {
+      const int off = static_cast<int>((want - from) / v);
+      s_tmp[0] = static_cast<int>(i / a.row_tiles);
+      s_tmp[1] = static_cast<int>(i % a.row_tiles);
+      s_tmp[2] = off;
+      s_tmp[3] = static_cast<int>((want - from) - static_cast<int64_t>(off) * v);
+    }
+    run += sum;
+    if (cand > nthr && run * a.c.H > want) break;  // the same for every thread
+  }
+  __syncthreads();
+  s->b = s_tmp[0];
+  s->rt = s_tmp[1];
+  s->h = s_tmp[2];
+  s->t = s_tmp[3];
+  __syncthreads();
+  return true;
+}
+
+// Walks the items of a run: (r, h) with tiles [t0, t1).
+template <int N>
+struct Walk {
+  RowTile r;
+  int h, t0, t1;
+  int64_t left;  // tiles of the run from t0 on
+
+  __device__ __forceinline__ Walk(const Kv8AttnArgs& a, const Start& s, int64_t count) {
+    r = row_tile<N>(a, s.b, s.rt);
+    h = s.h;
+    t0 = s.t;
+    left = count;
+    clip();
+  }
+  __device__ __forceinline__ void clip() { t1 = static_cast<int>(min(static_cast<int64_t>(r.tiles), t0 + left)); }
+  // The next item, if any is left.
+  __device__ __forceinline__ bool next(const Kv8AttnArgs& a) {
+    left -= t1 - t0;
+    if (left <= 0) return false;
+    t0 = 0;
+    if (++h == a.c.H) {
+      h = 0;
+      int b = r.b, rt = r.rt;
+      do {
+        if (++rt == a.row_tiles) {
+          rt = 0;
+          ++b;
+        }
+        if (b >= a.c.B) {  // cannot be: the run's tiles were counted
+          left = 0;
+          return false;
+        }
+        r = row_tile<N>(a, b, rt);
+        if (r.tiles == 0) rt = a.row_tiles - 1;  // no further row tile in this sequence
+      } while (r.tiles == 0);
+    }
+    clip();
+    return true;
+  }
+};
+
+// ---------------------------------------------------------- configuration --
+
+// D: head dimension. RW: rows of one softmax group of four warps, W: groups.
+template <int D_, int RW_, int W_, int TERMS_>
+struct Cfg {
+  static constexpr int D = D_, RW = RW_, W = W_, TERMS = TERMS_;
+  static constexpr int N = RW * W;
+  static constexpr int kCompute = W * 128, kThreads = kCompute + 64;
+  static constexpr int kCtas = N <= 32 ? 2 : 1;  // resident on an SM
+  static constexpr int kSlot = kTile * D;
+  static constexpr int kQ = TERMS * N * D < 1024 ? 1024 : TERMS * N * D;
+  static constexpr int kPanels = (TERMS * N + 127) / 128, kP = kPanels * kTile * 128;
+  static constexpr int kCols = 3 * N <= 64 ? 64 : (3 * N <= 128 ? 128 : (3 * N <= 256 ? 256 : 512));
+  static constexpr int kGrain = W > 2 ? 4 : 8;  // a group's rows are rounded to this, N to 16
+  static __device__ __forceinline__ int group_rows(int rows) {
+    constexpr int g = W == 1 ? 16 : kGrain;
+    return ((rows + W - 1) / W + g - 1) / g * g;
+  }
+  static constexpr uint32_t kLayout = D == 128 ? 2 : 4;
+
+  struct Small {
+    float smax[2][W][4][RW];
+    float2 ef[2][W * 4][RW];
+    float red[W * 4];
+    int nan[2][W][4];
+    int kexp[kMetaRing][kMaxPages], vexp[kMetaRing][kMaxPages];
+    alignas(8) uint64_t full[12], empty[12], s_full[2], p_ready, o_full, q_ready, drain;
+    uint32_t tmem;
+    int gave_up;
+    int tmp[36];
+  };
+  static constexpr int kBudget = kCtas == 2 ? 115712 : 231424;
+  static constexpr int kFixed = 1024 + kQ + kP + static_cast<int>(sizeof(Small));
+  static constexpr int kFit = (kBudget - kFixed) / kSlot;
+  static constexpr int kRing = kFit > 12 ? 12 : kFit;
+  static constexpr int kSmem = kFixed + kRing * kSlot;
+  static_assert(kRing >= 3, "ring of tile slots");
+  static_assert(kMetaRing >= (kRing + 1) / 2 + 1, "meta entries live as long as a tile's slots");
+};
+
+// Byte offset of element (row, byte) in a tile of rows of ROW bytes, swizzled as bulk tensor copies do.
+template <int ROW>
+__device__ __forceinline__ uint32_t swz(int row, int byte) {
+  const uint32_t o = static_cast<uint32_t>(row * ROW + byte);
+  return ROW == 128 ? o ^ ((o >> 3) & 0x70u) : o ^ ((o >> 3) & 0x30u);
+}
+
+// The e4m3 terms of eight query elements (already divided by the item's scale).
+template <int TERMS>
+__device__ __forceinline__ void split8(float* x, uint2* out) {
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t) {
+    out[t] = make_uint2(kv8_codes4(x, 1.f), kv8_codes4(x + 4, 1.f));
+    if (t + 1 < TERMS) {
+      float y[8];
+      kv8_values4(out[t].x, y);
+      kv8_values4(out[t].y, y + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] -= y[i];
+    }
   }
 }
 
-template <typename T>
-cudaError_t launch_rows(const Kv8AttnArgs& a, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(a.T + a.c.B), static_cast<unsigned>(a.c.H)), block(kTile);
-  return a.c.D == 128 ? launch_pdl(kv8_attention_rows<T, 128>, grid, block, st, a)
-                      : launch_pdl(kv8_attention_rows<T, 64>, grid, block, st, a);
+__device__ __forceinline__ float exp2_whole(float d) { return exp2f(d); }  // d whole, -inf or NaN: exact
+
+// Sums v[0 .. C - 1] over the warp's lanes; lane j (mod C) gets the sum of v[j].
+template <int C>
+__device__ __forceinline__ float lane_sums(float* v, int lane) {
+  if (C == 16) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], 16);
+  }
+#pragma unroll
+  for (int o = C / 2; o >= 1; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int k = 0; k < o; ++k) {
+      const float send = up ? v[k] : v[k + o], keep = up ? v[k + o] : v[k];
+      v[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  return v[0];
+}
+
+// Whether row r (token r / group of the step) sees step slot j.
+__device__ __forceinline__ bool sees(const Kv8AttnArgs& a, int b, int i, int j) {
+  return a.tree ? a.tree[(static_cast<int64_t>(b) * a.max_tokens + i) * a.max_tokens + j] != 0 : j <= i;
+}
+
+// A tile that holds NaN values and slots not every row sees: dimension d of one
+// row's weighted sum over the slots that the row does see.
+template <typename C>
+__device__ __noinline__ float masked_sum(const Kv8AttnArgs& a, const RowTile& r, int h, int slot0, int row, int token,
+                                         int d, const uint8_t* p_smem) {
+  float sum = 0.f;
+  const int bs = a.c.block;
+  for (int u = 0; u < kTile && slot0 + u < r.end; ++u) {
+    const int slot = slot0 + u;
+    if (slot >= r.ctx && !sees(a, r.b, token, slot - r.ctx)) continue;
+    const int id = a.c.table[static_cast<int64_t>(r.b) * a.c.max_blocks + slot / bs];
+    if (id < 0 || id >= a.c.num_blocks) return __int_as_float(0x7fffffff);
+    float w = 0.f, x[4];
+#pragma unroll
+    for (int t = 0; t < C::TERMS; ++t) {
+      const int col = t * C::N + row;
+      kv8_values4(p_smem[(col / 128) * (kTile * 128) + swz<128>(u, col % 128)], x);
+      w += x[0];
+    }
+    kv8_values4(a.c.v[id * a.c.sb + h * a.c.sh + (slot % bs) * a.c.ss + d], x);
+    sum = fmaf(w, x[0], sum);
+  }
+  return sum;
+}
+
+// ----------------------------------------------------------------- kernel --
+
+template <typename QT, typename C>
+__global__ void __launch_bounds__(C::kThreads, C::kCtas)
+    kv8_attention_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap) {
+  extern __shared__ uint8_t dyn[];
+  constexpr int D = C::D, N = C::N, RW = C::RW, NS = C::kRing;
+  constexpr int HC = 16, HN = RW / HC;         // columns read from tensor memory at a time
+  constexpr int RG = (RW + 31) / 32, RL = RW < 32 ? RW : 32;  // rows as lanes: groups, lanes used
+  constexpr int GR = C::kGrain;
+  uint8_t* base = dyn + ((1024u - (smem_addr(dyn) & 1023u)) & 1023u);
+  uint8_t* ring = base;
+  uint8_t* p_smem = ring + NS * C::kSlot;
+  uint8_t* q_smem = p_smem + C::kP;
+  typename C::Small& sm = *reinterpret_cast<typename C::Small*>(q_smem + C::kQ);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kLoadWarp = C::W * 4, kMmaWarp = C::W * 4 + 1;
+  volatile int* gave_up = &sm.gave_up;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      bar_init(smem_addr(&sm.full[i]), 1);
+      bar_init(smem_addr(&sm.empty[i]), 1);
+    }
+    bar_init(smem_addr(&sm.s_full[0]), 1);
+    bar_init(smem_addr(&sm.s_full[1]), 1);
+    bar_init(smem_addr(&sm.p_ready), C::W * 4);
+    bar_init(smem_addr(&sm.o_full), 1);
+    bar_init(smem_addr(&sm.q_ready), C::W * 4);
+    bar_init(smem_addr(&sm.drain), 1);
+    fence_bar_init();
+    sm.gave_up = 0;
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_addr(&sm.tmem), C::kCols);
+  griddep_wait();
+  int64_t lo, hi, all;
+  Start start;
+  fence_before();
+  const bool work = find_run<N>(a, blockIdx.x, false, &lo, &hi, &start, &all, sm.tmp);
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  if (work && warp == kLoadWarp) {
+    // ---- copies: the pages of each tile's keys, then of its values
+    Walk<N> it(a, start, hi - lo);
+    const int bs = a.c.block, ppt = kTile / bs;
+    uint32_t fill = 0, begun = 0;
+    int i = 0;
+    do {
+      const int pages = (it.r.end + bs - 1) / bs;
+      const int32_t* table = a.c.table + static_cast<int64_t>(it.r.b) * a.c.max_blocks;
+      int id = -1, ke = 0, ve = 0;
+      for (int t = it.t0, g = 0; t < it.t1; ++t, g += ppt, ++i) {
+        if ((g & 31) == 0) {  // the next 32 pages' ids and scales, one a lane
+          const int page = t * ppt + lane;
+          id = page < pages ? table[page] : -1;
+          if (id >= a.c.num_blocks) id = -1;
+          if (id >= 0) {
+            const int64_t s = static_cast<int64_t>(id) * a.c.H + it.h;
+            ke = kv8_exp(a.c.ks[s]);
+            ve = kv8_exp(a.c.vs[s]);
+          } else {
+            ke = kBadPage;
+            ve = 0;
+          }
+        }
+        const int from = (g & 31) + (lane & (ppt - 1));
+        const int my_id = __shfl_sync(0xffffffffu, id, from), my_ke = __shfl_sync(0xffffffffu, ke, from),
+                  my_ve = __shfl_sync(0xffffffffu, ve, from);
+        const bool mine = lane < ppt && my_id >= 0;
+        const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine)) * bs * D);
+        int at[3];
+        at[0] = 0;
+        at[1] = it.h;
+        at[2] = my_id;
+        const int x1 = at[a.order & 3], x2 = at[(a.order >> 2) & 3], x3 = at[(a.order >> 4) & 3];
+#pragma unroll
+        for (int part = 0; part < 2; ++part, ++fill) {
+          const uint32_t slot = fill % NS, bar = smem_addr(&sm.full[slot]);
+          bool ok = true;
+          if (fill >= NS) ok = bar_wait(smem_addr(&sm.empty[slot]), (fill / NS - 1) & 1, gave_up);
+          ok = __all_sync(0xffffffffu, ok);
+          if (part == 0 && lane < ppt) {
+            sm.kexp[i % kMetaRing][lane] = my_ke;
+            sm.vexp[i % kMetaRing][lane] = my_ve;
+          }
+          __syncwarp();
+          if (!ok) continue;  // a wait gave up: no copy is started any more
+          begun = fill + 1;
+          if (lane == 0) bar_expect(bar, bytes);
+          __syncwarp();
+          if (mine)
+            load_4d(smem_addr(ring + slot * C::kSlot + lane * bs * D), part == 0 ? &kmap : &vmap, bar, 0, x1, x2, x3);
+        }
+      }
+    } while (it.next(a));
+    if (*gave_up)  // copies that are still in flight write this block's memory
+      for (uint32_t f = begun > NS ? begun - NS : 0; f < begun; ++f)
+        for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.full[f % NS]), (f / NS) & 1); ++k) {
+        }
+  } else if (work && warp == kMmaWarp) {
+    // ---- products, issued by one thread
+    if (lane == 0) {
+      Walk<N> it(a, start, hi - lo);
+      int i = 0, seg = 0;
+      const uint32_t k_stride = 8 * D;
+      do {
+        const int nrw = C::group_rows(it.r.rows);
+        const uint32_t id_s = instr_desc(kTile, C::W * nrw, false), id_o = instr_desc(kTile, C::W * nrw, true);
+        auto scores = [&](int j) {  // S[j & 1] = K tile x Q^T
+          const uint32_t slot = (2u * j) % NS;
+          if (!bar_wait(smem_addr(&sm.full[slot]), ((2u * j) / NS) & 1, gave_up)) return;
+          fence_after();
+          const uint64_t kd = smem_desc(smem_addr(ring + slot * C::kSlot), 16, k_stride, C::kLayout);
+#pragma unroll
+          for (int t = 0; t < C::TERMS; ++t) {
+            const uint64_t qd = smem_desc(smem_addr(q_smem + t * N * D), 16, k_stride, C::kLayout);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+              mma_f8(tmem + (j & 1) * N, kd + 2 * k, qd + 2 * k, id_s, t > 0 || k > 0);
+          }
+          commit(smem_addr(&sm.empty[slot]));
+          commit(smem_addr(&sm.s_full[j & 1]));
+        };
+        bool ok = bar_wait(smem_addr(&sm.q_ready), seg & 1, gave_up);
+        fence_after();
+        if (ok) scores(i);
+        for (int t = it.t0; t < it.t1; ++t, ++i) {
+          if (*gave_up) continue;
+          if (t + 1 < it.t1) scores(i + 1);
+          const uint32_t slot = (2u * i + 1) % NS;
+          if (!bar_wait(smem_addr(&sm.p_ready), i & 1, gave_up)) continue;
+          if (!bar_wait(smem_addr(&sm.full[slot]), ((2u * i + 1) / NS) & 1, gave_up)) continue;
+          fence_after();
+          // D = 64: the two halves of the 128 rows are the same 64 dimensions (stride 0 between them)
+          const uint64_t vd = smem_desc(smem_addr(ring + slot * C::kSlot), 0, k_stride, C::kLayout);
+#pragma unroll
+          for (int u = 0; u < C::TERMS; ++u) {
+            const int col = u * N;
+            const uint64_t pd = smem_desc(smem_addr(p_smem + (col / 128) * (kTile * 128) + col % 128), 1024, 1024, 2);
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k)
+              mma_f8(tmem + 2 * N, vd + (k * 32 * D >> 4), pd + (k * 4096 >> 4), id_o, u > 0 || k > 0);
+          }
+          commit(smem_addr(&sm.empty[slot]));
+          commit(smem_addr(&sm.o_full));
+        }
+        ++seg;
+      } while (it.next(a));
+      if (*gave_up) {  // products that are still running write this block's tensor memory
+        commit(smem_addr(&sm.drain));
+        for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.drain), 0); ++k) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (work) {
+    // ---- softmax: a thread owns a slot of the tile and a dimension of the result
+    const int wg = warp >> 2, quarter = warp & 3;
+    const int own = quarter * 32 + lane;  // slot in the tile; dimension (mod D)
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    Walk<N> it(a, start, hi - lo);
+
+    // Queries of an item into shared memory, as e4m3 terms of q / 2^eq.
+    auto load_q = [&](const Walk<N>& w) -> int {
+      const int nrw = C::group_rows(w.r.rows);
+      const int chunks = C::W * nrw * (D / 8);
+      const int64_t r0 = static_cast<int64_t>(w.r.rt) * N;
+      const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (a.qst * 2) | (a.qsh * 2)) & 15) == 0;
+      auto chunk = [&](int c, float* x) {
+        const int row = c / (D / 8), d = (c % (D / 8)) * 8;
+        if (row >= w.r.rows) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = 0.f;
+          return;
+        }
+        const int64_t r = r0 + row;
+        const int64_t tok = r / a.group;
+        const int head = w.h * a.group + static_cast<int>(r - tok * a.group);
+        const QT* q = static_cast<const QT*>(a.q) + (w.r.first + tok) * a.qst + head * a.qsh + d;
+        if (vec) {
+          const uint4 u = *reinterpret_cast<const uint4*>(q);
+          const QT* e = reinterpret_cast<const QT*>(&u);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = to_f(e[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = to_f(q[k]);
+        }
+      };
+      float amax = 0.f;
+      for (int c = tid; c < chunks; c += C::kCompute) {
+        float x[8];
+        chunk(c, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (fabsf(x[k]) < -kNegInf) amax = fmaxf(amax, fabsf(x[k]));
+      }
+      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+      if (lane == 0) sm.red[warp] = amax;
+      named_sync(8, C::kCompute);
+      amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < C::W * 4; ++k) amax = fmaxf(amax, sm.red[k]);
+      const int eq = kv8_need(amax, -120, 120);
+      const float down = pow2i(-eq);
+      for (int c = tid; c < chunks; c += C::kCompute) {
+        float x[8];
+        chunk(c, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] *= down;
+        uint2 codes[C::TERMS];
+        split8<C::TERMS>(x, codes);
+        const uint32_t o = swz<D>(c / (D / 8), (c % (D / 8)) * 8);
+#pragma unroll
+        for (int t = 0; t < C::TERMS; ++t) *reinterpret_cast<uint2*>(q_smem + t * N * D + o) = codes[t];
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_addr(&sm.q_ready));
+      return eq;
+    };
+
+    float l[RW], o[RW];
+    float ref[RG];  // row 32 g + lane: the exponent its sums are relative to
+    int eq = load_q(it);
+    int i = 0;
+    bool more = true;
+    while (more) {
+      const RowTile r = it.r;
+      const int h = it.h, t0 = it.t0, t1 = it.t1;
+      const int nrw = C::group_rows(r.rows);
+      const int row_base = wg * nrw;  // first row of this group within the row tile
+      const int64_t r0 = static_cast<int64_t>(r.rt) * N;
+      const float scale = a.scale * pow2i(eq);
+#pragma unroll
+      for (int j = 0; j < RW; ++j) l[j] = 0.f, o[j] = 0.f;
+#pragma unroll
+      for (int g = 0; g < RG; ++g) ref[g] = kNegInf;
+      bool nan_prev = false;
+
+      // o += 2^(E - ref) times the product of tile number j, whose first slot is at
+      auto accumulate = [&](int j, int at, bool has_nan) {
+        bar_wait(smem_addr(&sm.o_full), j & 1, gave_up);
+        fence_after();
+        const float2* ef = sm.ef[j & 1][warp];
+#pragma unroll
+        for (int k = 0; k < HN; ++k) {
+          if (k * HC >= nrw) break;
+          uint32_t x[HC];
+          tmem_ld<HC>(lanes + 2 * N + row_base + k * HC, x);
+          wait_ld();
+          if (has_nan) {
+#pragma unroll 1
+            for (int q = 0; q < HC && k * HC + q < nrw; ++q) {
+              const int row = row_base + k * HC + q;
+              if (row >= r.rows) break;
+              const float sum = masked_sum<C>(a, r, h, at, row, static_cast<int>((r0 + row) / a.group), own % D, p_smem);
+#pragma unroll
+              for (int z = 0; z < HC; ++z)
+                if (z == q) x[z] = __float_as_uint(sum);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < HC; ++q) o[k * HC + q] = fmaf(ef[k * HC + q].y, __uint_as_float(x[q]), o[k * HC + q]);
+        }
+        if (has_nan) named_sync(1 + wg, 128);  // the weights are overwritten next
+      };
+
+      for (int t = t0; t < t1; ++t, ++i) {
+        const int slot0 = t * kTile, slot = slot0 + own, buf = i & 1;
+        bar_wait(smem_addr(&sm.s_full[buf]), (i >> 1) & 1, gave_up);
+        fence_after();
+        const int page = own / a.c.block;
+        const int ke = sm.kexp[i % kMetaRing][page], ve = sm.vexp[i % kMetaRing][page];
+        const float cs = ke == kBadPage ? __int_as_float(0x7fffffff) : scale * pow2i(ke);
+        const float ev = static_cast<float>(ve), ve_inv = pow2i(-ve);
+        const bool masked = slot0 + kTile > r.ctx;  // not every row sees every slot
+        if (masked) {
+          const uint32_t vslot = (2u * i + 1) % NS;
+          bar_wait(smem_addr(&sm.full[vslot]), ((2u * i + 1) / NS) & 1, gave_up);
+          uint4* vrow = reinterpret_cast<uint4*>(ring + vslot * C::kSlot + own * D);
+          bool nan = false;
+          if (slot >= r.end) {  // what lies behind the sequence is not read as values
+            if (wg == 0)
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) vrow[k] = make_uint4(0, 0, 0, 0);
+          } else {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint4 u = vrow[k];
+              nan |= (__vcmpeq4(u.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(u.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                      __vcmpeq4(u.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(u.w & 0x7f7f7f7fu, 0x7f7f7f7fu)) != 0;
+            }
+          }
+          nan = __any_sync(0xffffffffu, nan);
+          if (lane == 0) sm.nan[buf][wg][quarter] = nan;
+        }
+
+        // the tile's largest exponent of each row
+        float y[HC], mine = kNegInf;
+        uint32_t vis[HN];
+        auto scores = [&](int k) {
+          uint32_t x[HC];
+          tmem_ld<HC>(lanes + buf * N + row_base + k * HC, x);
+          wait_ld();
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < HC; ++j) y[j] = (vis[k] >> j) & 1 ? fmaf(__uint_as_float(x[j]), cs, ev) : kNegInf;
+          } else {
+#pragma unroll
+            for (int j = 0; j < HC; ++j) y[j] = fmaf(__uint_as_float(x[j]), cs, ev);
+          }
+        };
+#pragma unroll
+        for (int k = 0; k < HN; ++k) {
+          if (k * HC >= nrw) break;
+          vis[k] = 0xffffffffu;
+          if (masked && slot >= r.ctx) {
+            const int64_t row = r0 + row_base + k * HC;  // of the step
+            const int j = slot - r.ctx;
+            if (slot >= r.end) {
+              vis[k] = 0;
+            } else if (!a.tree) {
+              const int64_t first = static_cast<int64_t>(j) * a.group - row;
+              vis[k] = first <= 0 ? 0xffffffffu : (first >= HC ? 0u : 0xffffffffu << first);
+            } else {
+              uint32_t bits = 0;
+              int token = static_cast<int>(row / a.group), sub = static_cast<int>(row - static_cast<int64_t>(token) * a.group);
+              bool on = token < r.n && sees(a, r.b, token, j);
+              for (int q = 0; q < HC; ++q) {
+                if (on) bits |= 1u << q;
+                if (++sub == a.group) {
+                  sub = 0;
+                  ++token;
+                  on = token < r.n && sees(a, r.b, token, j);
+                }
+              }
+              vis[k] = bits;
+            }
+          }
+          scores(k);
+          if ((k & 1) == 0) mine = kNegInf;
+#pragma unroll
+          for (int j = 0; j < HC; ++j) {
+            if (j % GR == 0 && k * HC + j >= nrw) break;
+            const float m = warp_max(y[j]);
+            if (lane == (k & 1) * HC + j) mine = m;
+          }
+          if ((k & 1) == 1 || k == HN - 1 || (k + 1) * HC >= nrw) {
+            if (RL == 32 || lane < RL) sm.smax[buf][wg][quarter][(k / 2) * 32 + lane] = mine;
+          }
+        }
+        named_sync(1 + wg, 128);
+        bool nan_here = false;
+        if (masked) nan_here = (sm.nan[buf][wg][0] | sm.nan[buf][wg][1] | sm.nan[buf][wg][2] | sm.nan[buf][wg][3]) != 0;
+
+        if (t > t0) accumulate(i - 1, slot0 - kTile, nan_prev);
+        nan_prev = nan_here;
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+          if (g * 32 >= nrw) break;
+          const int row = g * 32 + lane % RL;
+          const float m = fmaxf(fmaxf(sm.smax[buf][wg][0][row], sm.smax[buf][wg][1][row]),
+                                fmaxf(sm.smax[buf][wg][2][row], sm.smax[buf][wg][3][row]));
+          const bool none = m == kNegInf;
+          const float e = none ? 0.f : ceilf(m);
+          const bool far = !none && e - ref[g] > 60.f;
+          if (__any_sync(0xffffffffu, far)) {
+            const float by = far ? exp2_whole(ref[g] - e) : 1.f;
+            if (far) ref[g] = e;
+#pragma unroll
+            for (int j = 0; j < RL; ++j) {
+              const float b = __shfl_sync(0xffffffffu, by, j);
+              l[g * 32 + j] *= b;
+              o[g * 32 + j] *= b;
+            }
+          }
+          sm.ef[buf][warp][row] = make_float2(e - 8.f, none ? 0.f : exp2_whole(e - ref[g]));
+        }
+        __syncwarp();
+
+        // weights, as e4m3 terms, and their sums
+        const float2* ef = sm.ef[buf][warp];
+#pragma unroll
+        for (int k = 0; k < HN; ++k) {
+          if (k * HC >= nrw) break;
+          scores(k);
+#pragma unroll
+          for (int jg = 0; jg < HC; jg += GR) {
+            if (k * HC + jg >= nrw) break;
+            uint32_t code[C::TERMS][GR / 4];
+#pragma unroll
+            for (int j = 0; j < GR; j += 2) {
+              const int q = k * HC + jg + j;
+              const float4 e = *reinterpret_cast<const float4*>(&ef[q]);
+              const float w0 = ex2_fast(y[jg + j] - e.x), w1 = ex2_fast(y[jg + j + 1] - e.z);
+              l[q] = fmaf(w0, e.y * ve_inv, l[q]);
+              l[q + 1] = fmaf(w1, e.w * ve_inv, l[q + 1]);
+              uint16_t c;
+              asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(w1), "f"(w0));
+              uint32_t rest;
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(rest) : "f"(w1), "f"(w0));
+#pragma unroll
+              for (int u = 0; u < C::TERMS; ++u) {
+                if (u > 0) {
+                  uint32_t back;
+                  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(c));
+                  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(rest) : "r"(back));
+                  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(rest));
+                }
+                if (j % 4 == 0) code[u][j / 4] = c;
+                else code[u][j / 4] |= static_cast<uint32_t>(c) << 16;
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < C::TERMS; ++u) {
+              const int col = u * N + row_base + k * HC + jg;
+              uint8_t* to = p_smem + (col / 128) * (kTile * 128) + swz<128>(own, col % 128);
+              if (GR == 8) *reinterpret_cast<uint2*>(to) = make_uint2(code[u][0], code[u][GR / 4 - 1]);
+              else *reinterpret_cast<uint32_t*>(to) = code[u][0];
+            }
+          }
+        }
+        fence_async_shared();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_addr(&sm.p_ready));
+      }
+
+      more = it.next(a);
+      if (more) eq = load_q(it);  // the products that read the last queries are done
+      accumulate(i - 1, (t1 - 1) * kTile, nan_prev);
+
+      // ---- the item's results, or its share of them
+      const bool whole = t0 == 0 && t1 == r.tiles;
+      const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (t0 > 0 ? 0 : 1);
+      auto& sums = sm.smax[(i - 1) & 1];  // every warp is past the last tile's maxima, and the next tile's go elsewhere
+#pragma unroll
+      for (int g = 0; g < RG; ++g) {
+        if (g * 32 >= nrw) break;
+        const float s = lane_sums<RL>(l + g * 32, lane);
+        if (RL == 32 || lane < RL) sums[wg][quarter][g * 32 + lane] = s;
+      }
+      named_sync(1 + wg, 128);
+#pragma unroll
+      for (int g = 0; g < RG; ++g) {
+        if (g * 32 >= nrw) break;
+        const int row = g * 32 + lane % RL;
+        const float s = (sums[wg][0][row] + sums[wg][1][row]) + (sums[wg][2][row] + sums[wg][3][row]);
+        if (whole) sm.ef[0][warp][row].x = s == 0.f ? 0.f : 1.f / s;
+        else if (quarter == 0 && lane < RL && row < nrw && row_base + row < r.rows)
+          a.part_ml[part * N + row_base + row] = make_float2(ref[g], s);
+      }
+      __syncwarp();
+      if (own < D) {
+        int64_t tok = (r0 + row_base) / a.group;
+        int sub = static_cast<int>(r0 + row_base - tok * a.group);
+        QT* out = static_cast<QT*>(a.out) + own;
+#pragma unroll
+        for (int j = 0; j < RW; ++j) {
+          if (j >= nrw || row_base + j >= r.rows) break;
+          if (whole) out[(r.first + tok) * a.ost + (h * a.group + sub) * a.osh] = from_f<QT>(o[j] * sm.ef[0][warp][j].x);
+          else a.part_o[(part * N + row_base + j) * D + own] = o[j];
+          if (++sub == a.group) sub = 0, ++tok;
+        }
+      }
+    }
+  }
+
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == kMmaWarp) tmem_free(tmem, C::kCols);
+  if (tid == 0) a.gave_up[blockIdx.x] = sm.gave_up;
+  griddep_launch_dependents();
+}
+
+// -------------------------------------------------------------------- join --
+//
+// Adds the shares of items that runs cut. Block x takes the item that begins in
+// part x and ends behind it, a warp one row: shares in the order of the parts,
+// each times 2^(its reference - the largest). The last blocks check sequences.
+
+constexpr int kJoinThreads = 256;
+
+template <typename QT, int D, int N>
+__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ Kv8AttnArgs a) {
+  __shared__ int s_tmp[36];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_launch_dependents();
+  if (blockIdx.x >= static_cast<unsigned>(a.parts)) {  // a warp per sequence: row_status
+    griddep_wait();
+    const int b = (blockIdx.x - a.parts) * (kJoinThreads / 32) + warp;
+    if (blockIdx.y > 0 || b >= a.c.B) return;
+    bool late = false;
+    for (int i = lane; i < a.parts; i += 32) late |= a.gave_up[i] != 0;
+    const int lo = a.cu[b], hi = a.cu[b + 1], len = a.c.len[b];
+    const bool sound = kv8_seq_ok(a.c, a.T, lo, hi, len) && hi - lo <= a.max_tokens;
+    bool bad = !sound;
+    if (sound && hi > lo) {
+      const int pages = (len + (hi - lo) + a.c.block - 1) / a.c.block;
+      for (int j = lane; j < pages; j += 32) {
+        const int id = a.c.table[static_cast<int64_t>(b) * a.c.max_blocks + j];
+        bad |= id < 0 || id >= a.c.num_blocks;
+      }
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    late = __any_sync(0xffffffffu, late);
+    if (lane == 0) a.row_status[b] = (bad ? SPEC_ROW_CACHE : 0) | (late ? SPEC_ROW_TIMEOUT : 0);
+    if (!sound && lo >= 0 && hi > lo && hi <= a.T) {
+      const int64_t rows = static_cast<int64_t>(hi - lo) * a.q_heads;
+      for (int64_t i = 0; i < rows; ++i) {
+        QT* out = static_cast<QT*>(a.out) + (lo + i / a.q_heads) * a.ost + (i % a.q_heads) * a.osh;
+        for (int d = lane; d < D; d += 32) out[d] = from_f<QT>(__int_as_float(0x7fffffff));
+      }
+    }
+    return;
+  }
+  int64_t lo, hi, all;
+  Start s;
+  if (!find_run<N>(a, blockIdx.x, true, &lo, &hi, &s, &all, s_tmp)) return;
+  const RowTile r = row_tile<N>(a, s.b, s.rt);
+  const int64_t begin = hi - 1 - s.t, end = begin + r.tiles;  // the item's tiles
+  const int row = blockIdx.y * (kJoinThreads / 32) + warp;
+  if (begin < lo || end <= hi || row >= r.rows) return;
+  const int64_t parts = min(static_cast<int64_t>(a.parts), all);
+  int64_t last = (end - 1) * parts / all;
+  while (all * (last + 1) / parts <= end - 1) ++last;
+  const int n = static_cast<int>(last - blockIdx.x) + 1;
+  griddep_wait();
+  const int64_t first = blockIdx.x;
+  auto share = [&](int i) { return (2 * (first + i) + (i == 0 ? 1 : 0)) * N + row; };
+  float top = kNegInf;
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, a.part_ml[share(i)].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (top == kNegInf) top = 0.f;
+  constexpr int V = D / 32;
+  float acc[V] = {}, sum = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float2 ml = a.part_ml[share(i)];
+    const float* p = a.part_o + share(i) * D + lane * V;
+    float x[V];
+    if (V == 4) {
+      const float4 u = *reinterpret_cast<const float4*>(p);
+      x[0] = u.x, x[1] = u.y, x[V - 2] = u.z, x[V - 1] = u.w;
+    } else {
+      const float2 u = *reinterpret_cast<const float2*>(p);
+      x[0] = u.x, x[1] = u.y;
+    }
+    const float w = exp2_whole(ml.x - top);
+    sum = fmaf(w, ml.y, sum);
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = fmaf(w, x[k], acc[k]);
+  }
+  const int64_t item_row = static_cast<int64_t>(s.rt) * N + row, tok = item_row / a.group;
+  QT* out = static_cast<QT*>(a.out) + (r.first + tok) * a.ost +
+            (s.h * a.group + static_cast<int>(item_row - tok * a.group)) * a.osh + lane * V;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int k = 0; k < V; ++k) out[k] = from_f<QT>(acc[k] * inv);
+}
+
+// ------------------------------------------------------------------ launch --
+
+constexpr int kSms = 152;
+
+template <typename QT, int D, int RW, int W, int TERMS>
+cudaError_t launch_attention(const Kv8AttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t st) {
+  using C = Cfg<D, RW, W, TERMS>;
+  auto kernel = kv8_attention_kernel<QT, C>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.parts));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, a, k, v);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(a.max_tokens) * a.group;
+  const int y = static_cast<int>((rows < C::N ? rows : C::N) + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+  const int checks = (a.c.B + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+  return launch_pdl(kv8_join_kernel<QT, D, C::N>, dim3(static_cast<unsigned>(a.parts + checks), static_cast<unsigned>(y)),
+                    dim3(kJoinThreads), st, a);
+}
+
+template <typename QT, int D, int TERMS>
+cudaError_t launch_rows(const Kv8AttnArgs& a, int rows, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t st) {
+  if (rows == 16) return launch_attention<QT, D, 16, 1, TERMS>(a, k, v, st);
+  if (rows == 32) return launch_attention<QT, D, 16, 2, TERMS>(a, k, v, st);
+  if (rows == 64) return launch_attention<QT, D, 16, 4, TERMS>(a, k, v, st);
+  return launch_attention<QT, D, 32, 4, TERMS>(a, k, v, st);
 }
 
 }  // namespace
 
-cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, int dtype, cudaStream_t st) {
-  return dtype == SPEC_BF16 ? launch_rows<__nv_bfloat16>(a, st) : launch_rows<__half>(a, st);
+int kv8_attention_rows(int64_t max_rows) { return max_rows <= 16 ? 16 : (max_rows <= 32 ? 32 : (max_rows <= 64 ? 64 : 128)); }
+
+int kv8_attention_parts(int rows) { return rows <= 32 ? 2 * kSms : kSms; }
+
+cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, int dtype, int rows, const CUtensorMap& k, const CUtensorMap& v,
+                                 cudaStream_t st) {
+  if (dtype == SPEC_BF16)
+    return a.c.D == 128 ? launch_rows<__nv_bfloat16, 128, 2>(a, rows, k, v, st)
+                        : launch_rows<__nv_bfloat16, 64, 2>(a, rows, k, v, st);
+  return a.c.D == 128 ? launch_rows<__half, 128, 3>(a, rows, k, v, st) : launch_rows<__half, 64, 3>(a, rows, k, v, st);
 }
 
 }  // namespace specv
