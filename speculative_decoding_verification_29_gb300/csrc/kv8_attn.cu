@@ -241,7 +241,7 @@ struct Cfg {
     float smax[2][W][4][RW];
     float2 ef[2][W * 4][RW];
     float red[W * 4];
-    int nan[2][W][4];
+    int nan[2];
     int kexp[kMetaRing][kMaxPages], vexp[kMetaRing][kMaxPages];
     alignas(8) uint64_t full[12], empty[12], s_full[2], p_ready, o_full, q_ready, drain;
     uint32_t tmem;
@@ -301,34 +301,9 @@ __device__ __forceinline__ float lane_sums(float* v, int lane) {
   return v[0];
 }
 
-// Whether row r (token r / group of the step) sees step slot j.
+// Whether the step's token i sees its token j.
 __device__ __forceinline__ bool sees(const Kv8AttnArgs& a, int b, int i, int j) {
   return a.tree ? a.tree[(static_cast<int64_t>(b) * a.max_tokens + i) * a.max_tokens + j] != 0 : j <= i;
-}
-
-// A tile that holds NaN values and slots not every row sees: dimension d of one
-// row's weighted sum over the slots that the row does see.
-template <typename C>
-__device__ __noinline__ float masked_sum(const Kv8AttnArgs& a, const RowTile& r, int h, int slot0, int row, int token,
-                                         int d, const uint8_t* p_smem) {
-  float sum = 0.f;
-  const int bs = a.c.block;
-  for (int u = 0; u < kTile && slot0 + u < r.end; ++u) {
-    const int slot = slot0 + u;
-    if (slot >= r.ctx && !sees(a, r.b, token, slot - r.ctx)) continue;
-    const int id = a.c.table[static_cast<int64_t>(r.b) * a.c.max_blocks + slot / bs];
-    if (id < 0 || id >= a.c.num_blocks) return __int_as_float(0x7fffffff);
-    float w = 0.f, x[4];
-#pragma unroll
-    for (int t = 0; t < C::TERMS; ++t) {
-      const int col = t * C::N + row;
-      kv8_values4(p_smem[(col / 128) * (kTile * 128) + swz<128>(u, col % 128)], x);
-      w += x[0];
-    }
-    kv8_values4(a.c.v[id * a.c.sb + h * a.c.sh + (slot % bs) * a.c.ss + d], x);
-    sum = fmaf(w, x[0], sum);
-  }
-  return sum;
 }
 
 // ----------------------------------------------------------------- kernel --
@@ -491,7 +466,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       }
     }
     __syncwarp();
-  } else if (work) {
+  } else if (work && warp < kLoadWarp) {
     // ---- softmax: a thread owns a slot of the tile and a dimension of the result
     const int wg = warp >> 2, quarter = warp & 3;
     const int own = quarter * 32 + lane;  // slot in the tile; dimension (mod D)
@@ -499,7 +474,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     Walk<N> it(a, start, hi - lo);
 
     // Queries of an item into shared memory, as e4m3 terms of q / 2^eq.
-    auto load_q = [&](const Walk<N>& w) -> int {
+    auto load_q = [&](const Walk<N>& w, int item) -> int {
       const int nrw = C::group_rows(w.r.rows);
       const int chunks = C::W * nrw * (D / 8);
       const int64_t r0 = static_cast<int64_t>(w.r.rt) * N;
@@ -535,6 +510,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       }
       amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
       if (lane == 0) sm.red[warp] = amax;
+      if (tid == 0) sm.nan[item & 1] = 0;
       named_sync(8, C::kCompute);
       amax = 0.f;
 #pragma unroll
@@ -560,8 +536,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 
     float l[RW], o[RW];
     float ref[RG];  // row 32 g + lane: the exponent its sums are relative to
-    int eq = load_q(it);
-    int i = 0;
+    int eq = load_q(it, 0);
+    int i = 0, seg = 0;  // tiles and items so far
     bool more = true;
     while (more) {
       const RowTile r = it.r;
@@ -574,10 +550,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       for (int j = 0; j < RW; ++j) l[j] = 0.f, o[j] = 0.f;
 #pragma unroll
       for (int g = 0; g < RG; ++g) ref[g] = kNegInf;
-      bool nan_prev = false;
 
-      // o += 2^(E - ref) times the product of tile number j, whose first slot is at
-      auto accumulate = [&](int j, int at, bool has_nan) {
+      // o += 2^(E - ref) times the product of tile number j
+      auto accumulate = [&](int j) {
         bar_wait(smem_addr(&sm.o_full), j & 1, gave_up);
         fence_after();
         const float2* ef = sm.ef[j & 1][warp];
@@ -587,21 +562,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           uint32_t x[HC];
           tmem_ld<HC>(lanes + 2 * N + row_base + k * HC, x);
           wait_ld();
-          if (has_nan) {
-#pragma unroll 1
-            for (int q = 0; q < HC && k * HC + q < nrw; ++q) {
-              const int row = row_base + k * HC + q;
-              if (row >= r.rows) break;
-              const float sum = masked_sum<C>(a, r, h, at, row, static_cast<int>((r0 + row) / a.group), own % D, p_smem);
-#pragma unroll
-              for (int z = 0; z < HC; ++z)
-                if (z == q) x[z] = __float_as_uint(sum);
-            }
-          }
 #pragma unroll
           for (int q = 0; q < HC; ++q) o[k * HC + q] = fmaf(ef[k * HC + q].y, __uint_as_float(x[q]), o[k * HC + q]);
         }
-        if (has_nan) named_sync(1 + wg, 128);  // the weights are overwritten next
       };
 
       for (int t = t0; t < t1; ++t, ++i) {
@@ -613,25 +576,28 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         const float cs = ke == kBadPage ? __int_as_float(0x7fffffff) : scale * pow2i(ke);
         const float ev = static_cast<float>(ve), ve_inv = pow2i(-ve);
         const bool masked = slot0 + kTile > r.ctx;  // not every row sees every slot
-        if (masked) {
+        if (masked && wg == 0) {
+          // Slots behind the sequence hold no values, and a NaN value must not reach the rows that do not see it
+          // through a weight of 0: both are cleared here, and the rows that see a NaN get it at the item's end.
           const uint32_t vslot = (2u * i + 1) % NS;
           bar_wait(smem_addr(&sm.full[vslot]), ((2u * i + 1) / NS) & 1, gave_up);
           uint4* vrow = reinterpret_cast<uint4*>(ring + vslot * C::kSlot + own * D);
           bool nan = false;
-          if (slot >= r.end) {  // what lies behind the sequence is not read as values
-            if (wg == 0)
+#pragma unroll 1
+          for (int k = 0; k < D / 16; ++k) {
+            uint4 u = vrow[k];
+            uint32_t any = 0;
+            uint32_t* w = &u.x;
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k) vrow[k] = make_uint4(0, 0, 0, 0);
-          } else {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint4 u = vrow[k];
-              nan |= (__vcmpeq4(u.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(u.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-                      __vcmpeq4(u.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(u.w & 0x7f7f7f7fu, 0x7f7f7f7fu)) != 0;
+            for (int z = 0; z < 4; ++z) {
+              const uint32_t m = slot >= r.end ? 0xffffffffu : __vcmpeq4(w[z] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              any |= m;
+              w[z] &= ~m;
             }
+            if (any) vrow[k] = u;
+            nan |= any != 0;
           }
-          nan = __any_sync(0xffffffffu, nan);
-          if (lane == 0) sm.nan[buf][wg][quarter] = nan;
+          if (nan && slot < r.end) sm.nan[seg & 1] = 1;
         }
 
         // the tile's largest exponent of each row
@@ -689,11 +655,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           }
         }
         named_sync(1 + wg, 128);
-        bool nan_here = false;
-        if (masked) nan_here = (sm.nan[buf][wg][0] | sm.nan[buf][wg][1] | sm.nan[buf][wg][2] | sm.nan[buf][wg][3]) != 0;
-
-        if (t > t0) accumulate(i - 1, slot0 - kTile, nan_prev);
-        nan_prev = nan_here;
+        if (t > t0) accumulate(i - 1);
 #pragma unroll
         for (int g = 0; g < RG; ++g) {
           if (g * 32 >= nrw) break;
@@ -766,8 +728,21 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       }
 
       more = it.next(a);
-      if (more) eq = load_q(it);  // the products that read the last queries are done
-      accumulate(i - 1, (t1 - 1) * kTile, nan_prev);
+      if (more) eq = load_q(it, seg + 1);  // the products that read the last queries are done
+      accumulate(i - 1);
+      if (sm.nan[seg & 1]) {  // set before the weights of its tile were ready
+        for (int slot = max(t0, r.ctx / kTile) * kTile; slot < min(r.end, t1 * kTile); ++slot) {
+          const int id = a.c.table[static_cast<int64_t>(r.b) * a.c.max_blocks + slot / a.c.block];
+          if (id < 0 || id >= a.c.num_blocks) continue;
+          const uint8_t code = a.c.v[id * a.c.sb + h * a.c.sh + (slot % a.c.block) * a.c.ss + own % D];
+          if ((code & 0x7f) != 0x7f) continue;
+#pragma unroll
+          for (int j = 0; j < RW; ++j)
+            if (slot < r.ctx || sees(a, r.b, min(r.n - 1, static_cast<int>((r0 + row_base + j) / a.group)), slot - r.ctx))
+              o[j] = __int_as_float(0x7fffffff);
+        }
+      }
+      ++seg;
 
       // ---- the item's results, or its share of them
       const bool whole = t0 == 0 && t1 == r.tiles;

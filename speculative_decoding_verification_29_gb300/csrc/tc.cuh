@@ -42,22 +42,17 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // a wait gives up after two second
 // Waits for the barrier's phase; false, with *gave_up set, when the limit ran
 // out. Once a wait of the block has given up no other waits: every role then
 // runs through its loop without touching the tensor core or starting copies.
-static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+  if (bar_try(bar, parity)) return true;
   const uint64_t t0 = now_ns();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (bar_try(bar, parity)) return true;
+  while (!bar_try(bar, parity)) {
     if (*gave_up) return false;
     if (now_ns() - t0 > kWaitNs) {
       *gave_up = 1;
       return false;
     }
   }
-}
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-  if (bar_try(bar, parity)) return true;
-  return bar_wait_slow(bar, parity, gave_up);
+  return true;
 }
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
