@@ -239,7 +239,8 @@ struct Cfg {
 
   struct Small {
     float smax[2][W][4][RW];
-    float2 ef[2][W * 4][RW];
+    float e[W * 4][RW];     // of each warp: what the tile's scores are shifted by
+    float f[2][W * 4][RW];  // and the tiles' factors
     float red[W * 4];
     int nan[2];
     int kexp[kMetaRing][kMaxPages], vexp[kMetaRing][kMaxPages];
@@ -280,7 +281,11 @@ __device__ __forceinline__ void split8(float* x, uint2* out) {
   }
 }
 
-__device__ __forceinline__ float exp2_whole(float d) { return exp2f(d); }  // d whole, -inf or NaN: exact
+// 2^d of a whole d <= 127, exact; 0 below -126 and for -inf, NaN for NaN.
+__device__ __forceinline__ float exp2_whole(float d) {
+  const float p = __int_as_float((static_cast<int>(fmaxf(d, -127.f)) + 127) << 23);
+  return d != d ? d : p;
+}
 
 // Sums v[0 .. C - 1] over the warp's lanes; lane j (mod C) gets the sum of v[j].
 template <int C>
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   const bool work = find_run<N>(a, blockIdx.x, false, &lo, &hi, &start, &all, sm.tmp);
   __syncthreads();
   fence_after();
-  const uint32_t tmem = sm.tmem;
+  const uint32_t tmem = uniform(sm.tmem);
 
   if (work && warp == kLoadWarp) {
     // ---- copies: the pages of each tile's keys, then of its values
@@ -411,45 +416,52 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.full[f % NS]), (f / NS) & 1); ++k) {
         }
   } else if (work && warp == kMmaWarp) {
-    // ---- products, issued by one thread
-    if (lane == 0) {
-      Walk<N> it(a, start, hi - lo);
-      int i = 0, seg = 0;
-      const uint32_t k_stride = 8 * D;
-      do {
-        const int nrw = C::group_rows(it.r.rows);
-        const uint32_t id_s = instr_desc(kTile, C::W * nrw, false), id_o = instr_desc(kTile, C::W * nrw, true);
-        auto scores = [&](int j) {  // S[j & 1] = K tile x Q^T
-          const uint32_t slot = (2u * j) % NS;
-          if (!bar_wait(smem_addr(&sm.full[slot]), ((2u * j) / NS) & 1, gave_up)) return;
-          fence_after();
-          const uint64_t kd = smem_desc(smem_addr(ring + slot * C::kSlot), 16, k_stride, C::kLayout);
+    // ---- products: the warp waits together, one lane issues
+    Walk<N> it(a, start, hi - lo);
+    int i = 0, seg = 0;
+    constexpr uint32_t kStride = 8 * D;
+    const uint32_t ring_at = smem_addr(ring), q_at = smem_addr(q_smem), p_at = smem_addr(p_smem);
+    do {
+      const uint32_t cols = uniform(C::W * C::group_rows(it.r.rows));
+      const uint32_t id_s = instr_desc(kTile, cols, false), id_o = instr_desc(kTile, cols, true);
+      auto scores = [&](int j) {  // S[j & 1] = K tile x Q^T
+        const uint32_t slot = uniform((2u * j) % NS), to = uniform(tmem + (j & 1) * N);
+        bool ok = bar_wait(smem_addr(&sm.full[slot]), ((2u * j) / NS) & 1, gave_up);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        fence_after();
+        if (elect()) {
+          const uint64_t kd = smem_desc(ring_at + slot * C::kSlot, 16, kStride, C::kLayout);
 #pragma unroll
           for (int t = 0; t < C::TERMS; ++t) {
-            const uint64_t qd = smem_desc(smem_addr(q_smem + t * N * D), 16, k_stride, C::kLayout);
+            const uint64_t qd = smem_desc(q_at + t * N * D, 16, kStride, C::kLayout);
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-              mma_f8(tmem + (j & 1) * N, kd + 2 * k, qd + 2 * k, id_s, t > 0 || k > 0);
+            for (int k = 0; k < D / 32; ++k) mma_f8(to, kd + 2 * k, qd + 2 * k, id_s, t > 0 || k > 0);
           }
           commit(smem_addr(&sm.empty[slot]));
           commit(smem_addr(&sm.s_full[j & 1]));
-        };
-        bool ok = bar_wait(smem_addr(&sm.q_ready), seg & 1, gave_up);
+        }
+        __syncwarp();
+      };
+      bool ok = bar_wait(smem_addr(&sm.q_ready), seg & 1, gave_up);
+      ok = __all_sync(0xffffffffu, ok);
+      fence_after();
+      if (ok) scores(i);
+      for (int t = it.t0; t < it.t1; ++t, ++i) {
+        if (t + 1 < it.t1) scores(i + 1);
+        const uint32_t slot = uniform((2u * i + 1) % NS);
+        ok = bar_wait(smem_addr(&sm.full[slot]), ((2u * i + 1) / NS) & 1, gave_up) &&
+             bar_wait(smem_addr(&sm.p_ready), i & 1, gave_up);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
         fence_after();
-        if (ok) scores(i);
-        for (int t = it.t0; t < it.t1; ++t, ++i) {
-          if (*gave_up) continue;
-          if (t + 1 < it.t1) scores(i + 1);
-          const uint32_t slot = (2u * i + 1) % NS;
-          if (!bar_wait(smem_addr(&sm.p_ready), i & 1, gave_up)) continue;
-          if (!bar_wait(smem_addr(&sm.full[slot]), ((2u * i + 1) / NS) & 1, gave_up)) continue;
-          fence_after();
+        if (elect()) {
           // D = 64: the two halves of the 128 rows are the same 64 dimensions (stride 0 between them)
-          const uint64_t vd = smem_desc(smem_addr(ring + slot * C::kSlot), 0, k_stride, C::kLayout);
+          const uint64_t vd = smem_desc(ring_at + slot * C::kSlot, 0, kStride, C::kLayout);
 #pragma unroll
           for (int u = 0; u < C::TERMS; ++u) {
-            const int col = u * N;
-            const uint64_t pd = smem_desc(smem_addr(p_smem + (col / 128) * (kTile * 128) + col % 128), 1024, 1024, 2);
+            constexpr uint32_t kPanel = kTile * 128;
+            const uint64_t pd = smem_desc(p_at + (u * N / 128) * kPanel + u * N % 128, 1024, 1024, 2);
 #pragma unroll
             for (int k = 0; k < kTile / 32; ++k)
               mma_f8(tmem + 2 * N, vd + (k * 32 * D >> 4), pd + (k * 4096 >> 4), id_o, u > 0 || k > 0);
@@ -457,18 +469,19 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           commit(smem_addr(&sm.empty[slot]));
           commit(smem_addr(&sm.o_full));
         }
-        ++seg;
-      } while (it.next(a));
-      if (*gave_up) {  // products that are still running write this block's tensor memory
-        commit(smem_addr(&sm.drain));
-        for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.drain), 0); ++k) {
-        }
+        __syncwarp();
+      }
+      ++seg;
+    } while (it.next(a));
+    if (*gave_up) {  // products that are still running write this block's tensor memory
+      if (elect()) commit(smem_addr(&sm.drain));
+      for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.drain), 0); ++k) {
       }
     }
     __syncwarp();
   } else if (work && warp < kLoadWarp) {
     // ---- softmax: a thread owns a slot of the tile and a dimension of the result
-    const int wg = warp >> 2, quarter = warp & 3;
+    const int wg = uniform(warp >> 2), quarter = uniform(warp & 3);
     const int own = quarter * 32 + lane;  // slot in the tile; dimension (mod D)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     Walk<N> it(a, start, hi - lo);
@@ -540,9 +553,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     int i = 0, seg = 0;  // tiles and items so far
     bool more = true;
     while (more) {
-      const RowTile r = it.r;
-      const int h = it.h, t0 = it.t0, t1 = it.t1;
-      const int nrw = C::group_rows(r.rows);
+      RowTile r = it.r;
+      r.ctx = uniform(r.ctx);
+      r.end = uniform(r.end);
+      r.rows = uniform(r.rows);
+      const int h = uniform(it.h), t0 = uniform(it.t0), t1 = uniform(it.t1);
+      const int nrw = uniform(C::group_rows(r.rows));
       const int row_base = wg * nrw;  // first row of this group within the row tile
       const int64_t r0 = static_cast<int64_t>(r.rt) * N;
       const float scale = a.scale * pow2i(eq);
@@ -555,7 +571,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       auto accumulate = [&](int j) {
         bar_wait(smem_addr(&sm.o_full), j & 1, gave_up);
         fence_after();
-        const float2* ef = sm.ef[j & 1][warp];
+        const float* f = sm.f[j & 1][warp];
 #pragma unroll
         for (int k = 0; k < HN; ++k) {
           if (k * HC >= nrw) break;
@@ -563,7 +579,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           tmem_ld<HC>(lanes + 2 * N + row_base + k * HC, x);
           wait_ld();
 #pragma unroll
-          for (int q = 0; q < HC; ++q) o[k * HC + q] = fmaf(ef[k * HC + q].y, __uint_as_float(x[q]), o[k * HC + q]);
+          for (int q = 0; q < HC; q += 4) {
+            const float4 g = *reinterpret_cast<const float4*>(f + k * HC + q);
+            float* to = o + k * HC + q;
+            const float2 u = fma2(make_float2(__uint_as_float(x[q]), __uint_as_float(x[q + 1])), make_float2(g.x, g.y),
+                                  make_float2(to[0], to[1]));
+            const float2 v = fma2(make_float2(__uint_as_float(x[q + 2]), __uint_as_float(x[q + 3])), make_float2(g.z, g.w),
+                                  make_float2(to[2], to[3]));
+            to[0] = u.x, to[1] = u.y, to[2] = v.x, to[3] = v.y;
+          }
         }
       };
 
@@ -607,12 +631,17 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           uint32_t x[HC];
           tmem_ld<HC>(lanes + buf * N + row_base + k * HC, x);
           wait_ld();
+#pragma unroll
+          for (int j = 0; j < HC; j += 2) {
+            const float2 z = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), make_float2(cs, cs),
+                                  make_float2(ev, ev));
+            y[j] = z.x;
+            y[j + 1] = z.y;
+          }
           if (masked) {
 #pragma unroll
-            for (int j = 0; j < HC; ++j) y[j] = (vis[k] >> j) & 1 ? fmaf(__uint_as_float(x[j]), cs, ev) : kNegInf;
-          } else {
-#pragma unroll
-            for (int j = 0; j < HC; ++j) y[j] = fmaf(__uint_as_float(x[j]), cs, ev);
+            for (int j = 0; j < HC; ++j)
+              if (!((vis[k] >> j) & 1)) y[j] = kNegInf;
           }
         };
 #pragma unroll
@@ -645,10 +674,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           scores(k);
           if ((k & 1) == 0) mine = kNegInf;
 #pragma unroll
-          for (int j = 0; j < HC; ++j) {
-            if (j % GR == 0 && k * HC + j >= nrw) break;
-            const float m = warp_max(y[j]);
-            if (lane == (k & 1) * HC + j) mine = m;
+          for (int jg = 0; jg < HC; jg += GR) {
+            if (k * HC + jg >= nrw) break;
+            float m[GR];
+#pragma unroll
+            for (int j = 0; j < GR; ++j) m[j] = warp_max(y[jg + j]);
+#pragma unroll
+            for (int j = 0; j < GR; ++j)
+              if (lane == (k & 1) * HC + jg + j) mine = m[j];
           }
           if ((k & 1) == 1 || k == HN - 1 || (k + 1) * HC >= nrw) {
             if (RL == 32 || lane < RL) sm.smax[buf][wg][quarter][(k / 2) * 32 + lane] = mine;
@@ -675,12 +708,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
               o[g * 32 + j] *= b;
             }
           }
-          sm.ef[buf][warp][row] = make_float2(e - 8.f, none ? 0.f : exp2_whole(e - ref[g]));
+          sm.e[warp][row] = 8.f - e;
+          sm.f[buf][warp][row] = none ? 0.f : exp2_whole(e - ref[g]);
         }
         __syncwarp();
 
         // weights, as e4m3 terms, and their sums
-        const float2* ef = sm.ef[buf][warp];
 #pragma unroll
         for (int k = 0; k < HN; ++k) {
           if (k * HC >= nrw) break;
@@ -692,10 +725,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
             for (int j = 0; j < GR; j += 2) {
               const int q = k * HC + jg + j;
-              const float4 e = *reinterpret_cast<const float4*>(&ef[q]);
-              const float w0 = ex2_fast(y[jg + j] - e.x), w1 = ex2_fast(y[jg + j + 1] - e.z);
-              l[q] = fmaf(w0, e.y * ve_inv, l[q]);
-              l[q + 1] = fmaf(w1, e.w * ve_inv, l[q + 1]);
+              const float2 e = *reinterpret_cast<const float2*>(&sm.e[warp][q]);
+              const float2 f = *reinterpret_cast<const float2*>(&sm.f[buf][warp][q]);
+              const float2 z = add2(make_float2(y[jg + j], y[jg + j + 1]), e);
+              const float w0 = ex2_fast(z.x), w1 = ex2_fast(z.y);
+              const float2 s = fma2(make_float2(w0, w1), mul2(f, make_float2(ve_inv, ve_inv)), make_float2(l[q], l[q + 1]));
+              l[q] = s.x;
+              l[q + 1] = s.y;
               uint16_t c;
               asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(w1), "f"(w0));
               uint32_t rest;
@@ -760,7 +796,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         if (g * 32 >= nrw) break;
         const int row = g * 32 + lane % RL;
         const float s = (sums[wg][0][row] + sums[wg][1][row]) + (sums[wg][2][row] + sums[wg][3][row]);
-        if (whole) sm.ef[0][warp][row].x = s == 0.f ? 0.f : 1.f / s;
+        if (whole) sm.e[warp][row] = s == 0.f ? 0.f : 1.f / s;
         else if (quarter == 0 && lane < RL && row < nrw && row_base + row < r.rows)
           a.part_ml[part * N + row_base + row] = make_float2(ref[g], s);
       }
@@ -772,7 +808,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
         for (int j = 0; j < RW; ++j) {
           if (j >= nrw || row_base + j >= r.rows) break;
-          if (whole) out[(r.first + tok) * a.ost + (h * a.group + sub) * a.osh] = from_f<QT>(o[j] * sm.ef[0][warp][j].x);
+          if (whole) out[(r.first + tok) * a.ost + (h * a.group + sub) * a.osh] = from_f<QT>(o[j] * sm.e[warp][j]);
           else a.part_o[(part * N + row_base + j) * D + own] = o[j];
           if (++sub == a.group) sub = 0, ++tok;
         }
