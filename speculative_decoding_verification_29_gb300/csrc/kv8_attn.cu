@@ -27,7 +27,12 @@
 // list, found on the device from the lengths. An item cut by a run's end leaves
 // partial sums; a second kernel joins them, in order. One warp copies K and V
 // blocks into a ring of tile slots by bulk tensor copies, one issues the
-// products, four or eight compute the softmax.
+// products, groups of four warps turn scores into weights and add the products
+// up, each for its share of the rows.
+// A step of the softmax group: scores and the product of the tile before last
+// leave tensor memory together, each row's maximum crosses lanes by redux and
+// warps by shared memory, the weights are written, and the tile's product runs
+// while the next tiles are worked on.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -220,41 +225,49 @@ struct Walk {
 // ---------------------------------------------------------- configuration --
 
 // D: head dimension. RW: rows of one softmax group of four warps, W: groups.
-template <int D_, int RW_, int W_, int TERMS_>
+template <int D_, int RW_, int W_, int TERMS_, int CTAS_>
 struct Cfg {
   static constexpr int D = D_, RW = RW_, W = W_, TERMS = TERMS_;
   static constexpr int N = RW * W;
-  static constexpr int kCompute = W * 128, kThreads = kCompute + 64;
-  static constexpr int kCtas = N <= 32 ? 2 : 1;  // resident on an SM
+  static constexpr int EW = (N + 31) / 32;                 // warps that load queries, a row a lane
+  static constexpr int kThreads = W * 128 + EW * 32 + 64;  // softmax, queries, copies and products
+  static constexpr int kCtas = CTAS_;                  // resident on an SM
   static constexpr int kSlot = kTile * D;
-  static constexpr int kQ = TERMS * N * D < 1024 ? 1024 : TERMS * N * D;
-  static constexpr int kPanels = (TERMS * N + 127) / 128, kP = kPanels * kTile * 128;
-  static constexpr int kCols = 3 * N <= 64 ? 64 : (3 * N <= 128 ? 128 : (3 * N <= 256 ? 256 : 512));
-  static constexpr int kGrain = W > 2 ? 4 : 8;  // a group's rows are rounded to this, N to 16
-  static __device__ __forceinline__ int group_rows(int rows) {
-    constexpr int g = W == 1 ? 16 : kGrain;
-    return ((rows + W - 1) / W + g - 1) / g * g;
-  }
+  static constexpr int kQ = TERMS * N * D;  // one item's queries; two are kept
+  static constexpr int kTerm = N == 48 ? 64 : N;  // a term's columns in a row of weights: none crosses a panel of 128
+  static constexpr int kPanels = (TERMS * kTerm + 127) / 128, kP = kPanels * kTile * 128;  // one tile's weights; two are kept
+  static_assert(128 % kTerm == 0, "terms within panels");
+  static constexpr int kCols = N <= 16 ? 64 : (N <= 32 ? 128 : 256);  // scores and products of two tiles: 4 N, a power of two
   static constexpr uint32_t kLayout = D == 128 ? 2 : 4;
+  static constexpr int kGrain = RW % 8 == 0 ? 8 : 4;  // weights stored at a time, in bytes
+  static_assert(RW % 4 == 0 && N % 16 == 0, "weights four at a time, products 16 columns at a time");
 
+  // One item, as the query warps hand it to the others.
+  struct Item {
+    int b, first, n, ctx, rows, end, r0, h, t0, t1, whole;
+  };
   struct Small {
-    float smax[2][W][4][RW];
-    float e[W * 4][RW];     // of each warp: what the tile's scores are shifted by
-    float f[2][W * 4][RW];  // and the tiles' factors
-    float red[W * 4];
-    int nan[2];
+    Item item[2];
+    alignas(16) float smax[2][W][4][RW];  // of two tiles: each warp's largest exponents
+    alignas(16) float e[W * 4][RW];       // of each warp: what the tile's scores are shifted by, 8 - E
+    alignas(16) float f[W * 4][4][RW];    // and the factors 2^(E - ref) of the last four tiles
+    float sums[2][W][4][RW];
+    float inv[W * 4][RW];
+    float red[2];
+    int nan[2], eq[2];
     int kexp[kMetaRing][kMaxPages], vexp[kMetaRing][kMaxPages];
-    alignas(8) uint64_t full[12], empty[12], s_full[2], p_ready, o_full, q_ready, drain;
+    alignas(8) uint64_t full[12], empty[12], s_full[2], p_ready[2], o_full[2], q_ready[2], q_free[2], drain;
     uint32_t tmem;
     int gave_up;
     int tmp[36];
   };
   static constexpr int kBudget = kCtas == 2 ? 115712 : 231424;
-  static constexpr int kFixed = 1024 + kQ + kP + static_cast<int>(sizeof(Small));
+  static constexpr int kFixed = 1024 + 2 * kQ + 2 * kP + static_cast<int>(sizeof(Small));
   static constexpr int kFit = (kBudget - kFixed) / kSlot;
   static constexpr int kRing = kFit > 12 ? 12 : kFit;
   static constexpr int kSmem = kFixed + kRing * kSlot;
   static_assert(kRing >= 3, "ring of tile slots");
+  static_assert(N * D + kRing * kSlot >= kTile * D, "128 query rows are read, whatever lies behind them");
   static_assert(kMetaRing >= (kRing + 1) / 2 + 1, "meta entries live as long as a tile's slots");
 };
 
@@ -319,16 +332,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
                          const __grid_constant__ CUtensorMap vmap) {
   extern __shared__ uint8_t dyn[];
   constexpr int D = C::D, N = C::N, RW = C::RW, NS = C::kRing;
-  constexpr int HC = 16, HN = RW / HC;         // columns read from tensor memory at a time
-  constexpr int RG = (RW + 31) / 32, RL = RW < 32 ? RW : 32;  // rows as lanes: groups, lanes used
   constexpr int GR = C::kGrain;
-  uint8_t* base = dyn + ((1024u - (smem_addr(dyn) & 1023u)) & 1023u);
-  uint8_t* ring = base;
+  uint8_t* q_smem = dyn + ((1024u - (smem_addr(dyn) & 1023u)) & 1023u);
+  uint8_t* ring = q_smem + 2 * C::kQ;
   uint8_t* p_smem = ring + NS * C::kSlot;
-  uint8_t* q_smem = p_smem + C::kP;
-  typename C::Small& sm = *reinterpret_cast<typename C::Small*>(q_smem + C::kQ);
+  typename C::Small& sm = *reinterpret_cast<typename C::Small*>(p_smem + 2 * C::kP);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kLoadWarp = C::W * 4, kMmaWarp = C::W * 4 + 1;
+  constexpr int kQueryWarp = C::W * 4, kLoadWarp = kQueryWarp + C::EW, kMmaWarp = kLoadWarp + 1;
+  constexpr uint32_t kO = 2 * N;  // tensor memory: scores at 0 and N, then products
   volatile int* gave_up = &sm.gave_up;
 
   if (tid == 0) {
@@ -336,11 +347,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       bar_init(smem_addr(&sm.full[i]), 1);
       bar_init(smem_addr(&sm.empty[i]), 1);
     }
-    bar_init(smem_addr(&sm.s_full[0]), 1);
-    bar_init(smem_addr(&sm.s_full[1]), 1);
-    bar_init(smem_addr(&sm.p_ready), C::W * 4);
-    bar_init(smem_addr(&sm.o_full), 1);
-    bar_init(smem_addr(&sm.q_ready), C::W * 4);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(smem_addr(&sm.s_full[i]), 1);
+      bar_init(smem_addr(&sm.p_ready[i]), C::W * 4);
+      bar_init(smem_addr(&sm.o_full[i]), 1);
+      bar_init(smem_addr(&sm.q_ready[i]), C::EW);
+      bar_init(smem_addr(&sm.q_free[i]), C::W * 4);
+    }
     bar_init(smem_addr(&sm.drain), 1);
     fence_bar_init();
     sm.gave_up = 0;
@@ -386,11 +399,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
                   my_ve = __shfl_sync(0xffffffffu, ve, from);
         const bool mine = lane < ppt && my_id >= 0;
         const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine)) * bs * D);
-        int at[3];
-        at[0] = 0;
-        at[1] = it.h;
-        at[2] = my_id;
-        const int x1 = at[a.order & 3], x2 = at[(a.order >> 2) & 3], x3 = at[(a.order >> 4) & 3];
+        auto at = [&](int name) { return name == 0 ? 0 : (name == 1 ? it.h : my_id); };
+        const int x1 = at(a.order & 3), x2 = at((a.order >> 2) & 3), x3 = at((a.order >> 4) & 3);
 #pragma unroll
         for (int part = 0; part < 2; ++part, ++fill) {
           const uint32_t slot = fill % NS, bar = smem_addr(&sm.full[slot]);
@@ -417,13 +427,16 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         }
   } else if (work && warp == kMmaWarp) {
     // ---- products: the warp waits together, one lane issues
-    Walk<N> it(a, start, hi - lo);
-    int i = 0, seg = 0;
     constexpr uint32_t kStride = 8 * D;
-    const uint32_t ring_at = smem_addr(ring), q_at = smem_addr(q_smem), p_at = smem_addr(p_smem);
-    do {
-      const uint32_t cols = uniform(C::W * C::group_rows(it.r.rows));
-      const uint32_t id_s = instr_desc(kTile, cols, false), id_o = instr_desc(kTile, cols, true);
+    const uint32_t ring_at = smem_addr(ring), p_at = smem_addr(p_smem);
+    for (int i = 0, seg = 0;; ++seg) {
+      bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 1]), (seg >> 1) & 1, gave_up);
+      ok = __all_sync(0xffffffffu, ok);
+      const int t0 = uniform(sm.item[seg & 1].t0), t1 = uniform(sm.item[seg & 1].t1);
+      if (!ok || t1 <= t0) break;
+      fence_after();
+      const uint32_t q_at = uniform(smem_addr(q_smem) + (seg & 1) * C::kQ);
+      constexpr uint32_t id_s = instr_desc(kTile, N, false), id_o = instr_desc(kTile, N, true);
       auto scores = [&](int j) {  // S[j & 1] = K tile x Q^T
         const uint32_t slot = uniform((2u * j) % NS), to = uniform(tmem + (j & 1) * N);
         bool ok = bar_wait(smem_addr(&sm.full[slot]), ((2u * j) / NS) & 1, gave_up);
@@ -443,15 +456,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         }
         __syncwarp();
       };
-      bool ok = bar_wait(smem_addr(&sm.q_ready), seg & 1, gave_up);
-      ok = __all_sync(0xffffffffu, ok);
-      fence_after();
-      if (ok) scores(i);
-      for (int t = it.t0; t < it.t1; ++t, ++i) {
-        if (t + 1 < it.t1) scores(i + 1);
-        const uint32_t slot = uniform((2u * i + 1) % NS);
+      scores(i);
+      for (int t = t0; t < t1; ++t, ++i) {
+        if (t + 1 < t1) scores(i + 1);
+        const uint32_t slot = uniform((2u * i + 1) % NS), to = uniform(tmem + kO + (i & 1) * N),
+                       p_now = uniform(p_at + (i & 1) * C::kP);
         ok = bar_wait(smem_addr(&sm.full[slot]), ((2u * i + 1) / NS) & 1, gave_up) &&
-             bar_wait(smem_addr(&sm.p_ready), i & 1, gave_up);
+             bar_wait(smem_addr(&sm.p_ready[i & 1]), (i >> 1) & 1, gave_up);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         fence_after();
@@ -461,273 +472,279 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
           for (int u = 0; u < C::TERMS; ++u) {
             constexpr uint32_t kPanel = kTile * 128;
-            const uint64_t pd = smem_desc(p_at + (u * N / 128) * kPanel + u * N % 128, 1024, 1024, 2);
+            const uint64_t pd = smem_desc(p_now + (u * C::kTerm / 128) * kPanel + u * C::kTerm % 128, 1024, 1024, 2);
 #pragma unroll
             for (int k = 0; k < kTile / 32; ++k)
-              mma_f8(tmem + 2 * N, vd + (k * 32 * D >> 4), pd + (k * 4096 >> 4), id_o, u > 0 || k > 0);
+              mma_f8(to, vd + (k * 32 * D >> 4), pd + (k * 4096 >> 4), id_o, u > 0 || k > 0);
           }
           commit(smem_addr(&sm.empty[slot]));
-          commit(smem_addr(&sm.o_full));
+          commit(smem_addr(&sm.o_full[i & 1]));
         }
         __syncwarp();
       }
-      ++seg;
-    } while (it.next(a));
+    }
     if (*gave_up) {  // products that are still running write this block's tensor memory
       if (elect()) commit(smem_addr(&sm.drain));
       for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.drain), 0); ++k) {
       }
     }
     __syncwarp();
-  } else if (work && warp < kLoadWarp) {
-    // ---- softmax: a thread owns a slot of the tile and a dimension of the result
-    const int wg = uniform(warp >> 2), quarter = uniform(warp & 3);
-    const int own = quarter * 32 + lane;  // slot in the tile; dimension (mod D)
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  } else if (work && warp >= kQueryWarp && warp < kLoadWarp) {
+    // ---- the items' queries, one item ahead: a thread owns a row
+    const int own = tid - kQueryWarp * 32, quarter = warp - kQueryWarp;
     Walk<N> it(a, start, hi - lo);
-
-    // Queries of an item into shared memory, as e4m3 terms of q / 2^eq.
-    auto load_q = [&](const Walk<N>& w, int item) -> int {
-      const int nrw = C::group_rows(w.r.rows);
-      const int chunks = C::W * nrw * (D / 8);
-      const int64_t r0 = static_cast<int64_t>(w.r.rt) * N;
-      const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (a.qst * 2) | (a.qsh * 2)) & 15) == 0;
-      auto chunk = [&](int c, float* x) {
-        const int row = c / (D / 8), d = (c % (D / 8)) * 8;
-        if (row >= w.r.rows) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = 0.f;
-          return;
-        }
-        const int64_t r = r0 + row;
-        const int64_t tok = r / a.group;
-        const int head = w.h * a.group + static_cast<int>(r - tok * a.group);
-        const QT* q = static_cast<const QT*>(a.q) + (w.r.first + tok) * a.qst + head * a.qsh + d;
+    const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (a.qst * 2) | (a.qsh * 2)) & 15) == 0;
+    int seg = 0;
+    do {
+      const RowTile r = it.r;
+      const int r0 = r.rt * N;
+      // the buffer's last item is behind every softmax warp
+      if (seg > 1) bar_wait(smem_addr(&sm.q_free[seg & 1]), ((seg >> 1) - 1) & 1, gave_up);
+      const int token = min(r.n - 1, static_cast<int>(static_cast<uint32_t>(r0 + own) / static_cast<uint32_t>(a.group)));
+      // queries into shared memory, as e4m3 terms of q / 2^eq
+      const QT* q = static_cast<const QT*>(a.q) + (r.first + static_cast<int64_t>(token)) * a.qst +
+                    (it.h * a.group + max(0, min(a.group - 1, r0 + own - token * a.group))) * a.qsh;
+      auto chunk = [&](int d, float* x) {
         if (vec) {
-          const uint4 u = *reinterpret_cast<const uint4*>(q);
+          const uint4 u = *reinterpret_cast<const uint4*>(q + d);
           const QT* e = reinterpret_cast<const QT*>(&u);
 #pragma unroll
           for (int k = 0; k < 8; ++k) x[k] = to_f(e[k]);
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = to_f(q[k]);
+          for (int k = 0; k < 8; ++k) x[k] = to_f(q[d + k]);
         }
       };
       float amax = 0.f;
-      for (int c = tid; c < chunks; c += C::kCompute) {
-        float x[8];
-        chunk(c, x);
+      if (own < r.rows) {
+#pragma unroll 8
+        for (int d = 0; d < D; d += 8) {
+          float x[8];
+          chunk(d, x);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (fabsf(x[k]) < -kNegInf) amax = fmaxf(amax, fabsf(x[k]));
+          for (int k = 0; k < 8; ++k)
+            if (fabsf(x[k]) < -kNegInf) amax = fmaxf(amax, fabsf(x[k]));
+        }
       }
       amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-      if (lane == 0) sm.red[warp] = amax;
-      if (tid == 0) sm.nan[item & 1] = 0;
-      named_sync(8, C::kCompute);
-      amax = 0.f;
-#pragma unroll
-      for (int k = 0; k < C::W * 4; ++k) amax = fmaxf(amax, sm.red[k]);
+      if (C::EW > 1) {
+        named_sync(2, C::EW * 32);  // the last item's maxima have been read
+        if (lane == 0) sm.red[quarter] = amax;
+        named_sync(2, C::EW * 32);
+        amax = fmaxf(sm.red[0], sm.red[1]);
+      }
       const int eq = kv8_need(amax, -120, 120);
       const float down = pow2i(-eq);
-      for (int c = tid; c < chunks; c += C::kCompute) {
-        float x[8];
-        chunk(c, x);
+      uint8_t* q_to = q_smem + (seg & 1) * C::kQ;
+      if (own < N) {
+#pragma unroll 4
+        for (int d = 0; d < D; d += 8) {
+          float x[8];
+          if (own < r.rows) {
+            chunk(d, x);
+          } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] *= down;
-        uint2 codes[C::TERMS];
-        split8<C::TERMS>(x, codes);
-        const uint32_t o = swz<D>(c / (D / 8), (c % (D / 8)) * 8);
+            for (int k = 0; k < 8; ++k) x[k] = 0.f;
+          }
 #pragma unroll
-        for (int t = 0; t < C::TERMS; ++t) *reinterpret_cast<uint2*>(q_smem + t * N * D + o) = codes[t];
+          for (int k = 0; k < 8; ++k) x[k] *= down;
+          uint2 codes[C::TERMS];
+          split8<C::TERMS>(x, codes);
+          const uint32_t o = swz<D>(own, d);
+#pragma unroll
+          for (int t = 0; t < C::TERMS; ++t) *reinterpret_cast<uint2*>(q_to + t * N * D + o) = codes[t];
+        }
+      }
+      if (own == 0) {
+        sm.nan[seg & 1] = 0;
+        sm.eq[seg & 1] = eq;
+        sm.item[seg & 1] = {r.b, r.first, r.n, r.ctx, r.rows, r.end, r0, it.h, it.t0, it.t1, it.t0 == 0 && it.t1 == r.tiles};
       }
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) bar_arrive(smem_addr(&sm.q_ready));
-      return eq;
-    };
-
+      if (lane == 0) bar_arrive(smem_addr(&sm.q_ready[seg & 1]));
+      ++seg;
+    } while (it.next(a));
+    if (seg > 1) bar_wait(smem_addr(&sm.q_free[seg & 1]), ((seg >> 1) - 1) & 1, gave_up);
+    if (own == 0) sm.item[seg & 1].t0 = sm.item[seg & 1].t1 = 0;  // no further item
+    __syncwarp();
+    if (lane == 0) bar_arrive(smem_addr(&sm.q_ready[seg & 1]));
+  } else if (work && warp < kQueryWarp) {
+    // ---- weights and sums: a thread owns a slot of the tile and a dimension of the result
+    const int wg = uniform(warp >> 2), quarter = uniform(warp & 3);
+    const int own = quarter * 32 + lane;  // slot in the tile; dimension (mod D)
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const int page = own / a.c.block;
+    const int row_base = wg * RW;  // first row of this group within the row tile
     float l[RW], o[RW];
-    float ref[RG];  // row 32 g + lane: the exponent its sums are relative to
-    int eq = load_q(it, 0);
-    int i = 0, seg = 0;  // tiles and items so far
-    bool more = true;
-    while (more) {
-      RowTile r = it.r;
-      r.ctx = uniform(r.ctx);
-      r.end = uniform(r.end);
-      r.rows = uniform(r.rows);
-      const int h = uniform(it.h), t0 = uniform(it.t0), t1 = uniform(it.t1);
-      const int nrw = uniform(C::group_rows(r.rows));
-      const int row_base = wg * nrw;  // first row of this group within the row tile
-      const int64_t r0 = static_cast<int64_t>(r.rt) * N;
-      const float scale = a.scale * pow2i(eq);
+    static_assert(RW <= 16, "a lane holds a row's reference; sums over lanes");
+    for (int i = 0, seg = 0;; ++seg) {  // tiles and items so far
+      bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 1]), (seg >> 1) & 1, gave_up);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {  // the group's other warps may be a few barriers behind
+        for (int64_t k = 0; k < 2 * (hi - lo) + 2; ++k) named_arrive(3 + wg, 128);
+        break;
+      }
+      const typename C::Item& it = sm.item[seg & 1];
+      const int t0 = uniform(it.t0), t1 = uniform(it.t1);
+      if (t1 <= t0) break;
+      const int first_masked = uniform(it.ctx / kTile);  // from this tile on not every row sees every slot
+      const float scale = a.scale * pow2i(sm.eq[seg & 1]);
+      float ref = kNegInf;  // of row lane % 16: the exponent its sums are relative to
 #pragma unroll
       for (int j = 0; j < RW; ++j) l[j] = 0.f, o[j] = 0.f;
-#pragma unroll
-      for (int g = 0; g < RG; ++g) ref[g] = kNegInf;
 
       // o += 2^(E - ref) times the product of tile number j
       auto accumulate = [&](int j) {
-        bar_wait(smem_addr(&sm.o_full), j & 1, gave_up);
+        bar_wait(smem_addr(&sm.o_full[j & 1]), (j >> 1) & 1, gave_up);
         fence_after();
-        const float* f = sm.f[j & 1][warp];
+        uint32_t x[RW];
+        tmem_ld<RW>(lanes + kO + (j & 1) * N + row_base, x);
+        const float* f = sm.f[warp][j & 3];
+        wait_ld();
 #pragma unroll
-        for (int k = 0; k < HN; ++k) {
-          if (k * HC >= nrw) break;
-          uint32_t x[HC];
-          tmem_ld<HC>(lanes + 2 * N + row_base + k * HC, x);
-          wait_ld();
-#pragma unroll
-          for (int q = 0; q < HC; q += 4) {
-            const float4 g = *reinterpret_cast<const float4*>(f + k * HC + q);
-            float* to = o + k * HC + q;
-            const float2 u = fma2(make_float2(__uint_as_float(x[q]), __uint_as_float(x[q + 1])), make_float2(g.x, g.y),
-                                  make_float2(to[0], to[1]));
-            const float2 v = fma2(make_float2(__uint_as_float(x[q + 2]), __uint_as_float(x[q + 3])), make_float2(g.z, g.w),
-                                  make_float2(to[2], to[3]));
-            to[0] = u.x, to[1] = u.y, to[2] = v.x, to[3] = v.y;
-          }
+        for (int q = 0; q < RW; q += 4) {
+          const float4 g = *reinterpret_cast<const float4*>(f + q);
+          const float2 u = fma2(make_float2(__uint_as_float(x[q]), __uint_as_float(x[q + 1])), make_float2(g.x, g.y),
+                                make_float2(o[q], o[q + 1]));
+          const float2 v = fma2(make_float2(__uint_as_float(x[q + 2]), __uint_as_float(x[q + 3])), make_float2(g.z, g.w),
+                                make_float2(o[q + 2], o[q + 3]));
+          o[q] = u.x, o[q + 1] = u.y, o[q + 2] = v.x, o[q + 3] = v.y;
         }
       };
 
       for (int t = t0; t < t1; ++t, ++i) {
-        const int slot0 = t * kTile, slot = slot0 + own, buf = i & 1;
+        const int buf = i & 1;
         bar_wait(smem_addr(&sm.s_full[buf]), (i >> 1) & 1, gave_up);
         fence_after();
-        const int page = own / a.c.block;
+        uint32_t x[RW];
+        tmem_ld<RW>(lanes + buf * N + row_base, x);
+
         const int ke = sm.kexp[i % kMetaRing][page], ve = sm.vexp[i % kMetaRing][page];
         const float cs = ke == kBadPage ? __int_as_float(0x7fffffff) : scale * pow2i(ke);
         const float ev = static_cast<float>(ve), ve_inv = pow2i(-ve);
-        const bool masked = slot0 + kTile > r.ctx;  // not every row sees every slot
-        if (masked && wg == 0) {
-          // Slots behind the sequence hold no values, and a NaN value must not reach the rows that do not see it
-          // through a weight of 0: both are cleared here, and the rows that see a NaN get it at the item's end.
-          const uint32_t vslot = (2u * i + 1) % NS;
-          bar_wait(smem_addr(&sm.full[vslot]), ((2u * i + 1) / NS) & 1, gave_up);
-          uint4* vrow = reinterpret_cast<uint4*>(ring + vslot * C::kSlot + own * D);
-          bool nan = false;
-#pragma unroll 1
-          for (int k = 0; k < D / 16; ++k) {
-            uint4 u = vrow[k];
-            uint32_t any = 0;
-            uint32_t* w = &u.x;
+        const bool masked = t >= first_masked;
+        uint32_t vis = 0xffffffffu;
+        if (masked) {
+          const int slot = t * kTile + own;
+          if (wg == 0) {
+            // Slots behind the sequence hold no values, and a NaN value must not reach the rows that do not see it
+            // through a weight of 0: both are cleared here, and the rows that see a NaN get it at the item's end.
+            const uint32_t vslot = (2u * i + 1) % NS;
+            bar_wait(smem_addr(&sm.full[vslot]), ((2u * i + 1) / NS) & 1, gave_up);
+            uint4* vrow = reinterpret_cast<uint4*>(ring + vslot * C::kSlot + own * D);
+            bool nan = false;
+#pragma unroll 2
+            for (int k = 0; k < D / 16; ++k) {
+              uint4 u = vrow[k];
+              uint32_t any = 0;
+              uint32_t* w = &u.x;
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              const uint32_t m = slot >= r.end ? 0xffffffffu : __vcmpeq4(w[z] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              any |= m;
-              w[z] &= ~m;
+              for (int z = 0; z < 4; ++z) {
+                const uint32_t m = slot >= it.end ? 0xffffffffu : __vcmpeq4(w[z] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                any |= m;
+                w[z] &= ~m;
+              }
+              if (any) vrow[k] = u;
+              nan |= any != 0;
             }
-            if (any) vrow[k] = u;
-            nan |= any != 0;
+            if (nan && slot < it.end) sm.nan[seg & 1] = 1;
           }
-          if (nan && slot < r.end) sm.nan[seg & 1] = 1;
-        }
-
-        // the tile's largest exponent of each row
-        float y[HC], mine = kNegInf;
-        uint32_t vis[HN];
-        auto scores = [&](int k) {
-          uint32_t x[HC];
-          tmem_ld<HC>(lanes + buf * N + row_base + k * HC, x);
-          wait_ld();
-#pragma unroll
-          for (int j = 0; j < HC; j += 2) {
-            const float2 z = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), make_float2(cs, cs),
-                                  make_float2(ev, ev));
-            y[j] = z.x;
-            y[j + 1] = z.y;
-          }
-          if (masked) {
-#pragma unroll
-            for (int j = 0; j < HC; ++j)
-              if (!((vis[k] >> j) & 1)) y[j] = kNegInf;
-          }
-        };
-#pragma unroll
-        for (int k = 0; k < HN; ++k) {
-          if (k * HC >= nrw) break;
-          vis[k] = 0xffffffffu;
-          if (masked && slot >= r.ctx) {
-            const int64_t row = r0 + row_base + k * HC;  // of the step
-            const int j = slot - r.ctx;
-            if (slot >= r.end) {
-              vis[k] = 0;
+          if (slot >= it.ctx) {
+            const int row = it.r0 + row_base, j = slot - it.ctx;  // row and token of the step
+            if (slot >= it.end) {
+              vis = 0;
             } else if (!a.tree) {
               const int64_t first = static_cast<int64_t>(j) * a.group - row;
-              vis[k] = first <= 0 ? 0xffffffffu : (first >= HC ? 0u : 0xffffffffu << first);
+              vis = first <= 0 ? 0xffffffffu : (first >= RW ? 0u : 0xffffffffu << first);
             } else {
               uint32_t bits = 0;
-              int token = static_cast<int>(row / a.group), sub = static_cast<int>(row - static_cast<int64_t>(token) * a.group);
-              bool on = token < r.n && sees(a, r.b, token, j);
-              for (int q = 0; q < HC; ++q) {
-                if (on) bits |= 1u << q;
-                if (++sub == a.group) {
-                  sub = 0;
-                  ++token;
-                  on = token < r.n && sees(a, r.b, token, j);
-                }
+              int token = row / a.group, sub = row - token * a.group;
+              for (int q = 0; q < RW;) {  // the rows of one token see the same
+                const bool on = token < it.n && sees(a, it.b, token, j);
+                const int many = min(RW - q, a.group - sub);
+                if (on) bits |= ((1u << many) - 1u) << q;
+                q += many;
+                sub = 0;
+                ++token;
               }
-              vis[k] = bits;
+              vis = bits;
             }
           }
-          scores(k);
-          if ((k & 1) == 0) mine = kNegInf;
-#pragma unroll
-          for (int jg = 0; jg < HC; jg += GR) {
-            if (k * HC + jg >= nrw) break;
-            float m[GR];
-#pragma unroll
-            for (int j = 0; j < GR; ++j) m[j] = warp_max(y[jg + j]);
-#pragma unroll
-            for (int j = 0; j < GR; ++j)
-              if (lane == (k & 1) * HC + jg + j) mine = m[j];
-          }
-          if ((k & 1) == 1 || k == HN - 1 || (k + 1) * HC >= nrw) {
-            if (RL == 32 || lane < RL) sm.smax[buf][wg][quarter][(k / 2) * 32 + lane] = mine;
-          }
         }
-        named_sync(1 + wg, 128);
-        if (t > t0) accumulate(i - 1);
+        wait_ld();
+
+        // each row's largest exponent: over the lanes, then over the four warps
+        float y[RW];
 #pragma unroll
-        for (int g = 0; g < RG; ++g) {
-          if (g * 32 >= nrw) break;
-          const int row = g * 32 + lane % RL;
+        for (int j = 0; j < RW; j += 2) {
+          const float2 z = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), make_float2(cs, cs),
+                                make_float2(ev, ev));
+          y[j] = z.x;
+          y[j + 1] = z.y;
+        }
+        if (masked) {
+#pragma unroll
+          for (int j = 0; j < RW; ++j)
+            if (!((vis >> j) & 1)) y[j] = kNegInf;
+        }
+        float mine = kNegInf;
+#pragma unroll
+        for (int jg = 0; jg < RW; jg += GR) {
+          float m[GR];
+#pragma unroll
+          for (int j = 0; j < GR; ++j) m[j] = warp_max(y[jg + j]);
+#pragma unroll
+          for (int j = 0; j < GR; ++j)
+            if (lane == jg + j) mine = m[j];
+        }
+        if (lane < RW) sm.smax[buf][wg][quarter][lane] = mine;
+        named_sync(3 + wg, 128);
+        {
+          const int row = lane % RW;
           const float m = fmaxf(fmaxf(sm.smax[buf][wg][0][row], sm.smax[buf][wg][1][row]),
                                 fmaxf(sm.smax[buf][wg][2][row], sm.smax[buf][wg][3][row]));
           const bool none = m == kNegInf;
           const float e = none ? 0.f : ceilf(m);
-          const bool far = !none && e - ref[g] > 60.f;
+          if (t == t0 && !none) ref = e;
+          const bool far = !none && e - ref > 60.f;
           if (__any_sync(0xffffffffu, far)) {
-            const float by = far ? exp2_whole(ref[g] - e) : 1.f;
-            if (far) ref[g] = e;
+            const float by = far ? exp2_whole(ref - e) : 1.f;
+            if (far) ref = e;
+            if (lane < RW) sm.f[warp][(i - 1) & 3][row] *= by;  // the product still to come is relative to the old one
 #pragma unroll
-            for (int j = 0; j < RL; ++j) {
+            for (int j = 0; j < RW; ++j) {
               const float b = __shfl_sync(0xffffffffu, by, j);
-              l[g * 32 + j] *= b;
-              o[g * 32 + j] *= b;
+              l[j] *= b;
+              o[j] *= b;
             }
           }
-          sm.e[warp][row] = 8.f - e;
-          sm.f[buf][warp][row] = none ? 0.f : exp2_whole(e - ref[g]);
+          if (lane < RW) {
+            sm.e[warp][row] = 8.f - e;
+            sm.f[warp][i & 3][row] = none ? 0.f : exp2_whole(e - ref);
+          }
         }
         __syncwarp();
 
         // weights, as e4m3 terms, and their sums
+        uint32_t turn = static_cast<uint32_t>(own & 7) << 4;  // the swizzle of this slot's row of weights
+        asm volatile("" : "+r"(turn));                      // its addresses are not kept over the loop
+        uint8_t* p_to = p_smem + buf * C::kP + own * 128;
+        const float* e_at = sm.e[warp];
+        const float* f_at = sm.f[warp][i & 3];
 #pragma unroll
-        for (int k = 0; k < HN; ++k) {
-          if (k * HC >= nrw) break;
-          scores(k);
+        for (int jg = 0; jg < RW; jg += GR) {
+          uint32_t code[C::TERMS][GR / 4];
 #pragma unroll
-          for (int jg = 0; jg < HC; jg += GR) {
-            if (k * HC + jg >= nrw) break;
-            uint32_t code[C::TERMS][GR / 4];
+          for (int j4 = 0; j4 < GR; j4 += 4) {
+            const float4 e4 = *reinterpret_cast<const float4*>(e_at + jg + j4);
+            const float4 f4 = *reinterpret_cast<const float4*>(f_at + jg + j4);
 #pragma unroll
-            for (int j = 0; j < GR; j += 2) {
-              const int q = k * HC + jg + j;
-              const float2 e = *reinterpret_cast<const float2*>(&sm.e[warp][q]);
-              const float2 f = *reinterpret_cast<const float2*>(&sm.f[buf][warp][q]);
-              const float2 z = add2(make_float2(y[jg + j], y[jg + j + 1]), e);
+            for (int j = 0; j < 4; j += 2) {
+              const int q = jg + j4 + j;
+              const float2 e = j == 0 ? make_float2(e4.x, e4.y) : make_float2(e4.z, e4.w);
+              const float2 f = j == 0 ? make_float2(f4.x, f4.y) : make_float2(f4.z, f4.w);
+              const float2 z = add2(make_float2(y[q], y[q + 1]), e);
               const float w0 = ex2_fast(z.x), w1 = ex2_fast(z.y);
               const float2 s = fma2(make_float2(w0, w1), mul2(f, make_float2(ve_inv, ve_inv)), make_float2(l[q], l[q + 1]));
               l[q] = s.x;
@@ -744,75 +761,72 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
                   asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(rest) : "r"(back));
                   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(rest));
                 }
-                if (j % 4 == 0) code[u][j / 4] = c;
-                else code[u][j / 4] |= static_cast<uint32_t>(c) << 16;
+                if (j == 0) code[u][j4 / 4] = c;
+                else code[u][j4 / 4] |= static_cast<uint32_t>(c) << 16;
               }
             }
+          }
 #pragma unroll
-            for (int u = 0; u < C::TERMS; ++u) {
-              const int col = u * N + row_base + k * HC + jg;
-              uint8_t* to = p_smem + (col / 128) * (kTile * 128) + swz<128>(own, col % 128);
-              if (GR == 8) *reinterpret_cast<uint2*>(to) = make_uint2(code[u][0], code[u][GR / 4 - 1]);
-              else *reinterpret_cast<uint32_t*>(to) = code[u][0];
-            }
+          for (int u = 0; u < C::TERMS; ++u) {
+            const int col = u * C::kTerm + row_base + jg;
+            uint8_t* to = p_to + (col / 128) * (kTile * 128) + ((col % 128) ^ turn);
+            if (GR == 8) *reinterpret_cast<uint2*>(to) = make_uint2(code[u][0], code[u][GR / 4 - 1]);
+            else *reinterpret_cast<uint32_t*>(to) = code[u][0];
           }
         }
         fence_async_shared();
         fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(smem_addr(&sm.p_ready));
+        if (lane == 0) bar_arrive(smem_addr(&sm.p_ready[buf]));
+        if (t > t0) accumulate(i - 1);
       }
-
-      more = it.next(a);
-      if (more) eq = load_q(it, seg + 1);  // the products that read the last queries are done
       accumulate(i - 1);
       if (sm.nan[seg & 1]) {  // set before the weights of its tile were ready
-        for (int slot = max(t0, r.ctx / kTile) * kTile; slot < min(r.end, t1 * kTile); ++slot) {
-          const int id = a.c.table[static_cast<int64_t>(r.b) * a.c.max_blocks + slot / a.c.block];
+        for (int slot = max(t0, it.ctx / kTile) * kTile; slot < min(it.end, t1 * kTile); ++slot) {
+          const int id = a.c.table[static_cast<int64_t>(it.b) * a.c.max_blocks + slot / a.c.block];
           if (id < 0 || id >= a.c.num_blocks) continue;
-          const uint8_t code = a.c.v[id * a.c.sb + h * a.c.sh + (slot % a.c.block) * a.c.ss + own % D];
+          const uint8_t code = a.c.v[id * a.c.sb + it.h * a.c.sh + (slot % a.c.block) * a.c.ss + own % D];
           if ((code & 0x7f) != 0x7f) continue;
 #pragma unroll
           for (int j = 0; j < RW; ++j)
-            if (slot < r.ctx || sees(a, r.b, min(r.n - 1, static_cast<int>((r0 + row_base + j) / a.group)), slot - r.ctx))
+            if (slot < it.ctx || sees(a, it.b, min(it.n - 1, (it.r0 + row_base + j) / a.group), slot - it.ctx))
               o[j] = __int_as_float(0x7fffffff);
         }
       }
-      ++seg;
 
       // ---- the item's results, or its share of them
-      const bool whole = t0 == 0 && t1 == r.tiles;
+      const bool whole = it.whole;
       const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (t0 > 0 ? 0 : 1);
-      auto& sums = sm.smax[(i - 1) & 1];  // every warp is past the last tile's maxima, and the next tile's go elsewhere
+      {
+        float v[16];
 #pragma unroll
-      for (int g = 0; g < RG; ++g) {
-        if (g * 32 >= nrw) break;
-        const float s = lane_sums<RL>(l + g * 32, lane);
-        if (RL == 32 || lane < RL) sums[wg][quarter][g * 32 + lane] = s;
-      }
-      named_sync(1 + wg, 128);
-#pragma unroll
-      for (int g = 0; g < RG; ++g) {
-        if (g * 32 >= nrw) break;
-        const int row = g * 32 + lane % RL;
-        const float s = (sums[wg][0][row] + sums[wg][1][row]) + (sums[wg][2][row] + sums[wg][3][row]);
-        if (whole) sm.e[warp][row] = s == 0.f ? 0.f : 1.f / s;
-        else if (quarter == 0 && lane < RL && row < nrw && row_base + row < r.rows)
-          a.part_ml[part * N + row_base + row] = make_float2(ref[g], s);
+        for (int j = 0; j < 16; ++j) v[j] = j < RW ? l[j < RW ? j : 0] : 0.f;
+        float s = lane_sums<16>(v, lane);
+        auto& sums = sm.sums[seg & 1];
+        if (lane < RW) sums[wg][quarter][lane] = s;
+        named_sync(3 + wg, 128);
+        const int row = lane % RW;
+        s = (sums[wg][0][row] + sums[wg][1][row]) + (sums[wg][2][row] + sums[wg][3][row]);
+        if (whole) sm.inv[warp][row] = s == 0.f ? 0.f : 1.f / s;
+        else if (quarter == 0 && lane < RW && row_base + row < it.rows)
+          a.part_ml[part * N + row_base + row] = make_float2(ref, s);
       }
       __syncwarp();
       if (own < D) {
-        int64_t tok = (r0 + row_base) / a.group;
-        int sub = static_cast<int>(r0 + row_base - tok * a.group);
+        int tok = (it.r0 + row_base) / a.group;
+        int sub = it.r0 + row_base - tok * a.group;
         QT* out = static_cast<QT*>(a.out) + own;
 #pragma unroll
         for (int j = 0; j < RW; ++j) {
-          if (j >= nrw || row_base + j >= r.rows) break;
-          if (whole) out[(r.first + tok) * a.ost + (h * a.group + sub) * a.osh] = from_f<QT>(o[j] * sm.e[warp][j]);
+          if (row_base + j >= it.rows) continue;
+          if (whole)
+            out[(it.first + static_cast<int64_t>(tok)) * a.ost + (it.h * a.group + sub) * a.osh] = from_f<QT>(o[j] * sm.inv[warp][j]);
           else a.part_o[(part * N + row_base + j) * D + own] = o[j];
           if (++sub == a.group) sub = 0, ++tok;
         }
       }
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_addr(&sm.q_free[seg & 1]));
     }
   }
 
@@ -915,9 +929,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
 
 constexpr int kSms = 152;
 
-template <typename QT, int D, int RW, int W, int TERMS>
+template <typename QT, int D, int RW, int W, int TERMS, int CTAS>
 cudaError_t launch_attention(const Kv8AttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t st) {
-  using C = Cfg<D, RW, W, TERMS>;
+  using C = Cfg<D, RW, W, TERMS, CTAS>;
   auto kernel = kv8_attention_kernel<QT, C>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
@@ -942,17 +956,17 @@ cudaError_t launch_attention(const Kv8AttnArgs& a, const CUtensorMap& k, const C
 
 template <typename QT, int D, int TERMS>
 cudaError_t launch_rows(const Kv8AttnArgs& a, int rows, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t st) {
-  if (rows == 16) return launch_attention<QT, D, 16, 1, TERMS>(a, k, v, st);
-  if (rows == 32) return launch_attention<QT, D, 16, 2, TERMS>(a, k, v, st);
-  if (rows == 64) return launch_attention<QT, D, 16, 4, TERMS>(a, k, v, st);
-  return launch_attention<QT, D, 32, 4, TERMS>(a, k, v, st);
+  if (rows == 16) return launch_attention<QT, D, 16, 1, TERMS, 2>(a, k, v, st);
+  if (rows == 32) return launch_attention<QT, D, 16, 2, TERMS, 1>(a, k, v, st);
+  if (rows == 48) return launch_attention<QT, D, 12, 4, TERMS, 1>(a, k, v, st);
+  return launch_attention<QT, D, 16, 4, TERMS, 1>(a, k, v, st);
 }
 
 }  // namespace
 
-int kv8_attention_rows(int64_t max_rows) { return max_rows <= 16 ? 16 : (max_rows <= 32 ? 32 : (max_rows <= 64 ? 64 : 128)); }
+int kv8_attention_rows(int64_t max_rows) { return max_rows <= 16 ? 16 : (max_rows <= 32 ? 32 : (max_rows <= 48 ? 48 : 64)); }
 
-int kv8_attention_parts(int rows) { return rows <= 32 ? 2 * kSms : kSms; }
+int kv8_attention_parts(int rows) { return rows <= 16 ? 2 * kSms : kSms; }
 
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, int dtype, int rows, const CUtensorMap& k, const CUtensorMap& v,
                                  cudaStream_t st) {

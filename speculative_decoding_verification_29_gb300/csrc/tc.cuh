@@ -32,22 +32,28 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
+// The same, the thread suspended until the phase ends or some 20 us have passed.
+__device__ __forceinline__ bool bar_try_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
 }
-constexpr uint64_t kWaitNs = 2000000000ull;  // a wait gives up after two seconds
+constexpr int kWaitTries = 100000;  // a wait gives up after these: about two seconds
 
 // Waits for the barrier's phase; false, with *gave_up set, when the limit ran
 // out. Once a wait of the block has given up no other waits: every role then
 // runs through its loop without touching the tensor core or starting copies.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
   if (bar_try(bar, parity)) return true;
-  const uint64_t t0 = now_ns();
-  while (!bar_try(bar, parity)) {
+  for (int i = 0; !bar_try_long(bar, parity); ++i) {
     if (*gave_up) return false;
-    if (now_ns() - t0 > kWaitNs) {
+    if (i == kWaitTries) {
       *gave_up = 1;
       return false;
     }
@@ -57,6 +63,9 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void fence_bar_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
@@ -119,7 +128,7 @@ __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// 8, 16 or 32 columns of the warp's 32 lanes (call wait_ld before use).
+// 8, 12, 16 or 32 columns of the warp's 32 lanes (call wait_ld before use).
 template <int C>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t* r);
 template <>
@@ -127,6 +136,15 @@ __device__ __forceinline__ void tmem_ld<8>(uint32_t addr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(addr));
+}
+template <>
+__device__ __forceinline__ void tmem_ld<12>(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11])
+               : "r"(addr + 8));
 }
 template <>
 __device__ __forceinline__ void tmem_ld<16>(uint32_t addr, uint32_t* r) {
