@@ -34,5 +34,6 @@ def __getattr__(name):
     if name in __all__:
         from . import api
 
-        return getattr(api, name)
+        value = globals()[name] = getattr(api, name)  # found directly from the next use on
+        return value
     raise AttributeError(name)

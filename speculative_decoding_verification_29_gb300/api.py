@@ -10,6 +10,7 @@ buffers uses.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 from typing import Dict, Optional
@@ -385,27 +386,30 @@ def spec_kv_compact(kv: torch.Tensor, base_pos, accept_len, path=None, out: Opti
 _KV8_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
 
 
-def _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len):
-    """The C record of one layer's cache, checked; the tensors stay the caller's."""
+def _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, planes: bool = False):
+    """The C record of a cache and its tensors' device, checked; the tensors stay the caller's. With ``planes`` the
+    codes and scales have a leading plane dimension."""
     dev = k_cache.device
-    if not k_cache.is_cuda or v_cache.device != dev:
+    shape, stride = k_cache.shape, k_cache.stride()
+    if dev.type != "cuda" or v_cache.device != dev:
         raise ValueError("k_cache and v_cache must be CUDA tensors of one device (the cache lives there)")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    if len(shape) != 4 + planes or v_cache.shape != shape or v_cache.stride() != stride:
         raise ValueError("k_cache and v_cache must both be [blocks, kv_heads, block, head_dim], with the same strides")
-    if k_cache.element_size() != 1 or v_cache.element_size() != 1 or k_cache.stride(3) != 1:
+    if k_cache.element_size() != 1 or v_cache.element_size() != 1 or stride[-1] != 1:
         raise ValueError("k_cache and v_cache hold one byte per code (uint8 or float8_e4m3fn), head_dim contiguous")
-    nb, H, bs, D = k_cache.shape
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t.device != dev or t.element_size() != 1 or t.shape != (nb, H) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous [blocks, kv_heads] tensor of bytes (uint8 or float8_e8m0fnu)")
+    nb, H, bs, D = shape[-4:]
+    for t in (k_scale, v_scale):
+        if t.device != dev or t.element_size() != 1 or t.shape != shape[:-2] or t.stride()[-2:] != (H, 1):
+            raise ValueError("k_scale and v_scale must be [blocks, kv_heads] tensors of bytes (uint8 or float8_e8m0fnu), "
+                             "contiguous in each plane")
     _int32(block_table, "block_table", dev)
     _int32(cache_len, "cache_len", dev)
-    if block_table.dim() != 2 or cache_len.shape != block_table.shape[:1]:
+    B = cache_len.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B or cache_len.dim() != 1:
         raise ValueError("block_table must be [B, max_blocks] and cache_len [B]")
-    sb, sh, ss, _ = k_cache.stride()
     return _lib.Kv8Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                         block_table.data_ptr(), cache_len.data_ptr(), block_table.shape[0], nb, block_table.shape[1], bs,
-                         H, D, sb, sh, ss)
+                         block_table.data_ptr(), cache_len.data_ptr(), B, nb, block_table.shape[1], bs, H, D,
+                         stride[-4], stride[-3], stride[-2]), dev
 
 
 def _int32(t, name, dev):
@@ -414,18 +418,17 @@ def _int32(t, name, dev):
 
 
 def _kv8_rows(t, name, D, dev):
-    """A packed [T, heads, head_dim] activation; returns its token and head strides."""
-    if t.device != dev or t.dim() != 3 or t.shape[2] != D or t.stride(2) != 1:
+    """The token and head strides of a packed [T, heads, head_dim] activation."""
+    stride = t.stride()
+    if t.device != dev or len(stride) != 3 or t.shape[2] != D or stride[2] != 1:
         raise ValueError(f"{name} must be a [tokens, heads, {D}] tensor on {dev}, head_dim contiguous")
     if t.dtype not in _KV8_DTYPES:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    return t.stride(0), t.stride(1)
+    return stride[0], stride[1]
 
 
 def _used_on(stream, *tensors):
     """Tensors allocated here on the current stream but used on `stream`."""
-    if stream is None:
-        return
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     for t in tensors:
@@ -452,8 +455,7 @@ def spec_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache
     q [T, q_heads, head_dim]: queries, rotated alike into q_out (allocated when
     None; may be q). Returns row_status [B] and, with q, q_out."""
     lib = _lib.load()
-    dev = k_cache.device
-    cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len)
+    cache, dev = _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len)
     D = cache.head_dim
     kst, ksh = _kv8_rows(k, "k", D, dev)
     vst, vsh = _kv8_rows(v, "v", D, dev)
@@ -483,11 +485,14 @@ def spec_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache
             held = inv_freq.detach().to("cpu", torch.float64).contiguous()
             rot, freq = 2 * held.numel(), held.data_ptr()
         else:
-            held = (ctypes.c_double * len(inv_freq))(*inv_freq)
-            rot, freq = 2 * len(inv_freq), ctypes.addressof(held)
+            held = array.array("d", inv_freq)
+            rot, freq = 2 * len(held), held.buffer_info()[0]
     if out is None:
         out = dict(row_status=torch.empty(cache.B, dtype=torch.int32, device=dev))
-        _used_on(stream, out["row_status"], made)
+        if stream is not None:
+            _used_on(stream, out["row_status"])
+    if made is not None and stream is not None:
+        _used_on(stream, made)
     if q is not None:
         out["q_out"] = q_out
     check("spec_kv8_append", lib.spec_kv8_append(
@@ -522,8 +527,7 @@ def spec_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cache
     tokens. sm_scale: head_dim ** -0.5 when None. Returns out (like q) and
     row_status [B]."""
     lib = _lib.load()
-    dev = k_cache.device
-    cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len)
+    cache, dev = _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len)
     qst, qsh = _kv8_rows(q, "q", cache.head_dim, dev)
     if q.dtype == torch.float32:
         raise TypeError("q must be bfloat16 or float16")
@@ -536,19 +540,21 @@ def spec_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cache
                 tree_mask.shape != (cache.B, max_tokens, max_tokens):
             raise ValueError("tree_mask must be a contiguous [B, max_tokens, max_tokens] tensor of bytes")
     code = _KV8_DTYPES[q.dtype]
-    made = []
     if out is None:
-        out = dict(out=torch.empty(q.shape, dtype=q.dtype, device=dev),
-                   row_status=torch.empty(cache.B, dtype=torch.int32, device=dev))
-        made += [out["out"], out["row_status"]]
+        out = dict(out=torch.empty_like(q), row_status=torch.empty(cache.B, dtype=torch.int32, device=dev))
+        if stream is not None:
+            _used_on(stream, *out.values())
     o = out["out"]
     ost, osh = _kv8_rows(o, "out", cache.head_dim, dev)
     if o.shape != q.shape or o.dtype != q.dtype:
         raise ValueError("out must have q's shape and type")
     if workspace is None:
-        workspace = alloc_workspace(lib.spec_kv8_workspace_bytes(ctypes.byref(cache), hq, max_tokens, code), dev)
-        made.append(workspace)
-    _used_on(stream, *made)
+        nbytes = lib.spec_kv8_workspace_bytes(ctypes.byref(cache), hq, max_tokens, code)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        if workspace.data_ptr() % 256:
+            workspace = alloc_workspace(nbytes, dev)
+        if stream is not None:
+            _used_on(stream, workspace)
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(cache.head_dim)
     check("spec_kv8_attention", lib.spec_kv8_attention(
@@ -570,17 +576,11 @@ def spec_kv8_compact(k_cache, v_cache, k_scale, v_scale, block_table, cache_len,
     call. Returns new_len [B] and row_status [B]."""
     lib = _lib.load()
     planes, sp, ssp = 1, 0, 0
-    kc, vc, ks, vs = k_cache, v_cache, k_scale, v_scale
+    cache, dev = _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, k_cache.dim() == 5)
     if k_cache.dim() == 5:
-        planes = k_cache.shape[0]
-        if v_cache.shape != k_cache.shape or k_scale.shape[:1] != (planes,) or v_scale.shape[:1] != (planes,) or planes < 1:
-            raise ValueError("k_cache, v_cache, k_scale and v_scale must have the same planes")
-        sp, ssp = k_cache.stride(0), k_scale.stride(0)
-        if v_cache.stride(0) != sp or v_scale.stride(0) != ssp:
-            raise ValueError("keys and values must have the same plane strides")
-        kc, vc, ks, vs = k_cache[0], v_cache[0], k_scale[0], v_scale[0]
-    cache = _kv8_cache(kc, vc, ks, vs, block_table, cache_len)
-    dev = kc.device
+        planes, sp, ssp = k_cache.shape[0], k_cache.stride(0), k_scale.stride(0)
+        if v_scale.stride(0) != ssp:
+            raise ValueError("k_scale and v_scale must have the same plane stride")
     _int32(accept_len, "accept_len", dev)
     if accept_len.numel() != cache.B:
         raise ValueError("accept_len must have B entries")
@@ -593,7 +593,8 @@ def spec_kv8_compact(k_cache, v_cache, k_scale, v_scale, block_table, cache_len,
     if out is None:
         out = dict(new_len=torch.empty(cache.B, dtype=torch.int32, device=dev),
                    row_status=torch.empty(cache.B, dtype=torch.int32, device=dev))
-        _used_on(stream, *out.values())
+        if stream is not None:
+            _used_on(stream, *out.values())
     check("spec_kv8_compact", lib.spec_kv8_compact(ctypes.byref(cache), planes, sp, ssp, _ptr(path), D,
                                                    accept_len.data_ptr(), out["new_len"].data_ptr(),
                                                    out["row_status"].data_ptr(), _stream(stream)))
