@@ -68,7 +68,8 @@ struct Kv8AttnArgs {
   int T, q_heads, group, max_tokens;
   const int32_t* cu;
   const uint8_t* tree;  // [B][max_tokens][max_tokens] or NULL
-  float scale;          // sm_scale * log2(e)
+  float scale;          // |sm_scale| * log2(e)
+  int negate;           // sm_scale < 0: the queries change sign
   int32_t* row_status;
   int row_tiles;        // row tiles a sequence has at most
   int parts;            // thread blocks the cache is split over
@@ -83,6 +84,8 @@ int kv8_attention_rows(int64_t max_rows);
 int kv8_attention_parts(int rows);
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, int dtype, int rows, const CUtensorMap& k, const CUtensorMap& v,
                                  cudaStream_t st);
+cudaError_t launch_kv8_wide(const Kv8AttnArgs& a, int dtype, int rows, const CUtensorMap& k, const CUtensorMap& v,
+                            cudaStream_t st);
 
 // ---------------------------------------------------------------- device --
 

@@ -227,7 +227,8 @@ int spec_kv8_attention(const spec_kv8_cache* cache, const void* queries, int64_t
   a.max_tokens = max_tokens;
   a.cu = cu_tokens;
   a.tree = tree_mask;
-  a.scale = static_cast<float>(sm_scale * 1.4426950408889634);
+  a.scale = static_cast<float>(fabs(sm_scale * 1.4426950408889634));
+  a.negate = sm_scale < 0.f;
   a.row_status = row_status;
   const int64_t most = static_cast<int64_t>(std::min(max_tokens, std::max(T, 1))) * a.group;  // no sequence has more than T
   const int rows = kv8_attention_rows(static_cast<int64_t>(max_tokens) * a.group);
@@ -240,7 +241,8 @@ int spec_kv8_attention(const spec_kv8_cache* cache, const void* queries, int64_t
   a.part_o = reinterpret_cast<float*>(ws + l.o);
   CUtensorMap kmap, vmap;
   if (!pool_map(a.c, a.c.k, &kmap, &a.order) || !pool_map(a.c, a.c.v, &vmap, &a.order)) return SPEC_ERR_CUDA;
-  return cuda_status(launch_kv8_attention(a, dtype, rows, kmap, vmap, static_cast<cudaStream_t>(stream)));
+  const auto launch = rows >= 128 ? launch_kv8_wide : launch_kv8_attention;
+  return cuda_status(launch(a, dtype, rows, kmap, vmap, static_cast<cudaStream_t>(stream)));
 }
 
 int spec_kv8_compact(const spec_kv8_cache* cache, int n_planes, int64_t stride_plane, int64_t scale_stride_plane,

@@ -33,194 +33,11 @@
 // leave tensor memory together, each row's maximum crosses lanes by redux and
 // warps by shared memory, the weights are written, and the tile's product runs
 // while the next tiles are worked on.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "internal.h"
-#include "kv8.h"
-#include "tc.cuh"
+#include "kv8_attn.cuh"
 
 namespace specv {
 
 namespace {
-
-using namespace tc;
-
-constexpr int kTile = 128;
-constexpr int kMetaRing = 8;
-constexpr int kMaxPages = kTile / 16;
-constexpr int kBadPage = 1 << 20;
-constexpr float kNegInf = -__builtin_huge_valf();
-
-template <typename T>
-__device__ __forceinline__ float to_f(T v);
-template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-template <typename T>
-__device__ __forceinline__ T from_f(float v);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
-
-// -------------------------------------------------------------- schedule --
-
-// One row tile of a sequence, all KV heads alike.
-struct RowTile {
-  int b, rt;
-  int first;  // first packed token of the sequence
-  int n;      // its step tokens
-  int ctx;    // tokens in the cache before the step
-  int rows;   // rows of this tile
-  int end;    // slots that some row of it may see
-  int tiles;  // ceil(end / 128); 0: no such row tile
-};
-
-template <int N>
-__device__ __forceinline__ RowTile row_tile(const Kv8AttnArgs& a, int b, int rt) {
-  RowTile r{};
-  r.b = b;
-  r.rt = rt;
-  const int lo = a.cu[b], hi = a.cu[b + 1], len = a.c.len[b];
-  if (!kv8_seq_ok(a.c, a.T, lo, hi, len) || hi - lo > a.max_tokens) return r;
-  const int64_t rows = static_cast<int64_t>(hi - lo) * a.group, r0 = static_cast<int64_t>(rt) * N;
-  if (r0 >= rows) return r;
-  r.first = lo;
-  r.n = hi - lo;
-  r.ctx = len;
-  r.rows = static_cast<int>(min(rows - r0, static_cast<int64_t>(N)));
-  r.end = len + (a.tree ? r.n : static_cast<int>((r0 + r.rows - 1) / a.group) + 1);
-  r.tiles = (r.end + kTile - 1) / kTile;
-  return r;
-}
-
-// Where a run of tiles begins.
-struct Start {
-  int b, rt, h, t;
-};
-
-// All threads of the block: the run [lo, hi) of part `part` and its first tile.
-// With `last`, the place of tile hi - 1 instead. s_tmp: 34 words of shared memory.
-template <int N>
-__device__ __forceinline__ bool find_run(const Kv8AttnArgs& a, int part, bool last, int64_t* lo, int64_t* hi, Start* s,
-                                         int64_t* all_tiles, int* s_tmp) {
-  const int nthr = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = nthr >> 5;
-  const int64_t cand = static_cast<int64_t>(a.c.B) * a.row_tiles;
-  int64_t total = 0;
-  int v0 = 0, incl0 = 0;  // this thread's candidate of the first round
-  for (int64_t base = 0; base < cand; base += nthr) {
-    const int64_t i = base + tid;
-    int v = 0;
-    if (i < cand) v = row_tile<N>(a, static_cast<int>(i / a.row_tiles), static_cast<int>(i % a.row_tiles)).tiles;
-    int x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) s_tmp[warp] = x;
-    __syncthreads();
-    int before = 0, sum = 0;
-    for (int w = 0; w < nw; ++w) {
-      if (w < warp) before += s_tmp[w];
-      sum += s_tmp[w];
-    }
-    __syncthreads();
-    if (base == 0) v0 = v, incl0 = x + before;
-    total += sum;
-  }
-  const int64_t all = total * a.c.H;
-  const int64_t parts = min(static_cast<int64_t>(a.parts), all);
-  *all_tiles = all;
-  *lo = part < parts ? all * part / parts : all;
-  *hi = part < parts ? all * (part + 1) / parts : all;
-  if (*lo >= *hi) return false;
-  const int64_t want = last ? *hi - 1 : *lo;
-  int64_t run = 0;
-  for (int64_t base = 0; base < cand; base += nthr) {
-    const int64_t i = base + tid;
-    int v = v0, incl = incl0, sum = 0;
-    if (base > 0 || cand > nthr) {
-      v = 0;
-      if (i < cand) v = row_tile<N>(a, static_cast<int>(i / a.row_tiles), static_cast<int>(i % a.row_tiles)).tiles;
-      int x = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (lane == 31) s_tmp[warp] = x;
-      __syncthreads();
-      int before = 0;
-      for (int w = 0; w < nw; ++w) {
-        if (w < warp) before += s_tmp[w];
-        sum += s_tmp[w];
-      }
-      __syncthreads();
-      incl = x + before;
-    }
-    const int64_t from = (run + incl - v) * a.c.H, to = (run + incl) * a.c.H;
-    if (v > 0 && want >= from && want < to) {
-      const int off = static_cast<int>((want - from) / v);
-      s_tmp[0] = static_cast<int>(i / a.row_tiles);
-      s_tmp[1] = static_cast<int>(i % a.row_tiles);
-      s_tmp[2] = off;
-      s_tmp[3] = static_cast<int>((want - from) - static_cast<int64_t>(off) * v);
-    }
-    run += sum;
-    if (cand > nthr && run * a.c.H > want) break;  // the same for every thread
-  }
-  __syncthreads();
-  s->b = s_tmp[0];
-  s->rt = s_tmp[1];
-  s->h = s_tmp[2];
-  s->t = s_tmp[3];
-  __syncthreads();
-  return true;
-}
-
-// Walks the items of a run: (r, h) with tiles [t0, t1).
-template <int N>
-struct Walk {
-  RowTile r;
-  int h, t0, t1;
-  int64_t left;  // tiles of the run from t0 on
-
-  __device__ __forceinline__ Walk(const Kv8AttnArgs& a, const Start& s, int64_t count) {
-    r = row_tile<N>(a, s.b, s.rt);
-    h = s.h;
-    t0 = s.t;
-    left = count;
-    clip();
-  }
-  __device__ __forceinline__ void clip() { t1 = static_cast<int>(min(static_cast<int64_t>(r.tiles), t0 + left)); }
-  // The next item, if any is left.
-  __device__ __forceinline__ bool next(const Kv8AttnArgs& a) {
-    left -= t1 - t0;
-    if (left <= 0) return false;
-    t0 = 0;
-    if (++h == a.c.H) {
-      h = 0;
-      int b = r.b, rt = r.rt;
-      do {
-        if (++rt == a.row_tiles) {
-          rt = 0;
-          ++b;
-        }
-        if (b >= a.c.B) {  // cannot be: the run's tiles were counted
-          left = 0;
-          return false;
-        }
-        r = row_tile<N>(a, b, rt);
-        if (r.tiles == 0) rt = a.row_tiles - 1;  // no further row tile in this sequence
-      } while (r.tiles == 0);
-    }
-    clip();
-    return true;
-  }
-};
 
 // ---------------------------------------------------------- configuration --
 
@@ -271,13 +88,6 @@ struct Cfg {
   static_assert(kMetaRing >= (kRing + 1) / 2 + 1, "meta entries live as long as a tile's slots");
 };
 
-// Byte offset of element (row, byte) in a tile of rows of ROW bytes, swizzled as bulk tensor copies do.
-template <int ROW>
-__device__ __forceinline__ uint32_t swz(int row, int byte) {
-  const uint32_t o = static_cast<uint32_t>(row * ROW + byte);
-  return ROW == 128 ? o ^ ((o >> 3) & 0x70u) : o ^ ((o >> 3) & 0x30u);
-}
-
 // The e4m3 terms of eight query elements (already divided by the item's scale).
 template <int TERMS>
 __device__ __forceinline__ void split8(float* x, uint2* out) {
@@ -292,12 +102,6 @@ __device__ __forceinline__ void split8(float* x, uint2* out) {
       for (int i = 0; i < 8; ++i) x[i] -= y[i];
     }
   }
-}
-
-// 2^d of a whole d <= 127, exact; 0 below -126 and for -inf, NaN for NaN.
-__device__ __forceinline__ float exp2_whole(float d) {
-  const float p = __int_as_float((static_cast<int>(fmaxf(d, -127.f)) + 127) << 23);
-  return d != d ? d : p;
 }
 
 // Sums v[0 .. C - 1] over the warp's lanes; lane j (mod C) gets the sum of v[j].
@@ -317,11 +121,6 @@ __device__ __forceinline__ float lane_sums(float* v, int lane) {
     }
   }
   return v[0];
-}
-
-// Whether the step's token i sees its token j.
-__device__ __forceinline__ bool sees(const Kv8AttnArgs& a, int b, int i, int j) {
-  return a.tree ? a.tree[(static_cast<int64_t>(b) * a.max_tokens + i) * a.max_tokens + j] != 0 : j <= i;
 }
 
 // ----------------------------------------------------------------- kernel --
@@ -371,60 +170,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   const uint32_t tmem = uniform(sm.tmem);
 
   if (work && warp == kLoadWarp) {
-    // ---- copies: the pages of each tile's keys, then of its values
-    Walk<N> it(a, start, hi - lo);
-    const int bs = a.c.block, ppt = kTile / bs;
-    uint32_t fill = 0, begun = 0;
-    int i = 0;
-    do {
-      const int pages = (it.r.end + bs - 1) / bs;
-      const int32_t* table = a.c.table + static_cast<int64_t>(it.r.b) * a.c.max_blocks;
-      int id = -1, ke = 0, ve = 0;
-      for (int t = it.t0, g = 0; t < it.t1; ++t, g += ppt, ++i) {
-        if ((g & 31) == 0) {  // the next 32 pages' ids and scales, one a lane
-          const int page = t * ppt + lane;
-          id = page < pages ? table[page] : -1;
-          if (id >= a.c.num_blocks) id = -1;
-          if (id >= 0) {
-            const int64_t s = static_cast<int64_t>(id) * a.c.H + it.h;
-            ke = kv8_exp(a.c.ks[s]);
-            ve = kv8_exp(a.c.vs[s]);
-          } else {
-            ke = kBadPage;
-            ve = 0;
-          }
-        }
-        const int from = (g & 31) + (lane & (ppt - 1));
-        const int my_id = __shfl_sync(0xffffffffu, id, from), my_ke = __shfl_sync(0xffffffffu, ke, from),
-                  my_ve = __shfl_sync(0xffffffffu, ve, from);
-        const bool mine = lane < ppt && my_id >= 0;
-        const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine)) * bs * D);
-        auto at = [&](int name) { return name == 0 ? 0 : (name == 1 ? it.h : my_id); };
-        const int x1 = at(a.order & 3), x2 = at((a.order >> 2) & 3), x3 = at((a.order >> 4) & 3);
-#pragma unroll
-        for (int part = 0; part < 2; ++part, ++fill) {
-          const uint32_t slot = fill % NS, bar = smem_addr(&sm.full[slot]);
-          bool ok = true;
-          if (fill >= NS) ok = bar_wait(smem_addr(&sm.empty[slot]), (fill / NS - 1) & 1, gave_up);
-          ok = __all_sync(0xffffffffu, ok);
-          if (part == 0 && lane < ppt) {
-            sm.kexp[i % kMetaRing][lane] = my_ke;
-            sm.vexp[i % kMetaRing][lane] = my_ve;
-          }
-          __syncwarp();
-          if (!ok) continue;  // a wait gave up: no copy is started any more
-          begun = fill + 1;
-          if (lane == 0) bar_expect(bar, bytes);
-          __syncwarp();
-          if (mine)
-            load_4d(smem_addr(ring + slot * C::kSlot + lane * bs * D), part == 0 ? &kmap : &vmap, bar, 0, x1, x2, x3);
-        }
-      }
-    } while (it.next(a));
-    if (*gave_up)  // copies that are still in flight write this block's memory
-      for (uint32_t f = begun > NS ? begun - NS : 0; f < begun; ++f)
-        for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.full[f % NS]), (f / NS) & 1); ++k) {
-        }
+    copy_tiles<N, D, NS>(a, start, hi - lo, kmap, vmap, ring, sm, gave_up);
   } else if (work && warp == kMmaWarp) {
     // ---- products: the warp waits together, one lane issues
     constexpr uint32_t kStride = 8 * D;
@@ -534,7 +280,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         amax = fmaxf(sm.red[0], sm.red[1]);
       }
       const int eq = kv8_need(amax, -120, 120);
-      const float down = pow2i(-eq);
+      const float down = a.negate ? -pow2i(-eq) : pow2i(-eq);
       uint8_t* q_to = q_smem + (seg & 1) * C::kQ;
       if (own < N) {
 #pragma unroll 4
@@ -838,120 +584,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   griddep_launch_dependents();
 }
 
-// -------------------------------------------------------------------- join --
-//
-// Adds the shares of items that runs cut. Block x takes the item that begins in
-// part x and ends behind it, a warp one row: shares in the order of the parts,
-// each times 2^(its reference - the largest). The last blocks check sequences.
-
-constexpr int kJoinThreads = 256;
-
-template <typename QT, int D, int N>
-__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ Kv8AttnArgs a) {
-  __shared__ int s_tmp[36];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  griddep_launch_dependents();
-  if (blockIdx.x >= static_cast<unsigned>(a.parts)) {  // a warp per sequence: row_status
-    griddep_wait();
-    const int b = (blockIdx.x - a.parts) * (kJoinThreads / 32) + warp;
-    if (blockIdx.y > 0 || b >= a.c.B) return;
-    bool late = false;
-    for (int i = lane; i < a.parts; i += 32) late |= a.gave_up[i] != 0;
-    const int lo = a.cu[b], hi = a.cu[b + 1], len = a.c.len[b];
-    const bool sound = kv8_seq_ok(a.c, a.T, lo, hi, len) && hi - lo <= a.max_tokens;
-    bool bad = !sound;
-    if (sound && hi > lo) {
-      const int pages = (len + (hi - lo) + a.c.block - 1) / a.c.block;
-      for (int j = lane; j < pages; j += 32) {
-        const int id = a.c.table[static_cast<int64_t>(b) * a.c.max_blocks + j];
-        bad |= id < 0 || id >= a.c.num_blocks;
-      }
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    late = __any_sync(0xffffffffu, late);
-    if (lane == 0) a.row_status[b] = (bad ? SPEC_ROW_CACHE : 0) | (late ? SPEC_ROW_TIMEOUT : 0);
-    if (!sound && lo >= 0 && hi > lo && hi <= a.T) {
-      const int64_t rows = static_cast<int64_t>(hi - lo) * a.q_heads;
-      for (int64_t i = 0; i < rows; ++i) {
-        QT* out = static_cast<QT*>(a.out) + (lo + i / a.q_heads) * a.ost + (i % a.q_heads) * a.osh;
-        for (int d = lane; d < D; d += 32) out[d] = from_f<QT>(__int_as_float(0x7fffffff));
-      }
-    }
-    return;
-  }
-  int64_t lo, hi, all;
-  Start s;
-  if (!find_run<N>(a, blockIdx.x, true, &lo, &hi, &s, &all, s_tmp)) return;
-  const RowTile r = row_tile<N>(a, s.b, s.rt);
-  const int64_t begin = hi - 1 - s.t, end = begin + r.tiles;  // the item's tiles
-  const int row = blockIdx.y * (kJoinThreads / 32) + warp;
-  if (begin < lo || end <= hi || row >= r.rows) return;
-  const int64_t parts = min(static_cast<int64_t>(a.parts), all);
-  int64_t last = (end - 1) * parts / all;
-  while (all * (last + 1) / parts <= end - 1) ++last;
-  const int n = static_cast<int>(last - blockIdx.x) + 1;
-  griddep_wait();
-  const int64_t first = blockIdx.x;
-  auto share = [&](int i) { return (2 * (first + i) + (i == 0 ? 1 : 0)) * N + row; };
-  float top = kNegInf;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, a.part_ml[share(i)].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (top == kNegInf) top = 0.f;
-  constexpr int V = D / 32;
-  float acc[V] = {}, sum = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float2 ml = a.part_ml[share(i)];
-    const float* p = a.part_o + share(i) * D + lane * V;
-    float x[V];
-    if (V == 4) {
-      const float4 u = *reinterpret_cast<const float4*>(p);
-      x[0] = u.x, x[1] = u.y, x[V - 2] = u.z, x[V - 1] = u.w;
-    } else {
-      const float2 u = *reinterpret_cast<const float2*>(p);
-      x[0] = u.x, x[1] = u.y;
-    }
-    const float w = exp2_whole(ml.x - top);
-    sum = fmaf(w, ml.y, sum);
-#pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = fmaf(w, x[k], acc[k]);
-  }
-  const int64_t item_row = static_cast<int64_t>(s.rt) * N + row, tok = item_row / a.group;
-  QT* out = static_cast<QT*>(a.out) + (r.first + tok) * a.ost +
-            (s.h * a.group + static_cast<int>(item_row - tok * a.group)) * a.osh + lane * V;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int k = 0; k < V; ++k) out[k] = from_f<QT>(acc[k] * inv);
-}
-
 // ------------------------------------------------------------------ launch --
-
-constexpr int kSms = 152;
 
 template <typename QT, int D, int RW, int W, int TERMS, int CTAS>
 cudaError_t launch_attention(const Kv8AttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t st) {
   using C = Cfg<D, RW, W, TERMS, CTAS>;
-  auto kernel = kv8_attention_kernel<QT, C>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.parts));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, a, k, v);
-  if (e != cudaSuccess) return e;
-  const int64_t rows = static_cast<int64_t>(a.max_tokens) * a.group;
-  const int y = static_cast<int>((rows < C::N ? rows : C::N) + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-  const int checks = (a.c.B + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-  return launch_pdl(kv8_join_kernel<QT, D, C::N>, dim3(static_cast<unsigned>(a.parts + checks), static_cast<unsigned>(y)),
-                    dim3(kJoinThreads), st, a);
+  const cudaError_t e = launch_tiles(kv8_attention_kernel<QT, C>, a, C::kThreads, C::kSmem, k, v, st);
+  return e != cudaSuccess ? e : launch_join<QT, D, C::N>(a, st);
 }
 
 template <typename QT, int D, int TERMS>
@@ -964,7 +603,9 @@ cudaError_t launch_rows(const Kv8AttnArgs& a, int rows, const CUtensorMap& k, co
 
 }  // namespace
 
-int kv8_attention_rows(int64_t max_rows) { return max_rows <= 16 ? 16 : (max_rows <= 32 ? 32 : (max_rows <= 48 ? 48 : 64)); }
+int kv8_attention_rows(int64_t max_rows) {
+  return max_rows <= 16 ? 16 : (max_rows <= 32 ? 32 : (max_rows <= 48 ? 48 : (max_rows <= 64 ? 64 : (max_rows <= 128 ? 128 : 256))));
+}
 
 int kv8_attention_parts(int rows) { return rows <= 16 ? 2 * kSms : kSms; }
 

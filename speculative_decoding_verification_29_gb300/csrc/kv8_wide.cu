@@ -1,0 +1,570 @@
+// kv8_wide.cu -- attention over the 8-bit paged KV cache for many rows: the
+// target's pass over draft positions, trees and prompts.
+//
+// Here a row of scores is one thread's. Tiles of keys and values are turned from
+// e4m3 into f16 once, exactly, for all the rows of the item (64 conversions a
+// thread and tile), which buys products in f16: queries (a power of two times
+// bf16 or fp16 values, exact above 2^-24 of the item's largest) and weights (2^-12
+// of their value, down to 2^-32 of the largest) need one term each, and because
+// f16 weights keep their precision over 24 powers of two, the output may stay in
+// tensor memory across tiles: a row's sums are relative to a reference that
+// moves only when a tile passes it by 2^8, and only then the accumulator is read
+// and scaled.
+// With exponents y_t = sm_scale log2(e) 2^ek(t) (q . ck_t) + ev(t) a row's result
+// is sum_t 2^(y_t - ref) cv_t / sum_t 2^(y_t - ref - ev(t)): the blocks' scales
+// enter as a factor of the score, a summand of the exponent, and a factor of
+// each block's sum of weights.
+//
+// Two streams, each with four softmax warps, 128 rows of scores that become the
+// weights in place, and 128 columns of output in tensor memory, take turns at the
+// tensor cores. PAIR: the streams are two row tiles (256 rows of an item) that
+// share the tiles. Otherwise they share the rows (128), take every other tile
+// and are added up at the item's end: both read each other's accumulator, since a
+// row has the same lane in both.
+// Four more warps convert tiles and load queries, one copies, one issues.
+#include <string.h>
+
+#include "kv8_attn.cuh"
+
+namespace specv {
+
+namespace {
+
+constexpr float kFar = 8.f;  // a tile moves the reference when it passes it by 2^8: weights stay below 2^8, far from 65504
+constexpr int kItems = 4;    // items in flight between the query loads and the results
+
+template <int D_, bool PAIR_>
+struct Wide {
+  static constexpr int D = D_, N = PAIR_ ? 256 : 128;
+  static constexpr bool PAIR = PAIR_;
+  static constexpr int kThreads = 3 * 128 + 64;
+  static constexpr int kF8 = kTile * D, kF16 = 2 * kF8;  // a tile of keys or values
+  static constexpr int kPanel = kTile * 128;             // 64 columns of f16
+  static constexpr int kQ = (PAIR ? 2 : 1) * kF16;
+  static constexpr int NF = PAIR ? 3 : 4;  // f16 tiles
+  struct Item {
+    int b, first, n, ctx, rows, end, r0, h, t0, t1, tiles, eq;
+  };
+  struct Small {
+    alignas(16) Item item[kItems];
+    float ref[2][2][kTile], sum[2][2][kTile];  // of two items: each stream's rows, exchanged at an item's end
+    float red[4];
+    int nan[kItems];
+    int kexp[kMetaRing][kMaxPages], vexp[kMetaRing][kMaxPages];
+    alignas(8) uint64_t full[8], empty[8], full16[4], empty16[4], s_full[2], p_ready[2], o_full[2], q_ready[kItems], q_free,
+        done, drain;
+    uint32_t tmem;
+    int gave_up;
+    int tmp[36];
+  };
+  static constexpr int kFixed = 1024 + kQ + NF * kF16 + static_cast<int>(sizeof(Small));
+  static constexpr int kFit = (231424 - kFixed) / kF8;
+  static constexpr int NS = kFit > 6 ? 6 : kFit;  // e4m3 tiles
+  static constexpr int kSmem = kFixed + NS * kF8;
+  static_assert(NS >= 3, "ring of e4m3 tiles");
+  static_assert(2 * kMetaRing >= NS + NF + 4, "a tile's exponents outlive its weights");
+};
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <typename QT, typename C>
+__global__ void __launch_bounds__(C::kThreads, 1)
+    kv8_wide_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ CUtensorMap kmap,
+                    const __grid_constant__ CUtensorMap vmap) {
+  extern __shared__ uint8_t dyn[];
+  constexpr int D = C::D, N = C::N, NS = C::NS, NF = C::NF;
+  constexpr bool PAIR = C::PAIR;
+  uint8_t* q_smem = dyn + ((1024u - (smem_addr(dyn) & 1023u)) & 1023u);
+  uint8_t* f16 = q_smem + C::kQ;
+  uint8_t* ring = f16 + NF * C::kF16;
+  typename C::Small& sm = *reinterpret_cast<typename C::Small*>(ring + NS * C::kF8);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kConvWarp = 8, kLoadWarp = 12, kMmaWarp = 13;
+  constexpr uint32_t kO = 256;  // tensor memory: scores (and weights) of the streams at 0 and 128, outputs behind
+  volatile int* gave_up = &sm.gave_up;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      bar_init(smem_addr(&sm.full[i]), 1);
+      bar_init(smem_addr(&sm.empty[i]), 4);
+    }
+    for (int i = 0; i < NF; ++i) {
+      bar_init(smem_addr(&sm.full16[i]), 4);
+      bar_init(smem_addr(&sm.empty16[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(smem_addr(&sm.s_full[i]), 1);
+      bar_init(smem_addr(&sm.p_ready[i]), 4);
+      bar_init(smem_addr(&sm.o_full[i]), 1);
+    }
+    for (int i = 0; i < kItems; ++i) bar_init(smem_addr(&sm.q_ready[i]), 4);
+    bar_init(smem_addr(&sm.q_free), 1);
+    bar_init(smem_addr(&sm.done), 8);
+    bar_init(smem_addr(&sm.drain), 1);
+    fence_bar_init();
+    sm.gave_up = 0;
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_addr(&sm.tmem), 512);
+  griddep_wait();
+  int64_t lo, hi, all;
+  Start start;
+  fence_before();
+  const bool work = find_run<N>(a, blockIdx.x, false, &lo, &hi, &start, &all, sm.tmp);
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = uniform(sm.tmem);
+  // Steps of the two streams for an item of nt tiles.
+  auto steps = [](int nt, int rows, int stream) {
+    if (PAIR) return stream == 0 || rows > kTile ? nt : 0;
+    return (nt + 1 - stream) / 2;
+  };
+
+  if (work && warp == kLoadWarp) {
+    copy_tiles<N, D, NS>(a, start, hi - lo, kmap, vmap, ring, sm, gave_up);
+  } else if (work && warp == kMmaWarp) {
+    // ---- products: the warp waits together, one lane issues
+    constexpr uint32_t id_s = instr_desc_f16(kTile, kTile, false), id_o = instr_desc_f16(kTile, D, true);
+    const uint32_t q_at = smem_addr(q_smem), f_at = smem_addr(f16);
+    int base = 0, count[2] = {0, 0};  // tiles and steps of earlier items
+    for (int seg = 0;; ++seg) {
+      bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 3]), (seg >> 2) & 1, gave_up);
+      ok = __all_sync(0xffffffffu, ok);
+      const int nt = uniform(sm.item[seg & 3].t1 - sm.item[seg & 3].t0), rows = uniform(sm.item[seg & 3].rows);
+      if (!ok || nt <= 0) break;
+      fence_after();
+      const int n0 = steps(nt, rows, 0), n1 = steps(nt, rows, 1);
+      auto scores = [&](int b, int s) {  // S[b] = Q x K^T
+        const uint32_t j = 2u * (base + (PAIR ? s : 2 * s + b)), slot = uniform(j % NF);
+        bool ok = bar_wait(smem_addr(&sm.full16[slot]), (j / NF) & 1, gave_up);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        fence_after();
+        const bool last = n1 == n0 ? b == 1 && s == n1 - 1 : b == 0 && s == n0 - 1;
+        if (elect()) {
+          const uint64_t qd = smem_desc(q_at + (PAIR ? b * C::kF16 : 0), 16, 1024, 2),
+                         kd = smem_desc(f_at + slot * C::kF16, 16, 1024, 2);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const int off = ((k / 4) * C::kPanel + (k % 4) * 32) >> 4;
+            mma_f16(tmem + b * kTile, qd + off, kd + off, id_s, k > 0);
+          }
+          if (!PAIR || b == 1 || n1 == 0) commit(smem_addr(&sm.empty16[slot]));
+          commit(smem_addr(&sm.s_full[b]));
+          if (last) commit(smem_addr(&sm.q_free));
+        }
+        __syncwarp();
+      };
+      auto product = [&](int b, int s) {  // O[b] += P[b] x V
+        const uint32_t j = 2u * (base + (PAIR ? s : 2 * s + b)) + 1, slot = uniform(j % NF);
+        bool ok = bar_wait(smem_addr(&sm.full16[slot]), (j / NF) & 1, gave_up) &&
+                  bar_wait(smem_addr(&sm.p_ready[b]), (count[b] + s) & 1, gave_up);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        fence_after();
+        if (elect()) {
+          const uint64_t vd = smem_desc(f_at + slot * C::kF16, C::kPanel, 1024, 2);
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_f16_tmem(tmem + kO + b * kTile, tmem + b * kTile + 8 * k, vd + (k * 2048 >> 4), id_o, s > 0 || k > 0);
+          if (!PAIR || b == 1 || n1 == 0) commit(smem_addr(&sm.empty16[slot]));
+          commit(smem_addr(&sm.o_full[b]));
+        }
+        __syncwarp();
+      };
+      scores(0, 0);
+      if (n1 > 0) scores(1, 0);
+      // the last item's outputs have been read
+      if (seg > 0) ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.done), (seg - 1) & 1, gave_up));
+      for (int s = 0; s < n0 && ok; ++s) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          if (s >= (b == 0 ? n0 : n1)) continue;
+          product(b, s);
+          if (s + 1 < (b == 0 ? n0 : n1)) scores(b, s + 1);
+        }
+        ok = !*gave_up;
+      }
+      base += nt;
+      count[0] += n0;
+      count[1] += n1;
+    }
+    if (*gave_up) {  // products that are still running write this block's tensor memory
+      if (elect()) commit(smem_addr(&sm.drain));
+      for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.drain), 0); ++k) {
+      }
+    }
+    __syncwarp();
+  } else if (work && warp >= kConvWarp && warp < kLoadWarp) {
+    // ---- an item's queries, then its tiles, into f16: a thread owns a row
+    const int own = tid - kConvWarp * 32, quarter = warp - kConvWarp;
+    const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (a.qst * 2) | (a.qsh * 2)) & 15) == 0;
+    const uint32_t turn = static_cast<uint32_t>(own & 7) << 4;  // the swizzle of this row
+    Walk<N> it(a, start, hi - lo);
+    int seg = 0, i = 0;
+    do {
+      const RowTile r = it.r;
+      const int r0 = r.rt * N;
+      auto chunk = [&](int row, int d, float* x) {
+        const uint32_t tok = static_cast<uint32_t>(r0 + row) / static_cast<uint32_t>(a.group);
+        const QT* q = static_cast<const QT*>(a.q) + (r.first + static_cast<int64_t>(tok)) * a.qst +
+                      (it.h * a.group + (r0 + row - static_cast<int>(tok) * a.group)) * a.qsh + d;
+        if (vec) {
+          const uint4 u = *reinterpret_cast<const uint4*>(q);
+          const QT* e = reinterpret_cast<const QT*>(&u);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = to_f(e[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = to_f(q[k]);
+        }
+      };
+      float amax = 0.f;
+      for (int row = own; row < r.rows; row += kTile) {
+#pragma unroll 4
+        for (int d = 0; d < D; d += 8) {
+          float x[8];
+          chunk(row, d, x);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (fabsf(x[k]) < -kNegInf) amax = fmaxf(amax, fabsf(x[k]));
+        }
+      }
+      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+      named_sync(2, 128);  // the last item's maxima have been read
+      if (lane == 0) sm.red[quarter] = amax;
+      named_sync(2, 128);
+      amax = fmaxf(fmaxf(sm.red[0], sm.red[1]), fmaxf(sm.red[2], sm.red[3]));
+      const int eq = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13, -110), 110);  // largest below 2^14
+      const float down = a.negate ? -pow2i(-eq) : pow2i(-eq);
+      if (seg > 0) bar_wait(smem_addr(&sm.q_free), (seg - 1) & 1, gave_up);
+      for (int row = own; row < r.rows; row += kTile) {
+        uint8_t* to = q_smem + (row / kTile) * C::kF16 + own * 128;
+#pragma unroll 4
+        for (int d = 0; d < D; d += 8) {
+          float x[8];
+          chunk(row, d, x);
+          uint4 u;
+          u.x = half2_bits(x[0] * down, x[1] * down);
+          u.y = half2_bits(x[2] * down, x[3] * down);
+          u.z = half2_bits(x[4] * down, x[5] * down);
+          u.w = half2_bits(x[6] * down, x[7] * down);
+          *reinterpret_cast<uint4*>(to + (d / 64) * C::kPanel + (((d % 64) * 2) ^ turn)) = u;
+        }
+      }
+      if (own == 0) {
+        sm.nan[seg & 3] = 0;
+        sm.item[seg & 3] = {r.b, r.first, r.n, r.ctx, r.rows, r.end, r0, it.h, it.t0, it.t1, r.tiles, eq};
+      }
+      fence_async_shared();
+      named_sync(2, 128);  // the flag is cleared before a tile of the item sets it
+      if (lane == 0) bar_arrive(smem_addr(&sm.q_ready[seg & 3]));
+
+      for (int t = it.t0; t < it.t1; ++t, ++i) {
+        const int slot = t * kTile + own;
+        const bool masked = t * kTile + kTile > r.ctx;  // not every row sees every slot
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const uint32_t j = 2u * i + part, from = j % NS, to = j % NF;
+          bar_wait(smem_addr(&sm.full[from]), (j / NS) & 1, gave_up);
+          if (j >= NF) bar_wait(smem_addr(&sm.empty16[to]), (j / NF - 1) & 1, gave_up);
+          const uint8_t* src = ring + from * C::kF8 + own * D;
+          uint8_t* dst = f16 + to * C::kF16 + own * 128;
+          // a row of D bytes is swizzled within 128 bytes, or within 64 by the row's second and third bit
+          const uint32_t src_turn = D == 128 ? turn : static_cast<uint32_t>((own >> 1) & 3) << 4;
+          bool nan = false;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint4 u = *reinterpret_cast<const uint4*>(src + ((16u * c) ^ src_turn));
+            uint32_t* w = &u.x;
+            if (part == 1 && masked) {
+              // Slots behind the sequence hold no values, and a NaN value must not reach the rows that do not see it
+              // through a weight of 0: both are cleared here, and the rows that see a NaN get it at the item's end.
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const uint32_t m = slot >= r.end ? 0xffffffffu : __vcmpeq4(w[z] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                nan |= m != 0;
+                w[z] &= ~m;
+              }
+            }
+            uint32_t v[8];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v[2 * z]) : "h"(static_cast<uint16_t>(w[z] & 0xffff)));
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v[2 * z + 1]) : "h"(static_cast<uint16_t>(w[z] >> 16)));
+            }
+            uint8_t* panel = dst + (c / 4) * C::kPanel;
+            *reinterpret_cast<uint4*>(panel + ((32u * (c % 4)) ^ turn)) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(panel + ((32u * (c % 4) + 16u) ^ turn)) = make_uint4(v[4], v[5], v[6], v[7]);
+          }
+          if (nan && slot < r.end) sm.nan[seg & 3] = 1;
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            bar_arrive(smem_addr(&sm.empty[from]));
+            bar_arrive(smem_addr(&sm.full16[to]));
+          }
+        }
+      }
+      ++seg;
+    } while (it.next(a));
+    bar_wait(smem_addr(&sm.q_free), (seg - 1) & 1, gave_up);
+    if (own == 0) sm.item[seg & 3].t0 = sm.item[seg & 3].t1 = 0;  // no further item
+    __syncwarp();
+    if (lane == 0) bar_arrive(smem_addr(&sm.q_ready[seg & 3]));
+  } else if (work && warp < kConvWarp) {
+    // ---- weights and sums: a thread owns a row of its stream
+    const int b = uniform(warp >> 2), quarter = uniform(warp & 3);
+    const int own = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t s_at = lanes + b * kTile, o_at = lanes + kO + b * kTile;
+    const int page_shift = 31 - __clz(a.c.block) - 4;  // sixteen slots g are in page g >> page_shift
+    int base = 0, count[2] = {0, 0};
+    for (int seg = 0;; ++seg) {
+      bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 3]), (seg >> 2) & 1, gave_up);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {  // the other warps may be a few barriers behind
+        for (int64_t k = 0; k < hi - lo + 2; ++k) named_arrive(1, 256);
+        break;
+      }
+      const typename C::Item& it = sm.item[seg & 3];
+      const int t0 = uniform(it.t0), nt = uniform(it.t1) - t0, rows = uniform(it.rows);
+      if (nt <= 0) break;
+      const int n[2] = {steps(nt, rows, 0), steps(nt, rows, 1)};
+      const int steps_here = b == 0 ? n[0] : n[1], count_here = b == 0 ? count[0] : count[1];
+      const int ctx = uniform(it.ctx);
+      const int row = PAIR ? b * kTile + own : own;  // within the item
+      const bool rows_here = (PAIR ? b * kTile : 0) + quarter * 32 < rows;
+      const float scale = a.scale * pow2i(it.eq);
+      float ref = kNegInf, l = 0.f;
+      for (int s = 0; s < steps_here; ++s) {
+        const int step = PAIR ? s : 2 * s + b, ti = base + step, slot0 = (t0 + step) * kTile;
+        const int* ke_at = sm.kexp[ti % kMetaRing];
+        const int* ve_at = sm.vexp[ti % kMetaRing];
+        bar_wait(smem_addr(&sm.s_full[b]), (count_here + s) & 1, gave_up);
+        fence_after();
+        if (rows_here) {
+          const bool masked = slot0 + kTile > ctx;
+          uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+          if (masked) {
+            const int token = min(it.n - 1, static_cast<int>(static_cast<uint32_t>(it.r0 + row) / static_cast<uint32_t>(a.group)));
+            const int seen = (a.tree ? ctx : ctx + token + 1) - slot0;  // slots before this are seen
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              vis[k] = seen >= 32 * k + 32 ? 0xffffffffu : (seen <= 32 * k ? 0u : (1u << (seen - 32 * k)) - 1u);
+            if (a.tree) {
+              const uint8_t* m8 = a.tree + (static_cast<int64_t>(it.b) * a.max_tokens + token) * a.max_tokens - ctx + slot0;
+              const int from = max(0, seen), to = min(kTile, it.end - slot0);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll 8
+                for (int c = max(from, 32 * k); c < min(to, 32 * k + 32); ++c)
+                  if (m8[c]) vis[k] |= 1u << (c - 32 * k);
+            }
+          }
+          // the largest exponent; NaN scores are passed over here
+          float m = kNegInf;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x[32];
+            tmem_ld<32>(s_at + 32 * k, x);
+            wait_ld();
+            if (masked) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((vis[k] >> j) & 1)) x[j] = 0xff800000u;
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              float top[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                top[j] = fmaxf(fmaxf(__uint_as_float(x[16 * g + j]), __uint_as_float(x[16 * g + 4 + j])),
+                               fmaxf(__uint_as_float(x[16 * g + 8 + j]), __uint_as_float(x[16 * g + 12 + j])));
+              const int page = (2 * k + g) >> page_shift, ke = ke_at[page];
+              if (ke != kBadPage)
+                m = fmaxf(m, fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), scale * pow2i(ke),
+                                  static_cast<float>(ve_at[page])));
+            }
+          }
+          const bool far = m - ref > kFar;  // true from no reference to any; false for m = -inf
+          if (__any_sync(0xffffffffu, far)) {
+            const float now = far ? ceilf(m) : ref;
+            const float by = ref == now ? 1.f : exp2_whole(ref - now);
+            ref = now;
+            l *= by;
+            if (s > 0) {
+              bar_wait(smem_addr(&sm.o_full[b]), (count_here + s - 1) & 1, gave_up);
+              fence_after();
+#pragma unroll 1
+              for (int k = 0; k < D / 16; ++k) {
+                uint32_t x[16];
+                tmem_ld<16>(o_at + 16 * k, x);
+                wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * by);
+                tmem_st16(o_at + 16 * k, x);
+              }
+            }
+          }
+          const float from = ref == kNegInf ? 0.f : ref;
+          // weights in place of the scores, and their sum
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x[32], p[16];
+            tmem_ld<32>(s_at + 32 * k, x);
+            wait_ld();
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const int page = (2 * k + g) >> page_shift, ke = ke_at[page], ve = ve_at[page];
+              const float cs = ke == kBadPage ? __int_as_float(0x7fffffff) : scale * pow2i(ke);
+              const float c0 = static_cast<float>(ve) - from;
+              float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int j = 16 * g; j < 16 * g + 16; j += 2) {
+                float2 y = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), make_float2(cs, cs),
+                                make_float2(c0, c0));
+                if (masked) {
+                  if (!((vis[k] >> j) & 1)) y.x = kNegInf;
+                  if (!((vis[k] >> (j + 1)) & 1)) y.y = kNegInf;
+                }
+                const float2 w = make_float2(ex2_fast(y.x), ex2_fast(y.y));
+                sum = add2(sum, w);
+                p[j / 2] = half2_bits(w.x, w.y);
+              }
+              l = fmaf(sum.x + sum.y, pow2i(-ve), l);
+            }
+            tmem_st16(s_at + 16 * k, p);
+          }
+          wait_st();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_addr(&sm.p_ready[b]));
+      }
+
+      // ---- the item's results, or its share of them
+      if (steps_here > 0) bar_wait(smem_addr(&sm.o_full[b]), (count_here + steps_here - 1) & 1, gave_up);
+      if (!PAIR) {
+        sm.ref[seg & 1][b][own] = ref;
+        sm.sum[seg & 1][b][own] = l;
+      }
+      fence_before();
+      named_sync(1, 256);  // both streams' products are done; and a stream without steps does not run ahead
+      fence_after();
+      float a0 = 1.f, a1 = 0.f;  // factors of the own and the other stream's sums
+      if (!PAIR) {
+        const float other = sm.ref[seg & 1][1 - b][own];
+        float top = fmaxf(ref, other);
+        if (top == kNegInf) top = 0.f;
+        a0 = exp2_whole(ref - top);
+        a1 = exp2_whole(other - top);
+        l = fmaf(a0, l, a1 * sm.sum[seg & 1][1 - b][own]);
+        ref = fmaxf(ref, other);
+      }
+      const bool whole = t0 == 0 && nt == it.tiles;
+      const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (t0 > 0 ? 0 : 1);
+      if (rows_here && (!PAIR || steps_here > 0)) {
+        const int tok = static_cast<int>(static_cast<uint32_t>(it.r0 + min(row, rows - 1)) / static_cast<uint32_t>(a.group));
+        const int head = it.h * a.group + (it.r0 + min(row, rows - 1) - tok * a.group);
+        QT* out = static_cast<QT*>(a.out) + (it.first + static_cast<int64_t>(tok)) * a.ost + head * a.osh;
+        const bool vec = ((reinterpret_cast<uintptr_t>(a.out) | (a.ost * 2) | (a.osh * 2)) & 15) == 0;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (!whole && row < rows && (PAIR || b == 0)) a.part_ml[part * N + row] = make_float2(ref, l);
+        const bool nan = sm.nan[seg & 3] != 0;  // set before the weights of its tile were used
+        // the streams of one row tile take half of the dimensions each
+        constexpr int kDims = PAIR ? D : D / 2;
+        const int d0 = PAIR ? 0 : b * kDims;
+#pragma unroll 1
+        for (int d = d0; d < d0 + kDims; d += 16) {
+          uint32_t x[16], z[16];
+          float v[16];
+          if (steps_here > 0) tmem_ld<16>(o_at + d, x);
+          const bool both = !PAIR && n[0] > 0 && n[1] > 0;
+          if (both) tmem_ld<16>(lanes + kO + (1 - b) * kTile + d, z);
+          if (!PAIR && steps_here == 0) tmem_ld<16>(lanes + kO + (1 - b) * kTile + d, z);
+          wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            v[k] = steps_here > 0 ? a0 * __uint_as_float(x[k]) : 0.f;
+            if (both || (!PAIR && steps_here == 0)) v[k] = fmaf(a1, __uint_as_float(z[k]), v[k]);
+          }
+          if (nan) {  // dimensions in which a value that this row sees is NaN
+            const int last = min(it.end, it.t1 * kTile);
+            for (int slot = max(t0, ctx / kTile) * kTile; slot < last; ++slot) {
+              if (slot >= ctx && !sees(a, it.b, tok, slot - ctx)) continue;
+              const int id = a.c.table[static_cast<int64_t>(it.b) * a.c.max_blocks + slot / a.c.block];
+              if (id < 0 || id >= a.c.num_blocks) continue;
+              const uint8_t* code = a.c.v + id * a.c.sb + it.h * a.c.sh + (slot % a.c.block) * a.c.ss + d;
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if ((code[k] & 0x7f) == 0x7f) v[k] = __int_as_float(0x7fffffff);
+            }
+          }
+          if (row >= rows) {
+          } else if (!whole) {
+            float4* to = reinterpret_cast<float4*>(a.part_o + (part * N + row) * D + d);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) to[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          } else {
+            QT h[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) h[k] = from_f<QT>(v[k] * inv);
+            if (vec) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint4 u;
+                memcpy(&u, h + 8 * k, 16);
+                *reinterpret_cast<uint4*>(out + d + 8 * k) = u;
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) out[d + k] = h[k];
+            }
+          }
+          __syncwarp();
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_addr(&sm.done));
+      base += nt;
+      count[0] += n[0];
+      count[1] += n[1];
+    }
+  }
+
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == kMmaWarp) tmem_free(tmem, 512);
+  if (tid == 0) a.gave_up[blockIdx.x] = sm.gave_up;
+  griddep_launch_dependents();
+}
+
+template <typename QT, int D, bool PAIR>
+cudaError_t launch_wide(const Kv8AttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t st) {
+  using C = Wide<D, PAIR>;
+  const cudaError_t e = launch_tiles(kv8_wide_kernel<QT, C>, a, C::kThreads, C::kSmem, k, v, st);
+  return e != cudaSuccess ? e : launch_join<QT, D, C::N>(a, st);
+}
+
+template <typename QT>
+cudaError_t launch_type(const Kv8AttnArgs& a, int rows, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t st) {
+  if (a.c.D == 128) return rows == 128 ? launch_wide<QT, 128, false>(a, k, v, st) : launch_wide<QT, 128, true>(a, k, v, st);
+  return rows == 128 ? launch_wide<QT, 64, false>(a, k, v, st) : launch_wide<QT, 64, true>(a, k, v, st);
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_wide(const Kv8AttnArgs& a, int dtype, int rows, const CUtensorMap& k, const CUtensorMap& v,
+                            cudaStream_t st) {
+  return dtype == SPEC_BF16 ? launch_type<__nv_bfloat16>(a, rows, k, v, st) : launch_type<__half>(a, rows, k, v, st);
+}
+
+}  // namespace specv
