@@ -61,7 +61,7 @@ struct Cfg {
 
   // One item, as the query warps hand it to the others.
   struct Item {
-    int b, first, n, ctx, rows, end, r0, h, t0, t1, whole;
+    int b, first, n, ctx, rows, end, part, r0, h, t0, t1, whole;
   };
   struct Small {
     Item item[2];
@@ -72,7 +72,7 @@ struct Cfg {
     float inv[W * 4][RW];
     float red[2];
     int nan[2], eq[2];
-    int kexp[kMetaRing][kMaxPages], vexp[kMetaRing][kMaxPages];
+    alignas(16) float4 page[kMetaRing][kMaxPages];
     alignas(8) uint64_t full[12], empty[12], s_full[2], p_ready[2], o_full[2], q_ready[2], q_free[2], drain;
     uint32_t tmem;
     int gave_up;
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       if (own == 0) {
         sm.nan[seg & 1] = 0;
         sm.eq[seg & 1] = eq;
-        sm.item[seg & 1] = {r.b, r.first, r.n, r.ctx, r.rows, r.end, r0, it.h, it.t0, it.t1, it.t0 == 0 && it.t1 == r.tiles};
+        sm.item[seg & 1] = {r.b, r.first, r.n, r.ctx, r.rows, r.end, r.part, r0, it.h, it.t0, it.t1, it.t0 == 0 && it.t1 == r.tiles};
       }
       fence_async_shared();
       __syncwarp();
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       const typename C::Item& it = sm.item[seg & 1];
       const int t0 = uniform(it.t0), t1 = uniform(it.t1);
       if (t1 <= t0) break;
-      const int first_masked = uniform(it.ctx / kTile);  // from this tile on not every row sees every slot
+      const int first_masked = uniform(it.part);  // from this tile on not every row sees every slot
       const float scale = a.scale * pow2i(sm.eq[seg & 1]);
       float ref = kNegInf;  // of row lane % 16: the exponent its sums are relative to
 #pragma unroll
@@ -366,9 +366,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         uint32_t x[RW];
         tmem_ld<RW>(lanes + buf * N + row_base, x);
 
-        const int ke = sm.kexp[i % kMetaRing][page], ve = sm.vexp[i % kMetaRing][page];
-        const float cs = ke == kBadPage ? __int_as_float(0x7fffffff) : scale * pow2i(ke);
-        const float ev = static_cast<float>(ve), ve_inv = pow2i(-ve);
+        const float4 meta = sm.page[i % kMetaRing][page];
+        const float cs = scale * meta.x, ev = meta.y, ve_inv = meta.z;
         const bool masked = t >= first_masked;
         uint32_t vis = 0xffffffffu;
         if (masked) {
@@ -528,7 +527,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       }
       accumulate(i - 1);
       if (sm.nan[seg & 1]) {  // set before the weights of its tile were ready
-        for (int slot = max(t0, it.ctx / kTile) * kTile; slot < min(it.end, t1 * kTile); ++slot) {
+        for (int slot = max(t0, it.part) * kTile; slot < min(it.end, t1 * kTile); ++slot) {
           const int id = a.c.table[static_cast<int64_t>(it.b) * a.c.max_blocks + slot / a.c.block];
           if (id < 0 || id >= a.c.num_blocks) continue;
           const uint8_t code = a.c.v[id * a.c.sb + it.h * a.c.sh + (slot % a.c.block) * a.c.ss + own % D];

@@ -18,7 +18,6 @@ using namespace tc;
 constexpr int kTile = 128;
 constexpr int kMetaRing = 8;
 constexpr int kMaxPages = kTile / 16;
-constexpr int kBadPage = 1 << 20;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 template <typename T>
@@ -45,6 +44,7 @@ struct RowTile {
   int rows;   // rows of this tile
   int end;    // slots that some row of it may see
   int tiles;  // ceil(end / 128); 0: no such row tile
+  int part;   // from this tile on some row does not see every slot
 };
 
 template <int N>
@@ -62,6 +62,7 @@ __device__ __forceinline__ RowTile row_tile(const Kv8AttnArgs& a, int b, int rt)
   r.rows = static_cast<int>(min(rows - r0, static_cast<int64_t>(N)));
   r.end = len + (a.tree ? r.n : static_cast<int>((r0 + r.rows - 1) / a.group) + 1);
   r.tiles = (r.end + kTile - 1) / kTile;
+  r.part = (len + (a.tree ? 0 : static_cast<int>(r0 / a.group) + 1)) / kTile;
   return r;
 }
 
@@ -210,7 +211,8 @@ __device__ __forceinline__ bool sees(const Kv8AttnArgs& a, int b, int i, int j) 
 }
 
 // The copying warp: the pages of each tile's keys, then of its values, into a
-// ring of NS slots, and the tile's block exponents into sm.kexp and sm.vexp.
+// ring of NS slots, and of each page of the tile 2^ek (NaN for a page outside the
+// pool), ev and 2^-ev into sm.page.
 template <int N, int D, int NS, typename S>
 __device__ __forceinline__ void copy_tiles(const Kv8AttnArgs& a, const Start& start, int64_t count, const CUtensorMap& kmap,
                                            const CUtensorMap& vmap, uint8_t* ring, S& sm, volatile int* gave_up) {
@@ -226,15 +228,16 @@ __device__ __forceinline__ void copy_tiles(const Kv8AttnArgs& a, const Start& st
     for (int t = it.t0, g = 0; t < it.t1; ++t, g += ppt, ++i) {
       if ((g & 31) == 0) {  // the next 32 pages' ids and scales, one a lane
         const int page = t * ppt + lane;
-        id = page < pages ? table[page] : -1;
-        if (id >= a.c.num_blocks) id = -1;
+        id = -1;  // behind the sequence
+        if (page < pages) {
+          id = table[page];
+          if (id < 0 || id >= a.c.num_blocks) id = -2;  // outside the pool
+        }
+        ke = ve = 0;
         if (id >= 0) {
           const int64_t s = static_cast<int64_t>(id) * a.c.H + it.h;
           ke = kv8_exp(a.c.ks[s]);
           ve = kv8_exp(a.c.vs[s]);
-        } else {
-          ke = kBadPage;
-          ve = 0;
         }
       }
       const int from = (g & 31) + (lane & (ppt - 1));
@@ -251,8 +254,8 @@ __device__ __forceinline__ void copy_tiles(const Kv8AttnArgs& a, const Start& st
         if (fill >= NS) ok = bar_wait(smem_addr(&sm.empty[slot]), (fill / NS - 1) & 1, gave_up);
         ok = __all_sync(0xffffffffu, ok);
         if (part == 0 && lane < ppt) {
-          sm.kexp[i % kMetaRing][lane] = my_ke;
-          sm.vexp[i % kMetaRing][lane] = my_ve;
+          sm.page[i % kMetaRing][lane] =
+              make_float4(my_id != -2 ? pow2i(my_ke) : __int_as_float(0x7fffffff), static_cast<float>(my_ve), pow2i(-my_ve), 0.f);
         }
         __syncwarp();
         if (!ok) continue;  // a wait gave up: no copy is started any more

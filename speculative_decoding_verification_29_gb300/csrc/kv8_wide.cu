@@ -24,6 +24,8 @@
 // Four more warps convert tiles and load queries, one copies, one issues.
 #include <string.h>
 
+#include <type_traits>
+
 #include "kv8_attn.cuh"
 
 namespace specv {
@@ -37,20 +39,20 @@ template <int D_, bool PAIR_>
 struct Wide {
   static constexpr int D = D_, N = PAIR_ ? 256 : 128;
   static constexpr bool PAIR = PAIR_;
-  static constexpr int kThreads = 3 * 128 + 64;
+  static constexpr int kThreads = 4 * 128;  // two softmax groups, conversions, one of copies and products
   static constexpr int kF8 = kTile * D, kF16 = 2 * kF8;  // a tile of keys or values
   static constexpr int kPanel = kTile * 128;             // 64 columns of f16
   static constexpr int kQ = (PAIR ? 2 : 1) * kF16;
   static constexpr int NF = PAIR ? 3 : 4;  // f16 tiles
   struct Item {
-    int b, first, n, ctx, rows, end, r0, h, t0, t1, tiles, eq;
+    int b, first, n, ctx, rows, end, part, r0, h, t0, t1, tiles, eq;
   };
   struct Small {
     alignas(16) Item item[kItems];
     float ref[2][2][kTile], sum[2][2][kTile];  // of two items: each stream's rows, exchanged at an item's end
     float red[4];
     int nan[kItems];
-    int kexp[kMetaRing][kMaxPages], vexp[kMetaRing][kMaxPages];
+    alignas(16) float4 page[kMetaRing][kMaxPages];
     alignas(8) uint64_t full[8], empty[8], full16[4], empty16[4], s_full[2], p_ready[2], o_full[2], q_ready[kItems], q_free,
         done, drain;
     uint32_t tmem;
@@ -125,9 +127,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     return (nt + 1 - stream) / 2;
   };
 
-  if (work && warp == kLoadWarp) {
-    copy_tiles<N, D, NS>(a, start, hi - lo, kmap, vmap, ring, sm, gave_up);
-  } else if (work && warp == kMmaWarp) {
+  auto products = [&]() {
     // ---- products: the warp waits together, one lane issues
     constexpr uint32_t id_s = instr_desc_f16(kTile, kTile, false), id_o = instr_desc_f16(kTile, D, true);
     const uint32_t q_at = smem_addr(q_smem), f_at = smem_addr(f16);
@@ -200,7 +200,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (work && warp >= kConvWarp && warp < kLoadWarp) {
+  };
+
+  auto convert_tiles = [&]() {
     // ---- an item's queries, then its tiles, into f16: a thread owns a row
     const int own = tid - kConvWarp * 32, quarter = warp - kConvWarp;
     const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (a.qst * 2) | (a.qsh * 2)) & 15) == 0;
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       };
       float amax = 0.f;
       for (int row = own; row < r.rows; row += kTile) {
-#pragma unroll 4
+#pragma unroll 2
         for (int d = 0; d < D; d += 8) {
           float x[8];
           chunk(row, d, x);
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       if (seg > 0) bar_wait(smem_addr(&sm.q_free), (seg - 1) & 1, gave_up);
       for (int row = own; row < r.rows; row += kTile) {
         uint8_t* to = q_smem + (row / kTile) * C::kF16 + own * 128;
-#pragma unroll 4
+#pragma unroll 2
         for (int d = 0; d < D; d += 8) {
           float x[8];
           chunk(row, d, x);
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       if (own == 0) {
         sm.nan[seg & 3] = 0;
-        sm.item[seg & 3] = {r.b, r.first, r.n, r.ctx, r.rows, r.end, r0, it.h, it.t0, it.t1, r.tiles, eq};
+        sm.item[seg & 3] = {r.b, r.first, r.n, r.ctx, r.rows, r.end, r.part, r0, it.h, it.t0, it.t1, r.tiles, eq};
       }
       fence_async_shared();
       named_sync(2, 128);  // the flag is cleared before a tile of the item sets it
@@ -267,8 +269,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 
       for (int t = it.t0; t < it.t1; ++t, ++i) {
         const int slot = t * kTile + own;
-        const bool masked = t * kTile + kTile > r.ctx;  // not every row sees every slot
-#pragma unroll
+        const bool masked = t >= r.part;  // not every row sees every slot
+#pragma unroll 1
         for (int part = 0; part < 2; ++part) {
           const uint32_t j = 2u * i + part, from = j % NS, to = j % NF;
           bar_wait(smem_addr(&sm.full[from]), (j / NS) & 1, gave_up);
@@ -278,30 +280,34 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           // a row of D bytes is swizzled within 128 bytes, or within 64 by the row's second and third bit
           const uint32_t src_turn = D == 128 ? turn : static_cast<uint32_t>((own >> 1) & 3) << 4;
           bool nan = false;
+          auto convert = [&](auto check) {
+#pragma unroll(decltype(check)::value ? 1 : D / 16)
+            for (int c = 0; c < D / 16; ++c) {
+              uint4 u = *reinterpret_cast<const uint4*>(src + ((16u * c) ^ src_turn));
+              uint32_t* w = &u.x;
+              if (decltype(check)::value) {
+                // Slots behind the sequence hold no values, and a NaN value must not reach the rows that do not see it
+                // through a weight of 0: both are cleared here, and the rows that see a NaN get it at the item's end.
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            uint4 u = *reinterpret_cast<const uint4*>(src + ((16u * c) ^ src_turn));
-            uint32_t* w = &u.x;
-            if (part == 1 && masked) {
-              // Slots behind the sequence hold no values, and a NaN value must not reach the rows that do not see it
-              // through a weight of 0: both are cleared here, and the rows that see a NaN get it at the item's end.
+                for (int z = 0; z < 4; ++z) {
+                  const uint32_t m = slot >= r.end ? 0xffffffffu : __vcmpeq4(w[z] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                  nan |= m != 0;
+                  w[z] &= ~m;
+                }
+              }
+              uint32_t v[8];
 #pragma unroll
               for (int z = 0; z < 4; ++z) {
-                const uint32_t m = slot >= r.end ? 0xffffffffu : __vcmpeq4(w[z] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                nan |= m != 0;
-                w[z] &= ~m;
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v[2 * z]) : "h"(static_cast<uint16_t>(w[z] & 0xffff)));
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v[2 * z + 1]) : "h"(static_cast<uint16_t>(w[z] >> 16)));
               }
+              uint8_t* panel = dst + (c / 4) * C::kPanel;
+              *reinterpret_cast<uint4*>(panel + ((32u * (c % 4)) ^ turn)) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(panel + ((32u * (c % 4) + 16u) ^ turn)) = make_uint4(v[4], v[5], v[6], v[7]);
             }
-            uint32_t v[8];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v[2 * z]) : "h"(static_cast<uint16_t>(w[z] & 0xffff)));
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v[2 * z + 1]) : "h"(static_cast<uint16_t>(w[z] >> 16)));
-            }
-            uint8_t* panel = dst + (c / 4) * C::kPanel;
-            *reinterpret_cast<uint4*>(panel + ((32u * (c % 4)) ^ turn)) = make_uint4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<uint4*>(panel + ((32u * (c % 4) + 16u) ^ turn)) = make_uint4(v[4], v[5], v[6], v[7]);
-          }
+          };
+          if (part == 1 && masked) convert(std::true_type{});
+          else convert(std::false_type{});
           if (nan && slot < r.end) sm.nan[seg & 3] = 1;
           fence_async_shared();
           __syncwarp();
@@ -317,7 +323,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     if (own == 0) sm.item[seg & 3].t0 = sm.item[seg & 3].t1 = 0;  // no further item
     __syncwarp();
     if (lane == 0) bar_arrive(smem_addr(&sm.q_ready[seg & 3]));
-  } else if (work && warp < kConvWarp) {
+  };
+
+  auto softmax = [&]() {
     // ---- weights and sums: a thread owns a row of its stream
     const int b = uniform(warp >> 2), quarter = uniform(warp & 3);
     const int own = quarter * 32 + lane;
@@ -341,56 +349,59 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const int row = PAIR ? b * kTile + own : own;  // within the item
       const bool rows_here = (PAIR ? b * kTile : 0) + quarter * 32 < rows;
       const float scale = a.scale * pow2i(it.eq);
+      // slots before this are seen by all of the warp's rows
+      const int warp_row = it.r0 + (PAIR ? b * kTile : 0) + quarter * 32;
+      const int all_seen = uniform(ctx + (a.tree ? 0 : min(it.n - 1, warp_row / a.group) + 1));
       float ref = kNegInf, l = 0.f;
       for (int s = 0; s < steps_here; ++s) {
         const int step = PAIR ? s : 2 * s + b, ti = base + step, slot0 = (t0 + step) * kTile;
-        const int* ke_at = sm.kexp[ti % kMetaRing];
-        const int* ve_at = sm.vexp[ti % kMetaRing];
+        const float4* pages = sm.page[ti % kMetaRing];
         bar_wait(smem_addr(&sm.s_full[b]), (count_here + s) & 1, gave_up);
         fence_after();
         if (rows_here) {
-          const bool masked = slot0 + kTile > ctx;
-          uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+          const bool masked = slot0 + kTile > all_seen;
+          uint64_t vis[2] = {~0ull, ~0ull};  // slots of the tile that the row sees
           if (masked) {
             const int token = min(it.n - 1, static_cast<int>(static_cast<uint32_t>(it.r0 + row) / static_cast<uint32_t>(a.group)));
             const int seen = (a.tree ? ctx : ctx + token + 1) - slot0;  // slots before this are seen
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              vis[k] = seen >= 32 * k + 32 ? 0xffffffffu : (seen <= 32 * k ? 0u : (1u << (seen - 32 * k)) - 1u);
+            for (int k = 0; k < 2; ++k)
+              vis[k] = seen >= 64 * k + 64 ? ~0ull : (seen <= 64 * k ? 0ull : (1ull << (seen - 64 * k)) - 1ull);
             if (a.tree) {
               const uint8_t* m8 = a.tree + (static_cast<int64_t>(it.b) * a.max_tokens + token) * a.max_tokens - ctx + slot0;
               const int from = max(0, seen), to = min(kTile, it.end - slot0);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-#pragma unroll 8
-                for (int c = max(from, 32 * k); c < min(to, 32 * k + 32); ++c)
-                  if (m8[c]) vis[k] |= 1u << (c - 32 * k);
+#pragma unroll 4
+              for (int c = from; c < to; ++c) {
+                const uint64_t bit = static_cast<uint64_t>(m8[c] != 0) << (c & 63);
+                vis[0] |= c < 64 ? bit : 0ull;
+                vis[1] |= c < 64 ? 0ull : bit;
+              }
             }
           }
+          auto bits = [&](int g) { return static_cast<uint32_t>((g < 4 ? vis[0] : vis[1]) >> (16 * (g & 3))); };
           // the largest exponent; NaN scores are passed over here
           float m = kNegInf;
+          uint32_t x[kTile];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t x[32];
-            tmem_ld<32>(s_at + 32 * k, x);
-            wait_ld();
-            if (masked) {
+          for (int k = 0; k < 4; ++k) tmem_ld<32>(s_at + 32 * k, x + 32 * k);
+          wait_ld();
+          if (masked) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!((vis[k] >> j) & 1)) x[j] = 0xff800000u;
+            for (int g = 0; g < 8; ++g) {
+              const uint32_t v = bits(g);
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (!((v >> j) & 1)) x[16 * g + j] = 0xff800000u;
             }
+          }
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              float top[4];
+          for (int g = 0; g < 8; ++g) {
+            float top[3] = {__uint_as_float(x[16 * g]), __uint_as_float(x[16 * g + 1]), __uint_as_float(x[16 * g + 2])};
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                top[j] = fmaxf(fmaxf(__uint_as_float(x[16 * g + j]), __uint_as_float(x[16 * g + 4 + j])),
-                               fmaxf(__uint_as_float(x[16 * g + 8 + j]), __uint_as_float(x[16 * g + 12 + j])));
-              const int page = (2 * k + g) >> page_shift, ke = ke_at[page];
-              if (ke != kBadPage)
-                m = fmaxf(m, fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), scale * pow2i(ke),
-                                  static_cast<float>(ve_at[page])));
-            }
+            for (int j = 3; j < 15; ++j) top[j % 3] = fmaxf(top[j % 3], __uint_as_float(x[16 * g + j]));
+            const float4 meta = pages[g >> page_shift];
+            m = fmaxf(m, fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], __uint_as_float(x[16 * g + 15]))), scale * meta.x,
+                              meta.y));
           }
           const bool far = m - ref > kFar;  // true from no reference to any; false for m = -inf
           if (__any_sync(0xffffffffu, far)) {
@@ -415,31 +426,24 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const float from = ref == kNegInf ? 0.f : ref;
           // weights in place of the scores, and their sum
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t x[32], p[16];
-            tmem_ld<32>(s_at + 32 * k, x);
-            wait_ld();
+          for (int g = 0; g < 8; ++g) {
+            const float4 meta = pages[g >> page_shift];
+            float cs = scale * meta.x;
+            if (cs == 0.f) cs = 1e-37f;  // what is not seen stays at -inf
+            const float c0 = meta.y - from;
+            float2 sum = make_float2(0.f, 0.f);
+            uint32_t p[8];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const int page = (2 * k + g) >> page_shift, ke = ke_at[page], ve = ve_at[page];
-              const float cs = ke == kBadPage ? __int_as_float(0x7fffffff) : scale * pow2i(ke);
-              const float c0 = static_cast<float>(ve) - from;
-              float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int j = 16 * g; j < 16 * g + 16; j += 2) {
-                float2 y = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), make_float2(cs, cs),
-                                make_float2(c0, c0));
-                if (masked) {
-                  if (!((vis[k] >> j) & 1)) y.x = kNegInf;
-                  if (!((vis[k] >> (j + 1)) & 1)) y.y = kNegInf;
-                }
-                const float2 w = make_float2(ex2_fast(y.x), ex2_fast(y.y));
-                sum = add2(sum, w);
-                p[j / 2] = half2_bits(w.x, w.y);
-              }
-              l = fmaf(sum.x + sum.y, pow2i(-ve), l);
+            for (int j = 0; j < 16; j += 2) {
+              const int c = 16 * g + j;
+              const float2 y = fma2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), make_float2(cs, cs),
+                                    make_float2(c0, c0));
+              const float2 w = make_float2(ex2_fast(y.x), ex2_fast(y.y));
+              sum = add2(sum, w);
+              p[j / 2] = half2_bits(w.x, w.y);
             }
-            tmem_st16(s_at + 16 * k, p);
+            l = fmaf(sum.x + sum.y, meta.z, l);
+            tmem_st8(s_at + 8 * g, p);
           }
           wait_st();
         }
@@ -496,7 +500,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           }
           if (nan) {  // dimensions in which a value that this row sees is NaN
             const int last = min(it.end, it.t1 * kTile);
-            for (int slot = max(t0, ctx / kTile) * kTile; slot < last; ++slot) {
+            for (int slot = max(t0, it.part) * kTile; slot < last; ++slot) {
               if (slot >= ctx && !sees(a, it.b, tok, slot - ctx)) continue;
               const int id = a.c.table[static_cast<int64_t>(it.b) * a.c.max_blocks + slot / a.c.block];
               if (id < 0 || id >= a.c.num_blocks) continue;
@@ -537,6 +541,19 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       count[0] += n[0];
       count[1] += n[1];
     }
+  };
+
+  // 512 threads of 128 registers; a softmax thread holds a row's 128 scores and takes from the others
+  if (warp < kConvWarp) {
+    more_registers<168>();
+    if (work) softmax();
+  } else if (warp < kLoadWarp) {
+    fewer_registers<80>();
+    if (work) convert_tiles();
+  } else {
+    fewer_registers<96>();
+    if (work && warp == kLoadWarp) copy_tiles<N, D, NS>(a, start, hi - lo, kmap, vmap, ring, sm, gave_up);
+    if (work && warp == kMmaWarp) products();
   }
 
   fence_before();
