@@ -233,6 +233,7 @@ int spec_kv8_attention(const spec_kv8_cache* cache, const void* queries, int64_t
   const int64_t most = static_cast<int64_t>(std::min(max_tokens, std::max(T, 1))) * a.group;  // no sequence has more than T
   const int rows = kv8_attention_rows(static_cast<int64_t>(max_tokens) * a.group);
   a.row_tiles = static_cast<int>((most + rows - 1) / rows);
+  if (static_cast<int64_t>(a.row_tiles) * a.c.B >= (1LL << 31)) return SPEC_ERR_UNSUPPORTED;
   a.parts = kv8_attention_parts(rows);
   const AttnLayout l = attn_layout(rows, a.c.D);
   char* ws = static_cast<char*>(workspace);

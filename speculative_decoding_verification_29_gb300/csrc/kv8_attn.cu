@@ -76,7 +76,7 @@ struct Cfg {
     alignas(8) uint64_t full[12], empty[12], s_full[2], p_ready[2], o_full[2], q_ready[2], q_free[2], drain;
     uint32_t tmem;
     int gave_up;
-    int tmp[36];
+    alignas(8) int tmp[64];
   };
   static constexpr int kBudget = kCtas == 2 ? 115712 : 231424;
   static constexpr int kFixed = 1024 + 2 * kQ + 2 * kP + static_cast<int>(sizeof(Small));
@@ -136,7 +136,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   uint8_t* ring = q_smem + 2 * C::kQ;
   uint8_t* p_smem = ring + NS * C::kSlot;
   typename C::Small& sm = *reinterpret_cast<typename C::Small*>(p_smem + 2 * C::kP);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = uniform(tid >> 5);  // known to be the warp's, so that roles keep their addresses in uniform registers
   constexpr int kQueryWarp = C::W * 4, kLoadWarp = kQueryWarp + C::EW, kMmaWarp = kLoadWarp + 1;
   constexpr uint32_t kO = 2 * N;  // tensor memory: scores at 0 and N, then products
   volatile int* gave_up = &sm.gave_up;
@@ -161,27 +162,31 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   }
   if (warp == kMmaWarp) tmem_alloc(smem_addr(&sm.tmem), C::kCols);
   griddep_wait();
-  int64_t lo, hi, all;
+  Runs runs;
   Start start;
   fence_before();
-  const bool work = find_run<N>(a, blockIdx.x, false, &lo, &hi, &start, &all, sm.tmp);
+  const bool work = uniform(find_run<N>(a, blockIdx.x, false, &runs, &start, sm.tmp)) != 0;
+  const int64_t my_tiles = work ? runs.begin(blockIdx.x + 1) - runs.begin(blockIdx.x) : 0;
   __syncthreads();
   fence_after();
   const uint32_t tmem = uniform(sm.tmem);
 
   if (work && warp == kLoadWarp) {
-    copy_tiles<N, D, NS>(a, start, hi - lo, kmap, vmap, ring, sm, gave_up);
+    copy_tiles<N, D, NS>(a, start, my_tiles, kmap, vmap, ring, sm, gave_up);
   } else if (work && warp == kMmaWarp) {
     // ---- products: the warp waits together, one lane issues
     constexpr uint32_t kStride = 8 * D;
-    const uint32_t ring_at = smem_addr(ring), p_at = smem_addr(p_smem);
+    // D = 64: the two halves of the values' 128 rows are the same 64 dimensions (stride 0 between them)
+    const uint64_t k_desc = smem_desc(smem_addr(ring), 16, kStride, C::kLayout),
+                   v_desc = smem_desc(smem_addr(ring), 0, kStride, C::kLayout),
+                   q_desc = smem_desc(smem_addr(q_smem), 16, kStride, C::kLayout),
+                   p_desc = smem_desc(smem_addr(p_smem), 1024, 1024, 2);
     for (int i = 0, seg = 0;; ++seg) {
       bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 1]), (seg >> 1) & 1, gave_up);
       ok = __all_sync(0xffffffffu, ok);
       const int t0 = uniform(sm.item[seg & 1].t0), t1 = uniform(sm.item[seg & 1].t1);
       if (!ok || t1 <= t0) break;
       fence_after();
-      const uint32_t q_at = uniform(smem_addr(q_smem) + (seg & 1) * C::kQ);
       constexpr uint32_t id_s = instr_desc(kTile, N, false), id_o = instr_desc(kTile, N, true);
       auto scores = [&](int j) {  // S[j & 1] = K tile x Q^T
         const uint32_t slot = uniform((2u * j) % NS), to = uniform(tmem + (j & 1) * N);
@@ -190,13 +195,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         if (!ok) return;
         fence_after();
         if (elect()) {
-          const uint64_t kd = smem_desc(ring_at + slot * C::kSlot, 16, kStride, C::kLayout);
+          const uint64_t kd = k_desc + (slot * C::kSlot >> 4), qd = q_desc + ((seg & 1) * C::kQ >> 4);
 #pragma unroll
-          for (int t = 0; t < C::TERMS; ++t) {
-            const uint64_t qd = smem_desc(q_at + t * N * D, 16, kStride, C::kLayout);
+          for (int t = 0; t < C::TERMS; ++t)
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) mma_f8(to, kd + 2 * k, qd + 2 * k, id_s, t > 0 || k > 0);
-          }
+            for (int k = 0; k < D / 32; ++k) mma_f8(to, kd + 2 * k, qd + (2 * k + (t * N * D >> 4)), id_s, t > 0 || k > 0);
           commit(smem_addr(&sm.empty[slot]));
           commit(smem_addr(&sm.s_full[j & 1]));
         }
@@ -205,23 +208,20 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       scores(i);
       for (int t = t0; t < t1; ++t, ++i) {
         if (t + 1 < t1) scores(i + 1);
-        const uint32_t slot = uniform((2u * i + 1) % NS), to = uniform(tmem + kO + (i & 1) * N),
-                       p_now = uniform(p_at + (i & 1) * C::kP);
+        const uint32_t slot = uniform((2u * i + 1) % NS), to = uniform(tmem + kO + (i & 1) * N);
         ok = bar_wait(smem_addr(&sm.full[slot]), ((2u * i + 1) / NS) & 1, gave_up) &&
              bar_wait(smem_addr(&sm.p_ready[i & 1]), (i >> 1) & 1, gave_up);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         fence_after();
         if (elect()) {
-          // D = 64: the two halves of the 128 rows are the same 64 dimensions (stride 0 between them)
-          const uint64_t vd = smem_desc(ring_at + slot * C::kSlot, 0, kStride, C::kLayout);
+          const uint64_t vd = v_desc + (slot * C::kSlot >> 4), pd = p_desc + ((i & 1) * C::kP >> 4);
 #pragma unroll
           for (int u = 0; u < C::TERMS; ++u) {
-            constexpr uint32_t kPanel = kTile * 128;
-            const uint64_t pd = smem_desc(p_now + (u * C::kTerm / 128) * kPanel + u * C::kTerm % 128, 1024, 1024, 2);
+            const uint32_t off = (u * C::kTerm / 128) * (kTile * 128) + u * C::kTerm % 128;
 #pragma unroll
             for (int k = 0; k < kTile / 32; ++k)
-              mma_f8(to, vd + (k * 32 * D >> 4), pd + (k * 4096 >> 4), id_o, u > 0 || k > 0);
+              mma_f8(to, vd + (k * 32 * D >> 4), pd + ((off + k * 4096) >> 4), id_o, u > 0 || k > 0);
           }
           commit(smem_addr(&sm.empty[slot]));
           commit(smem_addr(&sm.o_full[i & 1]));
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   } else if (work && warp >= kQueryWarp && warp < kLoadWarp) {
     // ---- the items' queries, one item ahead: a thread owns a row
     const int own = tid - kQueryWarp * 32, quarter = warp - kQueryWarp;
-    Walk<N> it(a, start, hi - lo);
+    Walk<N> it(a, start, my_tiles);
     const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (a.qst * 2) | (a.qsh * 2)) & 15) == 0;
     int seg = 0;
     do {
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 1]), (seg >> 1) & 1, gave_up);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {  // the group's other warps may be a few barriers behind
-        for (int64_t k = 0; k < 2 * (hi - lo) + 2; ++k) named_arrive(3 + wg, 128);
+        for (int64_t k = 0; k < 2 * my_tiles + 2; ++k) named_arrive(3 + wg, 128);
         break;
       }
       const typename C::Item& it = sm.item[seg & 1];

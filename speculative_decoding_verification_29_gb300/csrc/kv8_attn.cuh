@@ -54,15 +54,15 @@ __device__ __forceinline__ RowTile row_tile(const Kv8AttnArgs& a, int b, int rt)
   r.rt = rt;
   const int lo = a.cu[b], hi = a.cu[b + 1], len = a.c.len[b];
   if (!kv8_seq_ok(a.c, a.T, lo, hi, len) || hi - lo > a.max_tokens) return r;
-  const int64_t rows = static_cast<int64_t>(hi - lo) * a.group, r0 = static_cast<int64_t>(rt) * N;
+  const int rows = (hi - lo) * a.group, r0 = rt * N;  // below 2^31: the host has checked all rows
   if (r0 >= rows) return r;
   r.first = lo;
   r.n = hi - lo;
   r.ctx = len;
-  r.rows = static_cast<int>(min(rows - r0, static_cast<int64_t>(N)));
-  r.end = len + (a.tree ? r.n : static_cast<int>((r0 + r.rows - 1) / a.group) + 1);
+  r.rows = min(rows - r0, N);
+  r.end = len + (a.tree ? r.n : (r0 + r.rows - 1) / a.group + 1);
   r.tiles = (r.end + kTile - 1) / kTile;
-  r.part = (len + (a.tree ? 0 : static_cast<int>(r0 / a.group) + 1)) / kTile;
+  r.part = (len + (a.tree ? 0 : r0 / a.group + 1)) / kTile;
   return r;
 }
 
@@ -71,76 +71,88 @@ struct Start {
   int b, rt, h, t;
 };
 
-// All threads of the block: the run [lo, hi) of part `part` and its first tile.
-// With `last`, the place of tile hi - 1 instead. s_tmp: 34 words of shared memory.
+// Parts are equal runs of the tiles of all items, the first `more` of them one longer.
+struct Runs {
+  int64_t all, each;  // tiles, tiles of a run
+  int parts, more;
+  __device__ __forceinline__ int64_t begin(int part) const { return part * each + min(part, more); }
+};
+
+// All threads of the block: the runs, and where tile begin(part) lies, or with
+// `last` tile begin(part + 1) - 1. False where the part has no tile. s_tmp: 34
+// words of shared memory.
 template <int N>
-__device__ __forceinline__ bool find_run(const Kv8AttnArgs& a, int part, bool last, int64_t* lo, int64_t* hi, Start* s,
-                                         int64_t* all_tiles, int* s_tmp) {
+__device__ __forceinline__ bool find_run(const Kv8AttnArgs& a, int part, bool last, Runs* runs, Start* s, int* s_tmp) {
   const int nthr = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = nthr >> 5;
-  const int64_t cand = static_cast<int64_t>(a.c.B) * a.row_tiles;
-  int64_t total = 0;
-  int v0 = 0, incl0 = 0;  // this thread's candidate of the first round
-  for (int64_t base = 0; base < cand; base += nthr) {
-    const int64_t i = base + tid;
+  const uint32_t cand = static_cast<uint32_t>(a.c.B) * static_cast<uint32_t>(a.row_tiles);  // below 2^31
+  // Sums over the candidates base .. base + nthr - 1, one a thread: up to this one's, and all.
+  auto scan = [&](uint32_t base, int* tiles, int64_t* upto, int64_t* sum) {
+    const uint32_t i = base + tid;
     int v = 0;
-    if (i < cand) v = row_tile<N>(a, static_cast<int>(i / a.row_tiles), static_cast<int>(i % a.row_tiles)).tiles;
-    int x = v;
-#pragma unroll
+    if (i < cand) {
+      const uint32_t b = i / static_cast<uint32_t>(a.row_tiles);
+      v = row_tile<N>(a, static_cast<int>(b), static_cast<int>(i - b * a.row_tiles)).tiles;
+    }
+    int64_t x = v;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) s_tmp[warp] = x;
+    int64_t* at = reinterpret_cast<int64_t*>(s_tmp);
+    if (lane == 31) at[warp] = x;
     __syncthreads();
-    int before = 0, sum = 0;
+    int64_t before = 0, total = 0;
+#pragma unroll 1
     for (int w = 0; w < nw; ++w) {
-      if (w < warp) before += s_tmp[w];
-      sum += s_tmp[w];
+      if (w < warp) before += at[w];
+      total += at[w];
     }
     __syncthreads();
-    if (base == 0) v0 = v, incl0 = x + before;
-    total += sum;
-  }
-  const int64_t all = total * a.c.H;
-  const int64_t parts = min(static_cast<int64_t>(a.parts), all);
-  *all_tiles = all;
-  *lo = part < parts ? all * part / parts : all;
-  *hi = part < parts ? all * (part + 1) / parts : all;
-  if (*lo >= *hi) return false;
-  const int64_t want = last ? *hi - 1 : *lo;
-  int64_t run = 0;
-  for (int64_t base = 0; base < cand; base += nthr) {
-    const int64_t i = base + tid;
-    int v = v0, incl = incl0, sum = 0;
-    if (base > 0 || cand > nthr) {
-      v = 0;
-      if (i < cand) v = row_tile<N>(a, static_cast<int>(i / a.row_tiles), static_cast<int>(i % a.row_tiles)).tiles;
-      int x = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+    *tiles = v;
+    *upto = x + before;
+    *sum = total;
+  };
+  int64_t total = 0, want = 0, run = 0;
+  bool found = true;
+  // the first round's sums serve both the total and the search, as long as there is one round
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (uint32_t base = 0; base < cand; base += nthr) {
+      int v;
+      int64_t upto, sum;
+      scan(base, &v, &upto, &sum);
+      if (pass == 0) total += sum;
+      if (pass == 0 && cand <= static_cast<uint32_t>(nthr)) pass = 1;
+      if (pass == 0) continue;
+      if (run == 0 && base == 0) {
+        const int64_t all = total * a.c.H;
+        runs->all = all;
+        runs->parts = static_cast<int>(min(static_cast<int64_t>(a.parts), all));
+        if (part >= runs->parts) {
+          found = false;
+          break;
+        }
+        runs->each = all / runs->parts;
+        runs->more = static_cast<int>(all - runs->each * runs->parts);
+        want = last ? runs->begin(part + 1) - 1 : runs->begin(part);
       }
-      if (lane == 31) s_tmp[warp] = x;
-      __syncthreads();
-      int before = 0;
-      for (int w = 0; w < nw; ++w) {
-        if (w < warp) before += s_tmp[w];
-        sum += s_tmp[w];
+      const int64_t from = (run + upto - v) * a.c.H;
+      if (v > 0 && want >= from && want < (run + upto) * a.c.H) {
+        const uint32_t i = base + tid, b = i / static_cast<uint32_t>(a.row_tiles);
+        int64_t off = want - from;
+        int h = 0;
+        for (; off >= v; off -= v) ++h;  // at most kv_heads steps
+        s_tmp[0] = static_cast<int>(b);
+        s_tmp[1] = static_cast<int>(i - b * a.row_tiles);
+        s_tmp[2] = h;
+        s_tmp[3] = static_cast<int>(off);
       }
-      __syncthreads();
-      incl = x + before;
+      run += sum;
+      if (run * a.c.H > want) break;  // the same for every thread
     }
-    const int64_t from = (run + incl - v) * a.c.H, to = (run + incl) * a.c.H;
-    if (v > 0 && want >= from && want < to) {
-      const int off = static_cast<int>((want - from) / v);
-      s_tmp[0] = static_cast<int>(i / a.row_tiles);
-      s_tmp[1] = static_cast<int>(i % a.row_tiles);
-      s_tmp[2] = off;
-      s_tmp[3] = static_cast<int>((want - from) - static_cast<int64_t>(off) * v);
-    }
-    run += sum;
-    if (cand > nthr && run * a.c.H > want) break;  // the same for every thread
+    if (cand == 0 || !found) break;
   }
   __syncthreads();
   s->b = s_tmp[0];
@@ -148,7 +160,7 @@ __device__ __forceinline__ bool find_run(const Kv8AttnArgs& a, int part, bool la
   s->h = s_tmp[2];
   s->t = s_tmp[3];
   __syncthreads();
-  return true;
+  return found;
 }
 
 // Walks the items of a run: (r, h) with tiles [t0, t1).
@@ -283,7 +295,7 @@ constexpr int kJoinThreads = 256;
 
 template <typename QT, int D, int N>
 __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ Kv8AttnArgs a) {
-  __shared__ int s_tmp[36];
+  __shared__ __align__(8) int s_tmp[64];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_launch_dependents();
   if (blockIdx.x >= static_cast<unsigned>(a.parts)) {  // a warp per sequence: row_status
@@ -306,25 +318,25 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
     late = __any_sync(0xffffffffu, late);
     if (lane == 0) a.row_status[b] = (bad ? SPEC_ROW_CACHE : 0) | (late ? SPEC_ROW_TIMEOUT : 0);
     if (!sound && lo >= 0 && hi > lo && hi <= a.T) {
-      const int64_t rows = static_cast<int64_t>(hi - lo) * a.q_heads;
-      for (int64_t i = 0; i < rows; ++i) {
-        QT* out = static_cast<QT*>(a.out) + (lo + i / a.q_heads) * a.ost + (i % a.q_heads) * a.osh;
-        for (int d = lane; d < D; d += 32) out[d] = from_f<QT>(__int_as_float(0x7fffffff));
-      }
+#pragma unroll 1
+      for (int t = lo; t < hi; ++t)
+#pragma unroll 1
+        for (int h = 0; h < a.q_heads; ++h)
+          for (int d = lane; d < D; d += 32)
+            static_cast<QT*>(a.out)[t * a.ost + h * a.osh + d] = from_f<QT>(__int_as_float(0x7fffffff));
     }
     return;
   }
-  int64_t lo, hi, all;
+  Runs runs;
   Start s;
-  if (!find_run<N>(a, blockIdx.x, true, &lo, &hi, &s, &all, s_tmp)) return;
+  if (!find_run<N>(a, blockIdx.x, true, &runs, &s, s_tmp)) return;
   const RowTile r = row_tile<N>(a, s.b, s.rt);
+  const int64_t lo = runs.begin(blockIdx.x), hi = runs.begin(blockIdx.x + 1);
   const int64_t begin = hi - 1 - s.t, end = begin + r.tiles;  // the item's tiles
   const int row = blockIdx.y * (kJoinThreads / 32) + warp;
   if (begin < lo || end <= hi || row >= r.rows) return;
-  const int64_t parts = min(static_cast<int64_t>(a.parts), all);
-  int64_t last = (end - 1) * parts / all;
-  while (all * (last + 1) / parts <= end - 1) ++last;
-  const int n = static_cast<int>(last - blockIdx.x) + 1;
+  int n = 2;  // shares
+  while (runs.begin(blockIdx.x + n) < end) ++n;
   griddep_wait();
   const int64_t first = blockIdx.x;
   auto share = [&](int i) { return (2 * (first + i) + (i == 0 ? 1 : 0)) * N + row; };
@@ -352,9 +364,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = fmaf(w, x[k], acc[k]);
   }
-  const int64_t item_row = static_cast<int64_t>(s.rt) * N + row, tok = item_row / a.group;
-  QT* out = static_cast<QT*>(a.out) + (r.first + tok) * a.ost +
-            (s.h * a.group + static_cast<int>(item_row - tok * a.group)) * a.osh + lane * V;
+  const int item_row = s.rt * N + row, tok = item_row / a.group;
+  QT* out = static_cast<QT*>(a.out) + (r.first + static_cast<int64_t>(tok)) * a.ost +
+            (s.h * a.group + (item_row - tok * a.group)) * a.osh + lane * V;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
   for (int k = 0; k < V; ++k) out[k] = from_f<QT>(acc[k] * inv);

@@ -21,7 +21,7 @@
 // share the tiles. Otherwise they share the rows (128), take every other tile
 // and are added up at the item's end: both read each other's accumulator, since a
 // row has the same lane in both.
-// Four more warps convert tiles and load queries, one copies, one issues.
+// Four more warps convert tiles and load queries, one copies, one issues each stream's products.
 #include <string.h>
 
 #include <type_traits>
@@ -54,10 +54,10 @@ struct Wide {
     int nan[kItems];
     alignas(16) float4 page[kMetaRing][kMaxPages];
     alignas(8) uint64_t full[8], empty[8], full16[4], empty16[4], s_full[2], p_ready[2], o_full[2], q_ready[kItems], q_free,
-        done, drain;
+        done, drain[2];
     uint32_t tmem;
     int gave_up;
-    int tmp[36];
+    alignas(8) int tmp[64];
   };
   static constexpr int kFixed = 1024 + kQ + NF * kF16 + static_cast<int>(sizeof(Small));
   static constexpr int kFit = (231424 - kFixed) / kF8;
@@ -84,7 +84,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   uint8_t* f16 = q_smem + C::kQ;
   uint8_t* ring = f16 + NF * C::kF16;
   typename C::Small& sm = *reinterpret_cast<typename C::Small*>(ring + NS * C::kF8);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = uniform(tid >> 5);  // known to be the warp's, so that roles keep their addresses in uniform registers
   constexpr int kConvWarp = 8, kLoadWarp = 12, kMmaWarp = 13;
   constexpr uint32_t kO = 256;  // tensor memory: scores (and weights) of the streams at 0 and 128, outputs behind
   volatile int* gave_up = &sm.gave_up;
@@ -96,17 +97,17 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     for (int i = 0; i < NF; ++i) {
       bar_init(smem_addr(&sm.full16[i]), 4);
-      bar_init(smem_addr(&sm.empty16[i]), 1);
+      bar_init(smem_addr(&sm.empty16[i]), 2);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(smem_addr(&sm.s_full[i]), 1);
       bar_init(smem_addr(&sm.p_ready[i]), 4);
       bar_init(smem_addr(&sm.o_full[i]), 1);
+      bar_init(smem_addr(&sm.drain[i]), 1);
     }
     for (int i = 0; i < kItems; ++i) bar_init(smem_addr(&sm.q_ready[i]), 4);
-    bar_init(smem_addr(&sm.q_free), 1);
+    bar_init(smem_addr(&sm.q_free), 2);
     bar_init(smem_addr(&sm.done), 8);
-    bar_init(smem_addr(&sm.drain), 1);
     fence_bar_init();
     sm.gave_up = 0;
     prefetch_map(&kmap);
@@ -114,10 +115,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   }
   if (warp == kMmaWarp) tmem_alloc(smem_addr(&sm.tmem), 512);
   griddep_wait();
-  int64_t lo, hi, all;
+  Runs runs;
   Start start;
   fence_before();
-  const bool work = find_run<N>(a, blockIdx.x, false, &lo, &hi, &start, &all, sm.tmp);
+  const bool work = uniform(find_run<N>(a, blockIdx.x, false, &runs, &start, sm.tmp)) != 0;
+  const int64_t my_tiles = work ? runs.begin(blockIdx.x + 1) - runs.begin(blockIdx.x) : 0;
   __syncthreads();
   fence_after();
   const uint32_t tmem = uniform(sm.tmem);
@@ -127,76 +129,73 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     return (nt + 1 - stream) / 2;
   };
 
-  auto products = [&]() {
-    // ---- products: the warp waits together, one lane issues
+  // ---- products of one stream: the warp waits together, one lane issues
+  auto products = [&](auto stream) {
+    constexpr int b = decltype(stream)::value;
     constexpr uint32_t id_s = instr_desc_f16(kTile, kTile, false), id_o = instr_desc_f16(kTile, D, true);
-    const uint32_t q_at = smem_addr(q_smem), f_at = smem_addr(f16);
-    int base = 0, count[2] = {0, 0};  // tiles and steps of earlier items
+    const uint64_t q_desc = smem_desc(smem_addr(q_smem) + (PAIR ? b * C::kF16 : 0), 16, 1024, 2),
+                   k_desc = smem_desc(smem_addr(f16), 16, 1024, 2), v_desc = smem_desc(smem_addr(f16), C::kPanel, 1024, 2);
+    int base = 0, count = 0;  // tiles and steps of earlier items
     for (int seg = 0;; ++seg) {
       bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 3]), (seg >> 2) & 1, gave_up);
       ok = __all_sync(0xffffffffu, ok);
       const int nt = uniform(sm.item[seg & 3].t1 - sm.item[seg & 3].t0), rows = uniform(sm.item[seg & 3].rows);
       if (!ok || nt <= 0) break;
       fence_after();
-      const int n0 = steps(nt, rows, 0), n1 = steps(nt, rows, 1);
-      auto scores = [&](int b, int s) {  // S[b] = Q x K^T
-        const uint32_t j = 2u * (base + (PAIR ? s : 2 * s + b)), slot = uniform(j % NF);
-        bool ok = bar_wait(smem_addr(&sm.full16[slot]), (j / NF) & 1, gave_up);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
-        fence_after();
-        const bool last = n1 == n0 ? b == 1 && s == n1 - 1 : b == 0 && s == n0 - 1;
-        if (elect()) {
-          const uint64_t qd = smem_desc(q_at + (PAIR ? b * C::kF16 : 0), 16, 1024, 2),
-                         kd = smem_desc(f_at + slot * C::kF16, 16, 1024, 2);
+      const int n = steps(nt, rows, b);
+      const bool alone = !PAIR || steps(nt, rows, 1) == 0;  // the tiles' only user
+      if (n == 0 && elect()) bar_arrive(smem_addr(&sm.q_free));
+#pragma unroll 1
+      for (int s = -1; s < n; ++s) {
+        if (s >= 0) {  // O += P x V
+          const uint32_t j = 2u * (base + (PAIR ? s : 2 * s + b)) + 1, slot = uniform(j % NF);
+          // the last item's outputs have been read
+          if (s == 0 && seg > 0) ok = bar_wait(smem_addr(&sm.done), (seg - 1) & 1, gave_up);
+          ok = bar_wait(smem_addr(&sm.full16[slot]), (j / NF) & 1, gave_up) &&
+               bar_wait(smem_addr(&sm.p_ready[b]), (count + s) & 1, gave_up) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          fence_after();
+          const uint32_t add = uniform(s > 0);
+          if (elect()) {
+            const uint64_t vd = v_desc + (slot * C::kF16 >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const int off = ((k / 4) * C::kPanel + (k % 4) * 32) >> 4;
-            mma_f16(tmem + b * kTile, qd + off, kd + off, id_s, k > 0);
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_f16_tmem(tmem + kO + b * kTile, tmem + b * kTile + 8 * k, vd + (k * 2048 >> 4), id_o, k > 0 ? 1 : add);
+            commit(smem_addr(&sm.o_full[b]));
+            commit(smem_addr(&sm.empty16[slot]));
+            if (alone) commit(smem_addr(&sm.empty16[slot]));
           }
-          if (!PAIR || b == 1 || n1 == 0) commit(smem_addr(&sm.empty16[slot]));
-          commit(smem_addr(&sm.s_full[b]));
-          if (last) commit(smem_addr(&sm.q_free));
+          __syncwarp();
         }
-        __syncwarp();
-      };
-      auto product = [&](int b, int s) {  // O[b] += P[b] x V
-        const uint32_t j = 2u * (base + (PAIR ? s : 2 * s + b)) + 1, slot = uniform(j % NF);
-        bool ok = bar_wait(smem_addr(&sm.full16[slot]), (j / NF) & 1, gave_up) &&
-                  bar_wait(smem_addr(&sm.p_ready[b]), (count[b] + s) & 1, gave_up);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
-        fence_after();
-        if (elect()) {
-          const uint64_t vd = smem_desc(f_at + slot * C::kF16, C::kPanel, 1024, 2);
+        if (s + 1 < n) {  // the next S = Q x K^T
+          const uint32_t j = 2u * (base + (PAIR ? s + 1 : 2 * (s + 1) + b)), slot = uniform(j % NF);
+          ok = bar_wait(smem_addr(&sm.full16[slot]), (j / NF) & 1, gave_up);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          fence_after();
+          if (elect()) {
+            const uint64_t kd = k_desc + (slot * C::kF16 >> 4);
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_f16_tmem(tmem + kO + b * kTile, tmem + b * kTile + 8 * k, vd + (k * 2048 >> 4), id_o, s > 0 || k > 0);
-          if (!PAIR || b == 1 || n1 == 0) commit(smem_addr(&sm.empty16[slot]));
-          commit(smem_addr(&sm.o_full[b]));
+            for (int k = 0; k < D / 16; ++k) {
+              const int off = ((k / 4) * C::kPanel + (k % 4) * 32) >> 4;
+              mma_f16(tmem + b * kTile, q_desc + off, kd + off, id_s, k > 0);
+            }
+            commit(smem_addr(&sm.s_full[b]));
+            commit(smem_addr(&sm.empty16[slot]));
+            if (alone) commit(smem_addr(&sm.empty16[slot]));
+            if (s + 2 == n) commit(smem_addr(&sm.q_free));
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      };
-      scores(0, 0);
-      if (n1 > 0) scores(1, 0);
-      // the last item's outputs have been read
-      if (seg > 0) ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.done), (seg - 1) & 1, gave_up));
-      for (int s = 0; s < n0 && ok; ++s) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (s >= (b == 0 ? n0 : n1)) continue;
-          product(b, s);
-          if (s + 1 < (b == 0 ? n0 : n1)) scores(b, s + 1);
-        }
-        ok = !*gave_up;
       }
+      if (n == 0 && seg > 0) bar_wait(smem_addr(&sm.done), (seg - 1) & 1, gave_up);
       base += nt;
-      count[0] += n0;
-      count[1] += n1;
+      count += n;
     }
     if (*gave_up) {  // products that are still running write this block's tensor memory
-      if (elect()) commit(smem_addr(&sm.drain));
-      for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.drain), 0); ++k) {
+      if (elect()) commit(smem_addr(&sm.drain[b]));
+      for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.drain[b]), 0); ++k) {
       }
     }
     __syncwarp();
@@ -207,7 +206,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const int own = tid - kConvWarp * 32, quarter = warp - kConvWarp;
     const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (a.qst * 2) | (a.qsh * 2)) & 15) == 0;
     const uint32_t turn = static_cast<uint32_t>(own & 7) << 4;  // the swizzle of this row
-    Walk<N> it(a, start, hi - lo);
+    Walk<N> it(a, start, my_tiles);
     int seg = 0, i = 0;
     do {
       const RowTile r = it.r;
@@ -337,7 +336,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 3]), (seg >> 2) & 1, gave_up);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {  // the other warps may be a few barriers behind
-        for (int64_t k = 0; k < hi - lo + 2; ++k) named_arrive(1, 256);
+        for (int64_t k = 0; k < my_tiles + 2; ++k) named_arrive(1, 256);
         break;
       }
       const typename C::Item& it = sm.item[seg & 3];
@@ -552,8 +551,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     if (work) convert_tiles();
   } else {
     fewer_registers<96>();
-    if (work && warp == kLoadWarp) copy_tiles<N, D, NS>(a, start, hi - lo, kmap, vmap, ring, sm, gave_up);
-    if (work && warp == kMmaWarp) products();
+    if (work && warp == kLoadWarp) copy_tiles<N, D, NS>(a, start, my_tiles, kmap, vmap, ring, sm, gave_up);
+    if (work && warp == kMmaWarp) products(std::integral_constant<int, 0>{});
+    if (work && warp == kMmaWarp + 1) products(std::integral_constant<int, 1>{});
   }
 
   fence_before();

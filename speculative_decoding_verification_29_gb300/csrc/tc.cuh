@@ -51,6 +51,7 @@ constexpr int kWaitTries = 100000;  // a wait gives up after these: about two se
 // runs through its loop without touching the tensor core or starting copies.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
   if (bar_try(bar, parity)) return true;
+#pragma unroll 1
   for (int i = 0; !bar_try_long(bar, parity); ++i) {
     if (*gave_up) return false;
     if (i == kWaitTries) {
@@ -114,6 +115,9 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
   return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | static_cast<uint64_t>(lead >> 4) << 16 |
          static_cast<uint64_t>(stride >> 4) << 32 | 1ull << 46 | static_cast<uint64_t>(layout) << 61;
 }
+// Products and commits are issued in a branch on elect() of a warp whose number
+// and loops the compiler knows to be uniform: an issue then takes three
+// instructions, and some twenty where it has to move addresses between registers.
 // Instruction descriptor: e4m3 operands, fp32 accumulators, M x N; `major_mn`:
 // both operands lie with M (N) contiguous rather than K.
 __host__ __device__ constexpr uint32_t instr_desc(int m, int n, bool major_mn) {
