@@ -4,7 +4,7 @@
 // Here a row of scores is one thread's. Tiles of keys and values are turned from
 // e4m3 into f16 once, exactly, for all the rows of the item (64 conversions a
 // thread and tile), which buys products in f16: queries (a power of two times
-// bf16 or fp16 values, exact above 2^-24 of the item's largest) and weights (2^-12
+// bf16 or fp16 values, exact down to 2^-24 of the row's largest) and weights (2^-12
 // of their value, down to 2^-32 of the largest) need one term each, and because
 // f16 weights keep their precision over 24 powers of two, the output may stay in
 // tensor memory across tiles: a row's sums are relative to a reference that
@@ -21,7 +21,7 @@
 // share the tiles. Otherwise they share the rows (128), take every other tile
 // and are added up at the item's end: both read each other's accumulator, since a
 // row has the same lane in both.
-// Four more warps convert tiles and load queries, one copies, one issues each stream's products.
+// Four more warps convert tiles and load queries, one copies, one issues.
 #include <string.h>
 
 #include <type_traits>
@@ -45,16 +45,17 @@ struct Wide {
   static constexpr int kQ = (PAIR ? 2 : 1) * kF16;
   static constexpr int NF = PAIR ? 3 : 4;  // f16 tiles
   struct Item {
-    int b, first, n, ctx, rows, end, part, r0, h, t0, t1, tiles, eq;
+    int b, first, n, ctx, rows, end, part, r0, h, t0, t1, tiles;
   };
   struct Small {
     alignas(16) Item item[kItems];
     float ref[2][2][kTile], sum[2][2][kTile];  // of two items: each stream's rows, exchanged at an item's end
-    float red[4];
+    float qscale[kItems][N];             // 2^eq of the items' rows
+    alignas(8) int64_t qrow[N];          // where the item's rows of queries begin
     int nan[kItems];
     alignas(16) float4 page[kMetaRing][kMaxPages];
     alignas(8) uint64_t full[8], empty[8], full16[4], empty16[4], s_full[2], p_ready[2], o_full[2], q_ready[kItems], q_free,
-        done, drain[2];
+        done, drain;
     uint32_t tmem;
     int gave_up;
     alignas(8) int tmp[64];
@@ -66,6 +67,9 @@ struct Wide {
   static_assert(NS >= 3, "ring of e4m3 tiles");
   static_assert(2 * kMetaRing >= NS + NF + 4, "a tile's exponents outlive its weights");
 };
+
+__device__ __forceinline__ __half2 abs2(const __half* e) { return __habs2(__half2(e[0], e[1])); }
+__device__ __forceinline__ __nv_bfloat162 abs2(const __nv_bfloat16* e) { return __habs2(__nv_bfloat162(e[0], e[1])); }
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   uint32_t r;
@@ -97,16 +101,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     for (int i = 0; i < NF; ++i) {
       bar_init(smem_addr(&sm.full16[i]), 4);
-      bar_init(smem_addr(&sm.empty16[i]), 2);
+      bar_init(smem_addr(&sm.empty16[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(smem_addr(&sm.s_full[i]), 1);
       bar_init(smem_addr(&sm.p_ready[i]), 4);
       bar_init(smem_addr(&sm.o_full[i]), 1);
-      bar_init(smem_addr(&sm.drain[i]), 1);
     }
     for (int i = 0; i < kItems; ++i) bar_init(smem_addr(&sm.q_ready[i]), 4);
-    bar_init(smem_addr(&sm.q_free), 2);
+    bar_init(smem_addr(&sm.q_free), 1);
+    bar_init(smem_addr(&sm.drain), 1);
     bar_init(smem_addr(&sm.done), 8);
     fence_bar_init();
     sm.gave_up = 0;
@@ -129,73 +133,74 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     return (nt + 1 - stream) / 2;
   };
 
-  // ---- products of one stream: the warp waits together, one lane issues
-  auto products = [&](auto stream) {
-    constexpr int b = decltype(stream)::value;
+  // ---- products of both streams in turn: the warp waits together, one lane issues
+  auto products = [&]() {
     constexpr uint32_t id_s = instr_desc_f16(kTile, kTile, false), id_o = instr_desc_f16(kTile, D, true);
-    const uint64_t q_desc = smem_desc(smem_addr(q_smem) + (PAIR ? b * C::kF16 : 0), 16, 1024, 2),
-                   k_desc = smem_desc(smem_addr(f16), 16, 1024, 2), v_desc = smem_desc(smem_addr(f16), C::kPanel, 1024, 2);
-    int base = 0, count = 0;  // tiles and steps of earlier items
+    const uint64_t q_desc = smem_desc(smem_addr(q_smem), 16, 1024, 2), k_desc = smem_desc(smem_addr(f16), 16, 1024, 2),
+                   v_desc = smem_desc(smem_addr(f16), C::kPanel, 1024, 2);
+    int base = 0, count[2] = {0, 0};  // tiles and steps of earlier items
     for (int seg = 0;; ++seg) {
       bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 3]), (seg >> 2) & 1, gave_up);
       ok = __all_sync(0xffffffffu, ok);
       const int nt = uniform(sm.item[seg & 3].t1 - sm.item[seg & 3].t0), rows = uniform(sm.item[seg & 3].rows);
       if (!ok || nt <= 0) break;
       fence_after();
-      const int n = steps(nt, rows, b);
-      const bool alone = !PAIR || steps(nt, rows, 1) == 0;  // the tiles' only user
-      if (n == 0 && elect()) bar_arrive(smem_addr(&sm.q_free));
+      const int n[2] = {steps(nt, rows, 0), steps(nt, rows, 1)};
 #pragma unroll 1
-      for (int s = -1; s < n; ++s) {
-        if (s >= 0) {  // O += P x V
-          const uint32_t j = 2u * (base + (PAIR ? s : 2 * s + b)) + 1, slot = uniform(j % NF);
-          // the last item's outputs have been read
-          if (s == 0 && seg > 0) ok = bar_wait(smem_addr(&sm.done), (seg - 1) & 1, gave_up);
-          ok = bar_wait(smem_addr(&sm.full16[slot]), (j / NF) & 1, gave_up) &&
-               bar_wait(smem_addr(&sm.p_ready[b]), (count + s) & 1, gave_up) && ok;
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          fence_after();
-          const uint32_t add = uniform(s > 0);
-          if (elect()) {
-            const uint64_t vd = v_desc + (slot * C::kF16 >> 4);
+      for (int s = -1; s < n[0] && ok; ++s) {
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_f16_tmem(tmem + kO + b * kTile, tmem + b * kTile + 8 * k, vd + (k * 2048 >> 4), id_o, k > 0 ? 1 : add);
-            commit(smem_addr(&sm.o_full[b]));
-            commit(smem_addr(&sm.empty16[slot]));
-            if (alone) commit(smem_addr(&sm.empty16[slot]));
-          }
-          __syncwarp();
-        }
-        if (s + 1 < n) {  // the next S = Q x K^T
-          const uint32_t j = 2u * (base + (PAIR ? s + 1 : 2 * (s + 1) + b)), slot = uniform(j % NF);
-          ok = bar_wait(smem_addr(&sm.full16[slot]), (j / NF) & 1, gave_up);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          fence_after();
-          if (elect()) {
-            const uint64_t kd = k_desc + (slot * C::kF16 >> 4);
+        for (int b = 0; b < 2; ++b) {
+          if (s >= 0 && s < n[b] && ok) {  // O += P x V
+            const uint32_t j = 2u * (base + (PAIR ? s : 2 * s + b)) + 1, slot = uniform(j % NF);
+            // the last item's outputs have been read
+            if (b == 0 && s == 0 && seg > 0) ok = bar_wait(smem_addr(&sm.done), (seg - 1) & 1, gave_up);
+            ok = bar_wait(smem_addr(&sm.full16[slot]), (j / NF) & 1, gave_up) &&
+                 bar_wait(smem_addr(&sm.p_ready[b]), (count[b] + s) & 1, gave_up) && ok;
+            ok = __all_sync(0xffffffffu, ok);
+            fence_after();
+            const uint32_t add = uniform(s > 0);
+            const bool last = uniform(!PAIR || b == 1 || n[1] == 0);  // user of the tile
+            if (ok && elect()) {
+              const uint64_t vd = v_desc + (slot * C::kF16 >> 4);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const int off = ((k / 4) * C::kPanel + (k % 4) * 32) >> 4;
-              mma_f16(tmem + b * kTile, q_desc + off, kd + off, id_s, k > 0);
+              for (int k = 0; k < kTile / 16; ++k)
+                mma_f16_tmem(tmem + kO + b * kTile, tmem + b * kTile + 8 * k, vd + (k * 2048 >> 4), id_o, k > 0 ? 1 : add);
+              commit(smem_addr(&sm.o_full[b]));
+              if (last) commit(smem_addr(&sm.empty16[slot]));
             }
-            commit(smem_addr(&sm.s_full[b]));
-            commit(smem_addr(&sm.empty16[slot]));
-            if (alone) commit(smem_addr(&sm.empty16[slot]));
-            if (s + 2 == n) commit(smem_addr(&sm.q_free));
+            __syncwarp();
           }
-          __syncwarp();
+          if (s + 1 < n[b] && ok) {  // the next S = Q x K^T
+            const uint32_t j = 2u * (base + (PAIR ? s + 1 : 2 * (s + 1) + b)), slot = uniform(j % NF);
+            ok = bar_wait(smem_addr(&sm.full16[slot]), (j / NF) & 1, gave_up);
+            ok = __all_sync(0xffffffffu, ok);
+            fence_after();
+            const bool last = uniform(!PAIR || b == 1 || n[1] == 0);
+            const bool item_last = uniform(s + 2 == n[b] && (b == 1 || n[1] < n[0]));  // product with these queries
+            if (ok && elect()) {
+              const uint64_t qd = q_desc + (PAIR ? b * C::kF16 >> 4 : 0), kd = k_desc + (slot * C::kF16 >> 4);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const int off = ((k / 4) * C::kPanel + (k % 4) * 32) >> 4;
+                mma_f16(tmem + b * kTile, qd + off, kd + off, id_s, k > 0);
+              }
+              commit(smem_addr(&sm.s_full[b]));
+              if (last) commit(smem_addr(&sm.empty16[slot]));
+              if (item_last) commit(smem_addr(&sm.q_free));
+            }
+            __syncwarp();
+          }
         }
       }
-      if (n == 0 && seg > 0) bar_wait(smem_addr(&sm.done), (seg - 1) & 1, gave_up);
+      if (!ok) break;
       base += nt;
-      count += n;
+      count[0] += n[0];
+      count[1] += n[1];
     }
     if (*gave_up) {  // products that are still running write this block's tensor memory
-      if (elect()) commit(smem_addr(&sm.drain[b]));
-      for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.drain[b]), 0); ++k) {
+      if (elect()) commit(smem_addr(&sm.drain));
+#pragma unroll 1
+      for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.drain), 0); ++k) {
       }
     }
     __syncwarp();
@@ -203,70 +208,98 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 
   auto convert_tiles = [&]() {
     // ---- an item's queries, then its tiles, into f16: a thread owns a row
-    const int own = tid - kConvWarp * 32, quarter = warp - kConvWarp;
+    const int own = tid - kConvWarp * 32;
     const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (a.qst * 2) | (a.qsh * 2)) & 15) == 0;
     const uint32_t turn = static_cast<uint32_t>(own & 7) << 4;  // the swizzle of this row
     Walk<N> it(a, start, my_tiles);
+    auto row_at = [&](const RowTile& r, int h, int row) {  // where a row's queries begin
+      const uint32_t flat = static_cast<uint32_t>(r.rt * N + min(row, r.rows - 1)), tok = flat / static_cast<uint32_t>(a.group);
+      return (r.first + static_cast<int64_t>(tok)) * a.qst + (h * a.group + static_cast<int>(flat - tok * a.group)) * a.qsh;
+    };
     int seg = 0, i = 0;
+    bool more;
     do {
       const RowTile r = it.r;
-      const int r0 = r.rt * N;
-      auto chunk = [&](int row, int d, float* x) {
-        const uint32_t tok = static_cast<uint32_t>(r0 + row) / static_cast<uint32_t>(a.group);
-        const QT* q = static_cast<const QT*>(a.q) + (r.first + static_cast<int64_t>(tok)) * a.qst +
-                      (it.h * a.group + (r0 + row - static_cast<int>(tok) * a.group)) * a.qsh + d;
+      const int h = it.h, t0 = it.t0, t1 = it.t1, r0 = r.rt * N;
+      // Queries as f16, each row over the power of two that leaves its largest element in [2^13, 2^14): kLanes lanes a
+      // row, kBatch rows of a lane group in flight. Rows' places and scales are found while the last item's queries are
+      // still in use.
+      constexpr int kLanes = D / 8, kRows = 128 / kLanes, kBatch = 8;
+      const int chunk = lane % kLanes, sub = own / kLanes;
+      for (int row = own; row < N; row += 128) sm.qrow[row] = row_at(r, h, row);
+      named_sync(2, 128);
+      auto load = [&](int row, QT* e) {
+        const QT* q = static_cast<const QT*>(a.q) + sm.qrow[row] + chunk * 8;
         if (vec) {
           const uint4 u = *reinterpret_cast<const uint4*>(q);
-          const QT* e = reinterpret_cast<const QT*>(&u);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = to_f(e[k]);
+          memcpy(e, &u, 16);
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = to_f(q[k]);
+          for (int k = 0; k < 8; ++k) e[k] = q[k];
         }
       };
-      float amax = 0.f;
-      for (int row = own; row < r.rows; row += kTile) {
-#pragma unroll 2
-        for (int d = 0; d < D; d += 8) {
-          float x[8];
-          chunk(row, d, x);
+#pragma unroll 1
+      for (int row0 = sub; row0 < r.rows; row0 += kRows * kBatch) {
+        QT e[kBatch][8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (fabsf(x[k]) < -kNegInf) amax = fmaxf(amax, fabsf(x[k]));
+        for (int z = 0; z < kBatch; ++z) load(min(row0 + z * kRows, N - 1), e[z]);
+        float amax[kBatch];
+#pragma unroll
+        for (int z = 0; z < kBatch; ++z) {
+          auto m = abs2(e[z]);
+#pragma unroll
+          for (int k = 2; k < 8; k += 2) m = __hmax2(m, abs2(e[z] + k));
+          amax[z] = fmaxf(to_f(m.x), to_f(m.y));
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1)
+#pragma unroll
+          for (int z = 0; z < kBatch; ++z) amax[z] = fmaxf(amax[z], __shfl_xor_sync(0xffffffffu, amax[z], o));
+#pragma unroll
+        for (int z = 0; z < kBatch; ++z) {
+          const int eq = min(max(static_cast<int>(__float_as_uint(amax[z]) >> 23) - 127 - 13, -110), 110);
+          if (chunk == 0 && row0 + z * kRows < N) sm.qscale[seg & 3][row0 + z * kRows] = pow2i(eq);
         }
       }
-      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-      named_sync(2, 128);  // the last item's maxima have been read
-      if (lane == 0) sm.red[quarter] = amax;
-      named_sync(2, 128);
-      amax = fmaxf(fmaxf(sm.red[0], sm.red[1]), fmaxf(sm.red[2], sm.red[3]));
-      const int eq = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13, -110), 110);  // largest below 2^14
-      const float down = a.negate ? -pow2i(-eq) : pow2i(-eq);
+      __syncwarp();
       if (seg > 0) bar_wait(smem_addr(&sm.q_free), (seg - 1) & 1, gave_up);
-      for (int row = own; row < r.rows; row += kTile) {
-        uint8_t* to = q_smem + (row / kTile) * C::kF16 + own * 128;
-#pragma unroll 2
-        for (int d = 0; d < D; d += 8) {
-          float x[8];
-          chunk(row, d, x);
-          uint4 u;
-          u.x = half2_bits(x[0] * down, x[1] * down);
-          u.y = half2_bits(x[2] * down, x[3] * down);
-          u.z = half2_bits(x[4] * down, x[5] * down);
-          u.w = half2_bits(x[6] * down, x[7] * down);
-          *reinterpret_cast<uint4*>(to + (d / 64) * C::kPanel + (((d % 64) * 2) ^ turn)) = u;
+#pragma unroll 1
+      for (int row0 = sub; row0 < r.rows; row0 += kRows * kBatch) {
+        QT e[kBatch][8];
+#pragma unroll
+        for (int z = 0; z < kBatch; ++z) load(min(row0 + z * kRows, N - 1), e[z]);
+#pragma unroll
+        for (int z = 0; z < kBatch; ++z) {
+          const int row = min(row0 + z * kRows, N - 1);
+          const uint32_t inverse = 0x7f000000u - __float_as_uint(sm.qscale[seg & 3][row]);  // of a power of two
+          const float down = __uint_as_float(a.negate ? inverse | 0x80000000u : inverse);
+          uint32_t v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = mul2(make_float2(to_f(e[z][2 * k]), to_f(e[z][2 * k + 1])), make_float2(down, down));
+            v[k] = half2_bits(f.x, f.y);
+          }
+          *reinterpret_cast<uint4*>(q_smem + (row / kTile) * C::kF16 + (chunk / 8) * C::kPanel + (row % kTile) * 128 +
+                                    (((chunk % 8) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
         }
       }
       if (own == 0) {
         sm.nan[seg & 3] = 0;
-        sm.item[seg & 3] = {r.b, r.first, r.n, r.ctx, r.rows, r.end, r.part, r0, it.h, it.t0, it.t1, r.tiles, eq};
+        sm.item[seg & 3] = {r.b, r.first, r.n, r.ctx, r.rows, r.end, r.part, r0, h, t0, t1, r.tiles};
       }
       fence_async_shared();
       named_sync(2, 128);  // the flag is cleared before a tile of the item sets it
       if (lane == 0) bar_arrive(smem_addr(&sm.q_ready[seg & 3]));
 
-      for (int t = it.t0; t < it.t1; ++t, ++i) {
+      more = it.next(a);
+      if (more)  // the next item's queries come from memory by the time they are needed
+        for (int row = own; row < it.r.rows; row += 128) {
+          const QT* q = static_cast<const QT*>(a.q) + row_at(it.r, it.h, row);
+#pragma unroll
+          for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + d));
+        }
+
+      for (int t = t0; t < t1; ++t, ++i) {
         const int slot = t * kTile + own;
         const bool masked = t >= r.part;  // not every row sees every slot
 #pragma unroll 1
@@ -317,7 +350,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
       }
       ++seg;
-    } while (it.next(a));
+    } while (more);
     bar_wait(smem_addr(&sm.q_free), (seg - 1) & 1, gave_up);
     if (own == 0) sm.item[seg & 3].t0 = sm.item[seg & 3].t1 = 0;  // no further item
     __syncwarp();
@@ -347,7 +380,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const int ctx = uniform(it.ctx);
       const int row = PAIR ? b * kTile + own : own;  // within the item
       const bool rows_here = (PAIR ? b * kTile : 0) + quarter * 32 < rows;
-      const float scale = a.scale * pow2i(it.eq);
+      const float scale = a.scale * sm.qscale[seg & 3][min(row, rows - 1)];
       // slots before this are seen by all of the warp's rows
       const int warp_row = it.r0 + (PAIR ? b * kTile : 0) + quarter * 32;
       const int all_seen = uniform(ctx + (a.tree ? 0 : min(it.n - 1, warp_row / a.group) + 1));
@@ -552,8 +585,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   } else {
     fewer_registers<96>();
     if (work && warp == kLoadWarp) copy_tiles<N, D, NS>(a, start, my_tiles, kmap, vmap, ring, sm, gave_up);
-    if (work && warp == kMmaWarp) products(std::integral_constant<int, 0>{});
-    if (work && warp == kMmaWarp + 1) products(std::integral_constant<int, 1>{});
+    if (work && warp == kMmaWarp) products();
   }
 
   fence_before();
