@@ -75,6 +75,8 @@ struct Kv8AttnArgs {
   int parts;            // thread blocks the cache is split over
   int order;            // tensor maps' dimensions 1..3: 2-bit fields naming slot (0), head (1), block (2)
   int32_t* gave_up;     // workspace [parts]: a wait of the block ran out
+  int4* cut;            // workspace [parts]: the item that begins in the part and ends behind it: sequence, row tile, KV
+                        // head, shares (0: none)
   float2* part_ml;      // workspace [2 parts][rows]: exponent reference, sum of weights
   float* part_o;        // workspace [2 parts][rows][head_dim]: weighted sums
 };

@@ -72,16 +72,17 @@ uint64_t turn_fraction(double f) {
   return (static_cast<uint64_t>(a) << 32) + static_cast<uint64_t>(static_cast<int64_t>(llrint(rest)));
 }
 
-// The attention's workspace: a flag per part, then each part's two shares of
+// The attention's workspace: a flag and a cut item per part, then each part's two shares of
 // cut items (exponent references and sums, weighted sums).
 struct AttnLayout {
-  size_t ml, o, total;
+  size_t cut, ml, o, total;
 };
 AttnLayout attn_layout(int rows, int D) {
   const size_t parts = kv8_attention_parts(rows);
   auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
   AttnLayout l{};
-  l.ml = up(parts * sizeof(int32_t));
+  l.cut = up(parts * sizeof(int32_t));
+  l.ml = l.cut + up(parts * sizeof(int4));
   l.o = l.ml + up(2 * parts * rows * sizeof(float2));
   l.total = l.o + up(2 * parts * rows * D * sizeof(float));
   return l;
@@ -183,10 +184,6 @@ int spec_kv8_append(const spec_kv8_cache* cache, const void* keys, int64_t k_str
   a.cu = cu_tokens;
   a.pos = positions;
   a.row_status = row_status;
-  a.heads_per_cta = 1;
-  a.head_groups = (a.c.H + a.heads_per_cta - 1) / a.heads_per_cta;
-  a.status_ctas = (a.c.B + 7) / 8;
-  a.item_ctas = (T / a.c.block + 2 * a.c.B) * 2 * a.head_groups;
   return cuda_status(launch_kv8_append(a, dtype, static_cast<cudaStream_t>(stream)));
 }
 
@@ -238,6 +235,7 @@ int spec_kv8_attention(const spec_kv8_cache* cache, const void* queries, int64_t
   const AttnLayout l = attn_layout(rows, a.c.D);
   char* ws = static_cast<char*>(workspace);
   a.gave_up = reinterpret_cast<int32_t*>(ws);
+  a.cut = reinterpret_cast<int4*>(ws + l.cut);
   a.part_ml = reinterpret_cast<float2*>(ws + l.ml);
   a.part_o = reinterpret_cast<float*>(ws + l.o);
   CUtensorMap kmap, vmap;

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   Runs runs;
   Start start;
   fence_before();
-  const bool work = uniform(find_run<N>(a, blockIdx.x, false, &runs, &start, sm.tmp)) != 0;
+  const bool work = uniform(find_run<N>(a, blockIdx.x, &runs, &start, sm.tmp)) != 0;
   const int64_t my_tiles = work ? runs.begin(blockIdx.x + 1) - runs.begin(blockIdx.x) : 0;
   __syncthreads();
   fence_after();
@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     Walk<N> it(a, start, my_tiles);
     const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (a.qst * 2) | (a.qsh * 2)) & 15) == 0;
     int seg = 0;
+    bool more;
     do {
       const RowTile r = it.r;
       const int r0 = r.rt * N;
@@ -310,7 +311,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       __syncwarp();
       if (lane == 0) bar_arrive(smem_addr(&sm.q_ready[seg & 1]));
       ++seg;
-    } while (it.next(a));
+      const RowTile last = it.r;
+      const int h = it.h, t0 = it.t0, t1 = it.t1;
+      more = it.next(a);
+      if (!more && own == 0) a.cut[blockIdx.x] = cut_item<N>(runs, blockIdx.x, last, h, t0, t1);
+    } while (more);
     if (seg > 1) bar_wait(smem_addr(&sm.q_free[seg & 1]), ((seg >> 1) - 1) & 1, gave_up);
     if (own == 0) sm.item[seg & 1].t0 = sm.item[seg & 1].t1 = 0;  // no further item
     __syncwarp();
@@ -579,7 +584,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   __syncthreads();
   fence_after();
   if (warp == kMmaWarp) tmem_free(tmem, C::kCols);
-  if (tid == 0) a.gave_up[blockIdx.x] = sm.gave_up;
+  if (tid == 0) {
+    a.gave_up[blockIdx.x] = sm.gave_up;
+    if (!work) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
   griddep_launch_dependents();
 }
 

@@ -78,11 +78,10 @@ struct Runs {
   __device__ __forceinline__ int64_t begin(int part) const { return part * each + min(part, more); }
 };
 
-// All threads of the block: the runs, and where tile begin(part) lies, or with
-// `last` tile begin(part + 1) - 1. False where the part has no tile. s_tmp: 34
-// words of shared memory.
+// All threads of the block: the runs, and where the part's first tile lies. False
+// where it has none. s_tmp: 64 words of shared memory.
 template <int N>
-__device__ __forceinline__ bool find_run(const Kv8AttnArgs& a, int part, bool last, Runs* runs, Start* s, int* s_tmp) {
+__device__ __forceinline__ bool find_run(const Kv8AttnArgs& a, int part, Runs* runs, Start* s, int* s_tmp) {
   const int nthr = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = nthr >> 5;
   const uint32_t cand = static_cast<uint32_t>(a.c.B) * static_cast<uint32_t>(a.row_tiles);  // below 2^31
   // Sums over the candidates base .. base + nthr - 1, one a thread: up to this one's, and all.
@@ -136,7 +135,7 @@ __device__ __forceinline__ bool find_run(const Kv8AttnArgs& a, int part, bool la
         }
         runs->each = all / runs->parts;
         runs->more = static_cast<int>(all - runs->each * runs->parts);
-        want = last ? runs->begin(part + 1) - 1 : runs->begin(part);
+        want = runs->begin(part);
       }
       const int64_t from = (run + upto - v) * a.c.H;
       if (v > 0 && want >= from && want < (run + upto) * a.c.H) {
@@ -222,6 +221,16 @@ __device__ __forceinline__ bool sees(const Kv8AttnArgs& a, int b, int i, int j) 
   return a.tree ? a.tree[(static_cast<int64_t>(b) * a.max_tokens + i) * a.max_tokens + j] != 0 : j <= i;
 }
 
+// What the join needs to know of a part's last item.
+template <int N>
+__device__ __forceinline__ int4 cut_item(const Runs& runs, int part, const RowTile& r, int h, int t0, int t1) {
+  if (t0 > 0 || t1 == r.tiles) return make_int4(0, 0, 0, 0);
+  const int64_t end = runs.begin(part + 1) - t1 + r.tiles;
+  int n = 2;
+  while (runs.begin(part + n) < end) ++n;
+  return make_int4(r.b, r.rt, h, n);
+}
+
 // The copying warp: the pages of each tile's keys, then of its values, into a
 // ring of NS slots, and of each page of the tile 2^ek (NaN for a page outside the
 // pool), ev and 2^-ev into sm.page.
@@ -288,14 +297,13 @@ __device__ __forceinline__ void copy_tiles(const Kv8AttnArgs& a, const Start& st
 // -------------------------------------------------------------------- join --
 //
 // Adds the shares of items that runs cut. Block x takes the item that begins in
-// part x and ends behind it, a warp one row: shares in the order of the parts,
-// each times 2^(its reference - the largest). The last blocks check sequences.
+// part x and ends behind it, a warp one row at a time: shares in the order of the
+// parts, each times 2^(its reference - the largest). The last blocks check sequences.
 
 constexpr int kJoinThreads = 256;
 
 template <typename QT, int D, int N>
 __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ Kv8AttnArgs a) {
-  __shared__ __align__(8) int s_tmp[64];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_launch_dependents();
   if (blockIdx.x >= static_cast<unsigned>(a.parts)) {  // a warp per sequence: row_status
@@ -327,49 +335,46 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
     }
     return;
   }
-  Runs runs;
-  Start s;
-  if (!find_run<N>(a, blockIdx.x, true, &runs, &s, s_tmp)) return;
-  const RowTile r = row_tile<N>(a, s.b, s.rt);
-  const int64_t lo = runs.begin(blockIdx.x), hi = runs.begin(blockIdx.x + 1);
-  const int64_t begin = hi - 1 - s.t, end = begin + r.tiles;  // the item's tiles
-  const int row = blockIdx.y * (kJoinThreads / 32) + warp;
-  if (begin < lo || end <= hi || row >= r.rows) return;
-  int n = 2;  // shares
-  while (runs.begin(blockIdx.x + n) < end) ++n;
   griddep_wait();
+  const int4 item = a.cut[blockIdx.x];
+  const int n = item.w;
+  if (n == 0) return;
+  const RowTile r = row_tile<N>(a, item.x, item.y);
   const int64_t first = blockIdx.x;
-  auto share = [&](int i) { return (2 * (first + i) + (i == 0 ? 1 : 0)) * N + row; };
-  float top = kNegInf;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, a.part_ml[share(i)].x);
+#pragma unroll 1
+  for (int row = blockIdx.y * (kJoinThreads / 32) + warp; row < r.rows; row += gridDim.y * (kJoinThreads / 32)) {
+    auto share = [&](int i) { return (2 * (first + i) + (i == 0 ? 1 : 0)) * N + row; };
+    float top = kNegInf;
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, a.part_ml[share(i)].x);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (top == kNegInf) top = 0.f;
-  constexpr int V = D / 32;
-  float acc[V] = {}, sum = 0.f;
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top == kNegInf) top = 0.f;
+    constexpr int V = D / 32;
+    float acc[V] = {}, sum = 0.f;
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float2 ml = a.part_ml[share(i)];
-    const float* p = a.part_o + share(i) * D + lane * V;
-    float x[V];
-    if (V == 4) {
-      const float4 u = *reinterpret_cast<const float4*>(p);
-      x[0] = u.x, x[1] = u.y, x[V - 2] = u.z, x[V - 1] = u.w;
-    } else {
-      const float2 u = *reinterpret_cast<const float2*>(p);
-      x[0] = u.x, x[1] = u.y;
+    for (int i = 0; i < n; ++i) {
+      const float2 ml = a.part_ml[share(i)];
+      const float* p = a.part_o + share(i) * D + lane * V;
+      float x[V];
+      if (V == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(p);
+        x[0] = u.x, x[1] = u.y, x[V - 2] = u.z, x[V - 1] = u.w;
+      } else {
+        const float2 u = *reinterpret_cast<const float2*>(p);
+        x[0] = u.x, x[1] = u.y;
+      }
+      const float w = exp2_whole(ml.x - top);
+      sum = fmaf(w, ml.y, sum);
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k] = fmaf(w, x[k], acc[k]);
     }
-    const float w = exp2_whole(ml.x - top);
-    sum = fmaf(w, ml.y, sum);
+    const int item_row = item.y * N + row, tok = item_row / a.group;
+    QT* out = static_cast<QT*>(a.out) + (r.first + static_cast<int64_t>(tok)) * a.ost +
+              (item.z * a.group + (item_row - tok * a.group)) * a.osh + lane * V;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = fmaf(w, x[k], acc[k]);
+    for (int k = 0; k < V; ++k) out[k] = from_f<QT>(acc[k] * inv);
   }
-  const int item_row = s.rt * N + row, tok = item_row / a.group;
-  QT* out = static_cast<QT*>(a.out) + (r.first + static_cast<int64_t>(tok)) * a.ost +
-            (s.h * a.group + (item_row - tok * a.group)) * a.osh + lane * V;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int k = 0; k < V; ++k) out[k] = from_f<QT>(acc[k] * inv);
 }
 
 constexpr int kSms = 152;
@@ -378,7 +383,8 @@ constexpr int kSms = 152;
 template <typename QT, int D, int N>
 cudaError_t launch_join(const Kv8AttnArgs& a, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(a.max_tokens) * a.group;
-  const int y = static_cast<int>((rows < N ? rows : N) + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+  const int groups = static_cast<int>((rows < N ? rows : N) + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+  const int y = groups < 8 ? groups : 8;
   const int checks = (a.c.B + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
   return launch_pdl(kv8_join_kernel<QT, D, N>, dim3(static_cast<unsigned>(a.parts + checks), static_cast<unsigned>(y)),
                     dim3(kJoinThreads), st, a);

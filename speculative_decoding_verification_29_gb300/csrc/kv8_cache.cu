@@ -4,7 +4,7 @@
 // Append. One thread block owns one cache block of one head (or of a few
 // heads) and either its keys or its values, because the block's scale is a
 // maximum over everything the call writes into it: each thread keeps 16
-// elements of up to four rows in registers, the largest magnitude goes over
+// elements in registers, the largest magnitude goes over
 // warps and shared memory, and the codes are stored from the same registers,
 // so every input is read once. A cache block that already holds tokens is only
 // rewritten when its scale grows.
@@ -17,6 +17,9 @@
 // far positions and takes no 64-bit floating point.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <string.h>
+
+#include <algorithm>
 
 #include "kv8.h"
 #include "internal.h"
@@ -24,8 +27,6 @@
 namespace specv {
 
 namespace {
-
-constexpr int kAppThreads = 256;
 
 // ------------------------------------------------------------ elements --
 
@@ -136,9 +137,9 @@ __device__ __forceinline__ void turn(const Kv8Rope& r, float* x, const float* cs
 
 // ------------------------------------------------------------------ append --
 
-template <typename T>
+template <typename T, int NT>
 __device__ __forceinline__ void append_status(const Kv8AppendArgs& a) {  // a warp per sequence
-  const int b = blockIdx.x * (kAppThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int b = blockIdx.x * (NT / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (b >= a.c.B) return;
   const int lo = a.cu[b], hi = a.cu[b + 1], len = a.c.len[b];
   bool bad = !kv8_seq_ok(a.c, a.T, lo, hi, len);
@@ -153,10 +154,10 @@ __device__ __forceinline__ void append_status(const Kv8AppendArgs& a) {  // a wa
   else if (lane == 0) a.row_status[b] = 0;
 }
 
-template <typename T>
+template <typename T, int NT>
 __device__ __forceinline__ void append_queries(const Kv8AppendArgs& a) {  // a thread: 16 elements of a query row
   const int tpr = a.c.D / 16;
-  const int64_t item = static_cast<int64_t>(blockIdx.x - a.status_ctas - a.item_ctas) * kAppThreads + threadIdx.x;
+  const int64_t item = static_cast<int64_t>(blockIdx.x - a.status_ctas - a.item_ctas) * NT + threadIdx.x;
   const int64_t row = item / tpr;
   const int c = static_cast<int>(item - row * tpr);
   const int t = static_cast<int>(row / a.q_heads), h = static_cast<int>(row - static_cast<int64_t>(t) * a.q_heads);
@@ -194,26 +195,59 @@ __device__ __forceinline__ void append_queries(const Kv8AppendArgs& a) {  // a t
   }
 }
 
-// PASS: rows a thread holds (block * head_dim / 16 <= PASS * kAppThreads).
-template <typename T, int PASS>
-__global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a) {
+// 16 elements of a row as they are in memory.
+template <typename T>
+struct Row16 {
+  uint4 u[sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Row16<T> load_row(const T* row, int d0, int d1, bool vec) {
+  Row16<T> r;
+  if (vec) {
+    constexpr int kHalf = sizeof(T) / 2;  // vectors of eight elements
+#pragma unroll
+    for (int k = 0; k < kHalf; ++k) {
+      r.u[k] = reinterpret_cast<const uint4*>(row + d0)[k];
+      r.u[kHalf + k] = reinterpret_cast<const uint4*>(row + d1)[k];
+    }
+  } else {
+    T e[16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = row[d0 + k], e[8 + k] = row[d1 + k];
+    memcpy(r.u, e, sizeof(e));
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void row_floats(const Row16<T>& r, float* x) {
+  T e[16];
+  memcpy(e, r.u, sizeof(e));
+#pragma unroll
+  for (int k = 0; k < 16; ++k) x[k] = Act<T>::get(&e[k]);
+}
+
+// A thread holds 16 elements of one slot (NT >= block * head_dim / 16). A thread block takes heads_per_cta heads in turn: the angles and the
+// block's place are found once, and a head's rows are loaded while the head
+// before is rotated and stored.
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT) kv8_append_kernel(const __grid_constant__ Kv8AppendArgs a) {
   __shared__ int s_seq[4];  // sequence, candidate block of it, first token, tokens
-  __shared__ float s_amax[2][kAppThreads / 32];
+  __shared__ uint32_t s_amax[2][NT / 32];
   const int tid = threadIdx.x;
   griddep_launch_dependents();
   griddep_wait();
-  if (blockIdx.x < static_cast<unsigned>(a.status_ctas)) return append_status<T>(a);
+  if (blockIdx.x < static_cast<unsigned>(a.status_ctas)) return append_status<T, NT>(a);
   int item = blockIdx.x - a.status_ctas;
-  if (item >= a.item_ctas) return append_queries<T>(a);
+  if (item >= a.item_ctas) return append_queries<T, NT>(a);
 
   const int part = item % (2 * a.head_groups);
   item /= 2 * a.head_groups;
   const bool keys = part < a.head_groups;
   const int h0 = (keys ? part : part - a.head_groups) * a.heads_per_cta;
+  const int bs = a.c.block;
   if (tid == 0) s_seq[0] = -1;
   __syncthreads();
-  const int bs = a.c.block;
-  for (int b = tid; b < a.c.B; b += kAppThreads) {
+  for (int b = tid; b < a.c.B; b += NT) {
     const int lo = a.cu[b], hi = a.cu[b + 1];
     if (lo >= 0 && hi >= lo && hi <= a.T && lo / bs + 2 * b <= item && item < hi / bs + 2 * b + 2) {
       s_seq[0] = b;
@@ -231,95 +265,92 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const __grid_co
   const int64_t start = j * bs;
   if (n == 0 || start >= static_cast<int64_t>(len) + n) return;
   const int id = a.c.table[static_cast<int64_t>(b) * a.c.max_blocks + j];
-  if (id < 0 || id >= a.c.num_blocks) return;
   const int s_lo = max(0, static_cast<int>(len - start));  // slots written: [s_lo, s_hi)
   const int s_hi = static_cast<int>(min(static_cast<int64_t>(bs), static_cast<int64_t>(len) + n - start));
 
-  const int tpr = a.c.D / 16, c = tid % tpr, row0 = tid / tpr, rows = kAppThreads / tpr;
+  const int tpr = a.c.D / 16, c = tid % tpr, s = tid / tpr;
+  const bool written = s >= s_lo && s < s_hi;
   int d0 = 16 * c, d1 = 16 * c + 8;
   if (keys) chunk_dims(a.rope, c, &d0, &d1);
-  const bool rotated = keys && 16 * c < a.rope.rot;
-  const T* src = static_cast<const T*>(keys ? a.k : a.v);
-  const int64_t st = keys ? a.kst : a.vst, sh = keys ? a.ksh : a.vsh;
+  const bool rotated = written && keys && 16 * c < a.rope.rot;
+  const int64_t sh = keys ? a.ksh : a.vsh, t = first + (start + s - len);
   const bool vec = keys ? a.vec_k : a.vec_v;
-  uint8_t* pool = (keys ? a.c.k : a.c.v) + id * a.c.sb;
-  uint8_t* scales = (keys ? a.c.ks : a.c.vs) + static_cast<int64_t>(id) * a.c.H;
-  const int h1 = min(a.c.H, h0 + a.heads_per_cta);
-  for (int h = h0; h < h1; ++h) {
-    float x[PASS][16];
+  const T* src = static_cast<const T*>(keys ? a.k : a.v) + t * (keys ? a.kst : a.vst) + h0 * sh;
+  const int heads = min(a.c.H, h0 + a.heads_per_cta) - h0;
+  Row16<T> next = {};
+  if (written) next = load_row(src, d0, d1, vec);
+  if (id < 0 || id >= a.c.num_blocks) return;
+  float cs[8], sn[8];
+  if (rotated) angles(a.rope, c, a.pos ? a.pos[t] : start + s, cs, sn);
+  uint8_t* dst = (keys ? a.c.k : a.c.v) + id * a.c.sb + h0 * a.c.sh + s * a.c.ss;
+  uint8_t* scales = (keys ? a.c.ks : a.c.vs) + static_cast<int64_t>(id) * a.c.H + h0;
+#pragma unroll 1
+  for (int h = 0; h < heads; ++h, dst += a.c.sh) {
+    float x[16];
     float amax = 0.f;
-#pragma unroll
-    for (int p = 0; p < PASS; ++p) {
-      const int s = row0 + p * rows;
-      if (s < s_lo || s >= s_hi) continue;
-      const int64_t t = first + (start + s - len);
-      load_chunk(src + t * st + h * sh + d0, vec, x[p]);
-      load_chunk(src + t * st + h * sh + d1, vec, x[p] + 8);
-    }
-#pragma unroll
-    for (int p = 0; p < PASS; ++p) {
-      const int s = row0 + p * rows;
-      if (s < s_lo || s >= s_hi) continue;
-      if (rotated) {
-        const int64_t t = first + (start + s - len);
-        float cs[8], sn[8];
-        angles(a.rope, c, a.pos ? a.pos[t] : start + s, cs, sn);
-        turn(a.rope, x[p], cs, sn);
-      }
+    row_floats(next, x);
+    if (h + 1 < heads && written) next = load_row(src + (h + 1) * sh, d0, d1, vec);
+    if (rotated) turn(a.rope, x, cs, sn);
+    if (written) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float m = fabsf(x[p][i]);
+        const float m = fabsf(x[i]);
         if (m < __int_as_float(0x7f800000)) amax = fmaxf(amax, m);
       }
     }
-    uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));  // magnitudes order as their bits
-    if ((tid & 31) == 0) s_amax[h & 1][tid >> 5] = __uint_as_float(m);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));  // magnitudes order as their bits
+    if ((tid & 31) == 0) s_amax[h & 1][tid >> 5] = m;
     const uint8_t old_byte = scales[h];
     __syncthreads();
-    amax = 0.f;
-#pragma unroll
-    for (int w = 0; w < kAppThreads / 32; ++w) amax = fmaxf(amax, s_amax[h & 1][w]);
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, (tid & 31) < NT / 32 ? s_amax[h & 1][tid & 31] : 0u));
     const int old = kv8_exp(old_byte);
     const int need = kv8_need(amax);
     const int e = s_lo > 0 ? max(old, need) : need;
-    uint8_t* head = pool + h * a.c.sh;
-    const float down = pow2i(-e);
+    if (written) {
+      const float down = pow2i(-e);
+      *reinterpret_cast<uint2*>(dst + d0) = make_uint2(kv8_codes4(x, down), kv8_codes4(x + 4, down));
+      *reinterpret_cast<uint2*>(dst + d1) = make_uint2(kv8_codes4(x + 8, down), kv8_codes4(x + 12, down));
+    } else if (s < bs && s_lo > 0 && e > old) {  // codes of the block's other entries, rounded to the grown scale
+      const float up = pow2i(old - e);
+      uint4 w = *reinterpret_cast<const uint4*>(dst + 16 * c);
+      uint32_t* q = &w.x;
 #pragma unroll
-    for (int p = 0; p < PASS; ++p) {
-      const int s = row0 + p * rows;
-      if (s >= bs) continue;
-      uint8_t* dst = head + s * a.c.ss;
-      if (s >= s_lo && s < s_hi) {
-        *reinterpret_cast<uint2*>(dst + d0) = make_uint2(kv8_codes4(x[p], down), kv8_codes4(x[p] + 4, down));
-        *reinterpret_cast<uint2*>(dst + d1) = make_uint2(kv8_codes4(x[p] + 8, down), kv8_codes4(x[p] + 12, down));
-      } else if (s_lo > 0 && e > old) {  // codes of the block's other entries, rounded to the grown scale
-        const float up = pow2i(old - e);
-        uint4 w = *reinterpret_cast<const uint4*>(dst + 16 * c);
-        uint32_t* q = &w.x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float y[4];
-          kv8_values4(q[i], y);
-          q[i] = kv8_codes4(y, up);
-        }
-        *reinterpret_cast<uint4*>(dst + 16 * c) = w;
+      for (int i = 0; i < 4; ++i) {
+        float y[4];
+        kv8_values4(q[i], y);
+        q[i] = kv8_codes4(y, up);
       }
+      *reinterpret_cast<uint4*>(dst + 16 * c) = w;
     }
     // every thread has read the old scale before the barrier above
     if (tid == 0) scales[h] = static_cast<uint8_t>(e + 127);
   }
 }
 
-template <typename T>
-cudaError_t launch_append(const Kv8AppendArgs& a, cudaStream_t st) {
+template <typename T, int NT>
+cudaError_t launch_append(const Kv8AppendArgs& args, cudaStream_t st) {
+  Kv8AppendArgs a = args;
   const int tpr = a.c.D / 16;
+  // Heads to a thread block: as many as leave two rounds of resident blocks (1024 threads of 64 registers to an SM), so
+  // that what is found once for a block's heads (its sequence, its place, the angles) is shared. 22,000 tokens x 8 heads:
+  // 75 us with one head to a thread block.
+  const int64_t candidates = a.T / a.c.block + 2 * static_cast<int64_t>(a.c.B);
+  a.heads_per_cta = static_cast<int>(std::min<int64_t>(a.c.H, std::max<int64_t>(1, candidates * 2 * a.c.H / (152 * 2 * (1024 / NT)))));
+  a.head_groups = (a.c.H + a.heads_per_cta - 1) / a.heads_per_cta;
+  a.item_ctas = static_cast<int>(candidates * 2 * a.head_groups);
+  a.status_ctas = (a.c.B + NT / 32 - 1) / (NT / 32);
   const int64_t q_items = a.q ? static_cast<int64_t>(a.T) * a.q_heads * tpr : 0;
-  const int64_t ctas = a.status_ctas + static_cast<int64_t>(a.item_ctas) + (q_items + kAppThreads - 1) / kAppThreads;
-  const dim3 grid(static_cast<unsigned>(ctas)), block(kAppThreads);
-  const int pass = (a.c.block * tpr + kAppThreads - 1) / kAppThreads;
-  if (pass == 1) return launch_pdl(kv8_append_kernel<T, 1>, grid, block, st, a);
-  if (pass == 2) return launch_pdl(kv8_append_kernel<T, 2>, grid, block, st, a);
-  return launch_pdl(kv8_append_kernel<T, 4>, grid, block, st, a);
+  const int64_t ctas = a.status_ctas + static_cast<int64_t>(a.item_ctas) + (q_items + NT - 1) / NT;
+  return launch_pdl(kv8_append_kernel<T, NT>, dim3(static_cast<unsigned>(ctas)), dim3(NT), st, a);
+}
+
+template <typename T>
+cudaError_t launch_append_type(const Kv8AppendArgs& a, cudaStream_t st) {
+  const int threads = a.c.block * a.c.D / 16;  // 64 .. 1024: 16 elements each
+  if (threads <= 128) return launch_append<T, 128>(a, st);
+  if (threads == 256) return launch_append<T, 256>(a, st);
+  if (threads == 512) return launch_append<T, 512>(a, st);
+  return launch_append<T, 1024>(a, st);
 }
 
 // ----------------------------------------------------------------- compact --
@@ -469,9 +500,9 @@ __global__ void __launch_bounds__(kCompWarps * 32) kv8_compact_kernel(const __gr
 }  // namespace
 
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, int dtype, cudaStream_t st) {
-  if (dtype == SPEC_F32) return launch_append<float>(a, st);
-  if (dtype == SPEC_BF16) return launch_append<__nv_bfloat16>(a, st);
-  return launch_append<__half>(a, st);
+  if (dtype == SPEC_F32) return launch_append_type<float>(a, st);
+  if (dtype == SPEC_BF16) return launch_append_type<__nv_bfloat16>(a, st);
+  return launch_append_type<__half>(a, st);
 }
 
 cudaError_t launch_kv8_compact(const Kv8CompactArgs& a, cudaStream_t st) {

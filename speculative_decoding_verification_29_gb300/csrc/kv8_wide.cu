@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   Runs runs;
   Start start;
   fence_before();
-  const bool work = uniform(find_run<N>(a, blockIdx.x, false, &runs, &start, sm.tmp)) != 0;
+  const bool work = uniform(find_run<N>(a, blockIdx.x, &runs, &start, sm.tmp)) != 0;
   const int64_t my_tiles = work ? runs.begin(blockIdx.x + 1) - runs.begin(blockIdx.x) : 0;
   __syncthreads();
   fence_after();
@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       if (lane == 0) bar_arrive(smem_addr(&sm.q_ready[seg & 3]));
 
       more = it.next(a);
+      if (!more && own == 0) a.cut[blockIdx.x] = cut_item<N>(runs, blockIdx.x, r, h, t0, t1);
       if (more)  // the next item's queries come from memory by the time they are needed
         for (int row = own; row < it.r.rows; row += 128) {
           const QT* q = static_cast<const QT*>(a.q) + row_at(it.r, it.h, row);
@@ -592,7 +593,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   __syncthreads();
   fence_after();
   if (warp == kMmaWarp) tmem_free(tmem, 512);
-  if (tid == 0) a.gave_up[blockIdx.x] = sm.gave_up;
+  if (tid == 0) {
+    a.gave_up[blockIdx.x] = sm.gave_up;
+    if (!work) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
   griddep_launch_dependents();
 }
 
