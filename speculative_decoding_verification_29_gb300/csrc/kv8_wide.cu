@@ -146,38 +146,35 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       if (!ok || nt <= 0) break;
       fence_after();
       const int n[2] = {steps(nt, rows, 0), steps(nt, rows, 1)};
+      const bool both = n[1] > 0;  // PAIR: a tile's second user is stream 1
 #pragma unroll 1
       for (int s = -1; s < n[0] && ok; ++s) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          if (s >= 0 && s < n[b] && ok) {  // O += P x V
-            const uint32_t j = 2u * (base + (PAIR ? s : 2 * s + b)) + 1, slot = uniform(j % NF);
+          if (s >= 0 && s < n[b]) {  // O += P x V
+            const uint32_t j = 2u * (base + (PAIR ? s : 2 * s + b)) + 1, slot = j % NF;
             // the last item's outputs have been read
             if (b == 0 && s == 0 && seg > 0) ok = bar_wait(smem_addr(&sm.done), (seg - 1) & 1, gave_up);
-            ok = bar_wait(smem_addr(&sm.full16[slot]), (j / NF) & 1, gave_up) &&
-                 bar_wait(smem_addr(&sm.p_ready[b]), (count[b] + s) & 1, gave_up) && ok;
-            ok = __all_sync(0xffffffffu, ok);
+            if (!PAIR || b == 0) ok = bar_wait(smem_addr(&sm.full16[slot]), (j / NF) & 1, gave_up) && ok;
+            ok = bar_wait(smem_addr(&sm.p_ready[b]), (count[b] + s) & 1, gave_up) && ok;
+            __syncwarp();
             fence_after();
-            const uint32_t add = uniform(s > 0);
-            const bool last = uniform(!PAIR || b == 1 || n[1] == 0);  // user of the tile
-            if (ok && elect()) {
+            if (elect() && ok) {
               const uint64_t vd = v_desc + (slot * C::kF16 >> 4);
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k)
-                mma_f16_tmem(tmem + kO + b * kTile, tmem + b * kTile + 8 * k, vd + (k * 2048 >> 4), id_o, k > 0 ? 1 : add);
+                mma_f16_tmem(tmem + kO + b * kTile, tmem + b * kTile + 8 * k, vd + (k * 2048 >> 4), id_o, s > 0 || k > 0);
               commit(smem_addr(&sm.o_full[b]));
-              if (last) commit(smem_addr(&sm.empty16[slot]));
+              if (!PAIR || b == 1 || !both) commit(smem_addr(&sm.empty16[slot]));
             }
             __syncwarp();
           }
-          if (s + 1 < n[b] && ok) {  // the next S = Q x K^T
-            const uint32_t j = 2u * (base + (PAIR ? s + 1 : 2 * (s + 1) + b)), slot = uniform(j % NF);
-            ok = bar_wait(smem_addr(&sm.full16[slot]), (j / NF) & 1, gave_up);
-            ok = __all_sync(0xffffffffu, ok);
+          if (s + 1 < n[b]) {  // the next S = Q x K^T
+            const uint32_t j = 2u * (base + (PAIR ? s + 1 : 2 * (s + 1) + b)), slot = j % NF;
+            if (!PAIR || b == 0) ok = bar_wait(smem_addr(&sm.full16[slot]), (j / NF) & 1, gave_up) && ok;
+            __syncwarp();
             fence_after();
-            const bool last = uniform(!PAIR || b == 1 || n[1] == 0);
-            const bool item_last = uniform(s + 2 == n[b] && (b == 1 || n[1] < n[0]));  // product with these queries
-            if (ok && elect()) {
+            if (elect() && ok) {
               const uint64_t qd = q_desc + (PAIR ? b * C::kF16 >> 4 : 0), kd = k_desc + (slot * C::kF16 >> 4);
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
@@ -185,12 +182,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 mma_f16(tmem + b * kTile, qd + off, kd + off, id_s, k > 0);
               }
               commit(smem_addr(&sm.s_full[b]));
-              if (last) commit(smem_addr(&sm.empty16[slot]));
-              if (item_last) commit(smem_addr(&sm.q_free));
+              if (!PAIR || b == 1 || !both) commit(smem_addr(&sm.empty16[slot]));
+              if (s + 2 == n[b] && (b == 1 || n[1] < n[0])) commit(smem_addr(&sm.q_free));  // the last with these queries
             }
             __syncwarp();
           }
         }
+        ok = __all_sync(0xffffffffu, ok);
       }
       if (!ok) break;
       base += nt;
