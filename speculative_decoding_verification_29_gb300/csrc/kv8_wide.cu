@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               }
               commit(smem_addr(&sm.s_full[b]));
               if (!PAIR || b == 1 || !both) commit(smem_addr(&sm.empty16[slot]));
-              if (s + 2 == n[b] && (b == 1 || n[1] < n[0])) commit(smem_addr(&sm.q_free));  // the last with these queries
+              if (s + 2 == n[b] && (b == 1) == (n[1] == n[0])) commit(smem_addr(&sm.q_free));  // the last with these queries
             }
             __syncwarp();
           }

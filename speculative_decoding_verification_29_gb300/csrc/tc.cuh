@@ -44,17 +44,25 @@ __device__ __forceinline__ bool bar_try_long(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-constexpr int kWaitTries = 100000;  // a wait gives up after these: about two seconds
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+constexpr uint64_t kWaitNs = 2000000000ull;  // a wait gives up after two seconds
 
 // Waits for the barrier's phase; false, with *gave_up set, when the limit ran
 // out. Once a wait of the block has given up no other waits: every role then
 // runs through its loop without touching the tensor core or starting copies.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
   if (bar_try(bar, parity)) return true;
+  uint64_t t0 = 0;
 #pragma unroll 1
-  for (int i = 0; !bar_try_long(bar, parity); ++i) {
+  while (!bar_try_long(bar, parity)) {
     if (*gave_up) return false;
-    if (i == kWaitTries) {
+    const uint64_t t = now_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitNs) {
       *gave_up = 1;
       return false;
     }

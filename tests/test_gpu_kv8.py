@@ -214,6 +214,18 @@ def test_attention(ctx, new, Hq, H, D, bs, dt, tree, how, layout):
     check_attention(c, q, mask, how)
 
 
+@pytest.mark.parametrize("new,Hq,H,D,dt", [((1, 2), 8, 4, 128, BF), ((5, 9), 12, 4, 64, HF), ((9, 16), 32, 4, 128, BF),
+                                           ((9, 16), 32, 4, 64, HF), ((33, 61), 16, 2, 128, HF)])
+def test_attention_many_items(new, Hq, H, D, dt):
+    """Several items to a thread block, of odd and even numbers of tiles, some cut by a block's run."""
+    rng = random.Random(5)
+    B = 14 if new[1] < 30 else 6
+    ctx = [rng.choice([rng.randint(0, 500), rng.randint(500, 2600)]) for _ in range(B)]
+    c = plain.Cache(ctx, [rng.randint(*new) for _ in ctx], H, D, 64, seed=17).fill()
+    g = torch.Generator().manual_seed(15)
+    check_attention(c, (randn(g, sum(c.new), Hq, D) * 2).to(dt))
+
+
 @pytest.mark.parametrize("dt", [BF, HF])
 def test_attention_sharp_and_flat_weights(dt):
     """One entry that takes nearly all of the weight, then hundreds that share it, and the reverse."""
