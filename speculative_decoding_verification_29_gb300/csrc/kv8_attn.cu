@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
               vis = bits;
             }
           }
+          __syncwarp();
         }
         wait_ld();
 

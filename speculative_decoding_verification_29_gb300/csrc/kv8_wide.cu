@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       // row, kBatch rows of a lane group in flight. Rows' places and scales are found while the last item's queries are
       // still in use.
       constexpr int kLanes = D / 8, kRows = 128 / kLanes, kBatch = 8;
+      static_assert(N % (kRows * kBatch) == 0, "whole batches");
       const int chunk = lane % kLanes, sub = own / kLanes;
       for (int row = own; row < N; row += 128) sm.qrow[row] = row_at(r, h, row);
       named_sync(2, 128);
@@ -237,10 +238,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
       };
 #pragma unroll 1
-      for (int row0 = sub; row0 < r.rows; row0 += kRows * kBatch) {
+      for (int row0 = 0; row0 < r.rows; row0 += kRows * kBatch) {  // the same for every lane; places behind the rows repeat the last
         QT e[kBatch][8];
 #pragma unroll
-        for (int z = 0; z < kBatch; ++z) load(min(row0 + z * kRows, N - 1), e[z]);
+        for (int z = 0; z < kBatch; ++z) load(row0 + z * kRows + sub, e[z]);
         float amax[kBatch];
 #pragma unroll
         for (int z = 0; z < kBatch; ++z) {
@@ -256,19 +257,19 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
         for (int z = 0; z < kBatch; ++z) {
           const int eq = min(max(static_cast<int>(__float_as_uint(amax[z]) >> 23) - 127 - 13, -110), 110);
-          if (chunk == 0 && row0 + z * kRows < N) sm.qscale[seg & 3][row0 + z * kRows] = pow2i(eq);
+          if (chunk == 0) sm.qscale[seg & 3][row0 + z * kRows + sub] = pow2i(eq);
         }
       }
       __syncwarp();
       if (seg > 0) bar_wait(smem_addr(&sm.q_free), (seg - 1) & 1, gave_up);
 #pragma unroll 1
-      for (int row0 = sub; row0 < r.rows; row0 += kRows * kBatch) {
+      for (int row0 = 0; row0 < r.rows; row0 += kRows * kBatch) {
         QT e[kBatch][8];
 #pragma unroll
-        for (int z = 0; z < kBatch; ++z) load(min(row0 + z * kRows, N - 1), e[z]);
+        for (int z = 0; z < kBatch; ++z) load(row0 + z * kRows + sub, e[z]);
 #pragma unroll
         for (int z = 0; z < kBatch; ++z) {
-          const int row = min(row0 + z * kRows, N - 1);
+          const int row = row0 + z * kRows + sub;
           const uint32_t inverse = 0x7f000000u - __float_as_uint(sm.qscale[seg & 3][row]);  // of a power of two
           const float down = __uint_as_float(a.negate ? inverse | 0x80000000u : inverse);
           uint32_t v[4];
@@ -408,6 +409,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 vis[1] |= c < 64 ? 0ull : bit;
               }
             }
+            __syncwarp();
           }
           auto bits = [&](int g) { return static_cast<uint32_t>((g < 4 ? vis[0] : vis[1]) >> (16 * (g & 3))); };
           // the largest exponent; NaN scores are passed over here

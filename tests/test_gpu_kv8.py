@@ -183,6 +183,12 @@ ATTN = [
     ([300, 20], [20, 20], 8, 2, 64, 16, BF, True, "odd", "nhd"),
     ([100], [140], 4, 1, 64, 128, BF, False, "heads", "padded"),
     ([260], [2], 64, 1, 128, 64, BF, False, "dense", "hnd"),
+    # row tiles with one or two rows beside full ones
+    ([0, 300, 5], [1, 70, 2], 2, 2, 128, 64, BF, False, "dense", "hnd"),
+    ([20, 300, 0], [1, 70, 3], 4, 2, 64, 32, HF, False, "dense", "hnd"),
+    ([130, 3], [257, 1], 1, 1, 128, 64, HF, False, "dense", "hnd"),
+    ([9], [129], 4, 2, 64, 16, BF, False, "dense", "nhd"),
+    ([700, 40, 0], [129, 128, 1], 1, 1, 64, 128, HF, False, "dense", "hnd"),
 ]
 
 
