@@ -33,6 +33,8 @@
 // leave tensor memory together, each row's maximum crosses lanes by redux and
 // warps by shared memory, the weights are written, and the tile's product runs
 // while the next tiles are worked on.
+#include <string.h>
+
 #include "kv8_attn.cuh"
 
 namespace specv {
@@ -46,7 +48,7 @@ template <int D_, int RW_, int W_, int TERMS_, int CTAS_>
 struct Cfg {
   static constexpr int D = D_, RW = RW_, W = W_, TERMS = TERMS_;
   static constexpr int N = RW * W;
-  static constexpr int EW = (N + 31) / 32;                 // warps that load queries, a row a lane
+  static constexpr int EW = (N + 31) / 32;                 // warps that load queries
   static constexpr int kThreads = W * 128 + EW * 32 + 64;  // softmax, queries, copies and products
   static constexpr int kCtas = CTAS_;                  // resident on an SM
   static constexpr int kSlot = kTile * D;
@@ -245,32 +247,43 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     do {
       const RowTile r = it.r;
       const int r0 = r.rt * N;
-      // the buffer's last item is behind every softmax warp
-      if (seg > 1) bar_wait(smem_addr(&sm.q_free[seg & 1]), ((seg >> 1) - 1) & 1, gave_up);
-      const int token = min(r.n - 1, static_cast<int>(static_cast<uint32_t>(r0 + own) / static_cast<uint32_t>(a.group)));
-      // queries into shared memory, as e4m3 terms of q / 2^eq
-      const QT* q = static_cast<const QT*>(a.q) + (r.first + static_cast<int64_t>(token)) * a.qst +
-                    (it.h * a.group + max(0, min(a.group - 1, r0 + own - token * a.group))) * a.qsh;
-      auto chunk = [&](int d, float* x) {
-        if (vec) {
-          const uint4 u = *reinterpret_cast<const uint4*>(q + d);
-          const QT* e = reinterpret_cast<const QT*>(&u);
+      // Queries into shared memory, as e4m3 terms of q / 2^eq: kLanes lanes a row. Up to eight loads a lane are in
+      // flight at once; an item of more rows is read a second time, from L2, when its scale is known.
+      constexpr int kLanes = D / 8, kRows = C::EW * 32 / kLanes, kSteps = (N + kRows - 1) / kRows,
+                    kBatch = kSteps <= 8 ? kSteps : kSteps / 2;
+      static_assert(kSteps % kBatch == 0 && N % kRows == 0, "whole batches of whole rows");
+      const int d = (lane % kLanes) * 8, sub = own / kLanes;
+      uint4 u[kBatch];
+      auto load = [&](int z0) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = to_f(e[k]);
-        } else {
+        for (int z = 0; z < kBatch; ++z) {
+          const uint32_t flat = static_cast<uint32_t>(r0 + min((z0 + z) * kRows + sub, r.rows - 1)),
+                         tok = flat / static_cast<uint32_t>(a.group);
+          const QT* q = static_cast<const QT*>(a.q) + (r.first + static_cast<int64_t>(tok)) * a.qst +
+                        (it.h * a.group + static_cast<int>(flat - tok * a.group)) * a.qsh + d;
+          if (vec) {
+            u[z] = *reinterpret_cast<const uint4*>(q);
+          } else {
+            QT e[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = to_f(q[d + k]);
+            for (int k = 0; k < 8; ++k) e[k] = q[k];
+            memcpy(&u[z], e, 16);
+          }
         }
       };
       float amax = 0.f;
-      if (own < r.rows) {
-#pragma unroll 8
-        for (int d = 0; d < D; d += 8) {
-          float x[8];
-          chunk(d, x);
+#pragma unroll 1
+      for (int z0 = 0; z0 < kSteps; z0 += kBatch) {
+        load(z0);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (fabsf(x[k]) < -kNegInf) amax = fmaxf(amax, fabsf(x[k]));
+        for (int z = 0; z < kBatch; ++z) {
+          QT e[8];
+          memcpy(e, &u[z], 16);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float m = fabsf(to_f(e[k]));
+            if (m < -kNegInf) amax = fmaxf(amax, m);
+          }
         }
       }
       amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
@@ -282,22 +295,23 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       }
       const int eq = kv8_need(amax, -120, 120);
       const float down = a.negate ? -pow2i(-eq) : pow2i(-eq);
+      if (seg > 1) bar_wait(smem_addr(&sm.q_free[seg & 1]), ((seg >> 1) - 1) & 1, gave_up);
+      __syncwarp();
       uint8_t* q_to = q_smem + (seg & 1) * C::kQ;
-      if (own < N) {
-#pragma unroll 4
-        for (int d = 0; d < D; d += 8) {
+#pragma unroll 1
+      for (int z0 = 0; z0 < kSteps; z0 += kBatch) {
+        if (kBatch < kSteps) load(z0);
+#pragma unroll
+        for (int z = 0; z < kBatch; ++z) {
+          const int row = (z0 + z) * kRows + sub;
+          QT e[8];
+          memcpy(e, &u[z], 16);
           float x[8];
-          if (own < r.rows) {
-            chunk(d, x);
-          } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = 0.f;
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] *= down;
+          for (int k = 0; k < 8; ++k) x[k] = row < r.rows ? to_f(e[k]) * down : 0.f;
           uint2 codes[C::TERMS];
           split8<C::TERMS>(x, codes);
-          const uint32_t o = swz<D>(own, d);
+          const uint32_t o = swz<D>(row, d);
 #pragma unroll
           for (int t = 0; t < C::TERMS; ++t) *reinterpret_cast<uint2*>(q_to + t * N * D + o) = codes[t];
         }
@@ -383,22 +397,23 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             const uint32_t vslot = (2u * i + 1) % NS;
             bar_wait(smem_addr(&sm.full[vslot]), ((2u * i + 1) / NS) & 1, gave_up);
             uint4* vrow = reinterpret_cast<uint4*>(ring + vslot * C::kSlot + own * D);
-            bool nan = false;
-#pragma unroll 2
-            for (int k = 0; k < D / 16; ++k) {
-              uint4 u = vrow[k];
-              uint32_t any = 0;
-              uint32_t* w = &u.x;
+            if (slot >= it.end) {
 #pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const uint32_t m = slot >= it.end ? 0xffffffffu : __vcmpeq4(w[z] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                any |= m;
-                w[z] &= ~m;
+              for (int k = 0; k < D / 16; ++k) vrow[k] = make_uint4(0, 0, 0, 0);
+            } else {
+              uint32_t nan = 0;
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint4 u = vrow[k];
+                nan |= nan_codes(u.x) | nan_codes(u.y) | nan_codes(u.z) | nan_codes(u.w);
               }
-              if (any) vrow[k] = u;
-              nan |= any != 0;
+              if (nan & 0x80808080u) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(vrow);
+#pragma unroll 1
+                for (int k = 0; k < D / 4; ++k) w[k] &= ~__vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                sm.nan[seg & 1] = 1;
+              }
             }
-            if (nan && slot < it.end) sm.nan[seg & 1] = 1;
           }
           if (slot >= it.ctx) {
             const int row = it.r0 + row_base, j = slot - it.ctx;  // row and token of the step

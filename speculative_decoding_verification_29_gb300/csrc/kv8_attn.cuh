@@ -216,6 +216,9 @@ __device__ __forceinline__ float exp2_whole(float d) {
   return d != d ? d : p;
 }
 
+// Bit 7 of a byte of the result is set where w holds a NaN code there.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
+
 // Whether the step's token i sees its token j.
 __device__ __forceinline__ bool sees(const Kv8AttnArgs& a, int b, int i, int j) {
   return a.tree ? a.tree[(static_cast<int64_t>(b) * a.max_tokens + i) * a.max_tokens + j] != 0 : j <= i;
@@ -245,51 +248,65 @@ __device__ __forceinline__ void copy_tiles(const Kv8AttnArgs& a, const Start& st
   do {
     const int pages = (it.r.end + bs - 1) / bs;
     const int32_t* table = a.c.table + static_cast<int64_t>(it.r.b) * a.c.max_blocks;
-    int id = -1, ke = 0, ve = 0;
+    // 32 pages' ids and scales at a time, one a lane; those of the next 32 are on their way meanwhile
+    auto page_id = [&](int page) {
+      int id = -1;  // behind the sequence
+      if (page < pages) {
+        id = table[page];
+        if (id < 0 || id >= a.c.num_blocks) id = -2;  // outside the pool
+      }
+      return id;
+    };
+    auto scale_at = [&](const uint8_t* scales, int id) {
+      return id >= 0 ? scales[static_cast<int64_t>(id) * a.c.H + it.h] : static_cast<uint8_t>(127);
+    };
+    int id = -1, id_next = page_id(it.t0 * ppt + lane);
+    uint8_t ke = 127, ve = 127, ke_next = scale_at(a.c.ks, id_next), ve_next = scale_at(a.c.vs, id_next);
+#pragma unroll 1
     for (int t = it.t0, g = 0; t < it.t1; ++t, g += ppt, ++i) {
-      if ((g & 31) == 0) {  // the next 32 pages' ids and scales, one a lane
-        const int page = t * ppt + lane;
-        id = -1;  // behind the sequence
-        if (page < pages) {
-          id = table[page];
-          if (id < 0 || id >= a.c.num_blocks) id = -2;  // outside the pool
-        }
-        ke = ve = 0;
-        if (id >= 0) {
-          const int64_t s = static_cast<int64_t>(id) * a.c.H + it.h;
-          ke = kv8_exp(a.c.ks[s]);
-          ve = kv8_exp(a.c.vs[s]);
-        }
+      if ((g & 31) == 0) {
+        id = id_next;
+        ke = ke_next;
+        ve = ve_next;
+        id_next = page_id(t * ppt + 32 + lane);
+      }
+      if ((g & 31) == 16) {
+        ke_next = scale_at(a.c.ks, id_next);
+        ve_next = scale_at(a.c.vs, id_next);
       }
       const int from = (g & 31) + (lane & (ppt - 1));
-      const int my_id = __shfl_sync(0xffffffffu, id, from), my_ke = __shfl_sync(0xffffffffu, ke, from),
-                my_ve = __shfl_sync(0xffffffffu, ve, from);
+      const int my_id = __shfl_sync(0xffffffffu, id, from);
       const bool mine = lane < ppt && my_id >= 0;
       const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine)) * bs * D);
       auto at = [&](int name) { return name == 0 ? 0 : (name == 1 ? it.h : my_id); };
       const int x1 = at(a.order & 3), x2 = at((a.order >> 2) & 3), x3 = at((a.order >> 4) & 3);
-#pragma unroll
+#pragma unroll 1
       for (int part = 0; part < 2; ++part, ++fill) {
         const uint32_t slot = fill % NS, bar = smem_addr(&sm.full[slot]);
         bool ok = true;
         if (fill >= NS) ok = bar_wait(smem_addr(&sm.empty[slot]), (fill / NS - 1) & 1, gave_up);
         ok = __all_sync(0xffffffffu, ok);
-        if (part == 0 && lane < ppt) {
-          sm.page[i % kMetaRing][lane] =
-              make_float4(my_id != -2 ? pow2i(my_ke) : __int_as_float(0x7fffffff), static_cast<float>(my_ve), pow2i(-my_ve), 0.f);
-        }
-        __syncwarp();
         if (!ok) continue;  // a wait gave up: no copy is started any more
         begun = fill + 1;
-        if (lane == 0) bar_expect(bar, bytes);
-        __syncwarp();
+        // the copies begin before the scales are there; the barrier's one arrival comes after both
         if (mine)
           load_4d(smem_addr(ring + slot * (kTile * D) + lane * bs * D), part == 0 ? &kmap : &vmap, bar, 0, x1, x2, x3);
+        if (part == 0) {
+          const int my_ke = kv8_exp(static_cast<uint8_t>(__shfl_sync(0xffffffffu, static_cast<int>(ke), from))),
+                    my_ve = kv8_exp(static_cast<uint8_t>(__shfl_sync(0xffffffffu, static_cast<int>(ve), from)));
+          if (lane < ppt)
+            sm.page[i % kMetaRing][lane] = make_float4(my_id != -2 ? pow2i(my_ke) : __int_as_float(0x7fffffff),
+                                                       static_cast<float>(my_ve), pow2i(-my_ve), 0.f);
+        }
+        __syncwarp();
+        if (lane == 0) bar_expect(bar, bytes);
       }
     }
   } while (it.next(a));
   if (*gave_up)  // copies that are still in flight write this block's memory
+#pragma unroll 1
     for (uint32_t f = begun > NS ? begun - NS : 0; f < begun; ++f)
+#pragma unroll 1
       for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.full[f % NS]), (f / NS) & 1); ++k) {
       }
 }

@@ -313,20 +313,28 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const uint32_t src_turn = D == 128 ? turn : static_cast<uint32_t>((own >> 1) & 3) << 4;
           bool nan = false;
           auto convert = [&](auto check) {
-#pragma unroll(decltype(check)::value ? 1 : D / 16)
+#pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               uint4 u = *reinterpret_cast<const uint4*>(src + ((16u * c) ^ src_turn));
-              uint32_t* w = &u.x;
               if (decltype(check)::value) {
                 // Slots behind the sequence hold no values, and a NaN value must not reach the rows that do not see it
                 // through a weight of 0: both are cleared here, and the rows that see a NaN get it at the item's end.
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                  const uint32_t m = slot >= r.end ? 0xffffffffu : __vcmpeq4(w[z] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                  nan |= m != 0;
-                  w[z] &= ~m;
+                if (slot >= r.end) {
+                  u = make_uint4(0, 0, 0, 0);
+                } else if ((nan_codes(u.x) | nan_codes(u.y) | nan_codes(u.z) | nan_codes(u.w)) & 0x80808080u) {
+                  nan = true;
+#pragma unroll 1
+                  for (int z = 0; z < 4; ++z) {
+                    const uint32_t x = z == 0 ? u.x : (z == 1 ? u.y : (z == 2 ? u.z : u.w));
+                    const uint32_t y = x & ~__vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    if (z == 0) u.x = y;
+                    else if (z == 1) u.y = y;
+                    else if (z == 2) u.z = y;
+                    else u.w = y;
+                  }
                 }
               }
+              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
               uint32_t v[8];
 #pragma unroll
               for (int z = 0; z < 4; ++z) {
@@ -340,7 +348,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           };
           if (part == 1 && masked) convert(std::true_type{});
           else convert(std::false_type{});
-          if (nan && slot < r.end) sm.nan[seg & 3] = 1;
+          if (nan) sm.nan[seg & 3] = 1;
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
