@@ -86,7 +86,7 @@ enum {
   SPEC_ERR_ARG = -1,           /* a size, pointer, dtype or temperature is invalid */
   SPEC_ERR_ALIGN = -2,         /* workspace NULL, misaligned (256 B) or too small */
   SPEC_ERR_CUDA = -3,          /* a kernel launch or an enqueued copy failed */
-  SPEC_ERR_TIMEOUT = -4,       /* reserved: no kernel of this library waits on a flag, so none times out */
+  SPEC_ERR_TIMEOUT = -4,       /* reserved: waits inside kernels are reported in row_status (SPEC_ROW_TIMEOUT) */
   SPEC_ERR_UNIMPLEMENTED = -5, /* sizes beyond the documented limits */
   /* older names of the same codes */
   SPEC_ERR_WORKSPACE = SPEC_ERR_ALIGN,
@@ -491,19 +491,23 @@ int spec_kv8_append(const spec_kv8_cache* cache, const void* keys, int64_t k_str
  *       spec_merge_trees with N = max_tokens)
  *   sm_scale      finite
  *   q_heads       a multiple of kv_heads, at most 64 * kv_heads
- * Scores, maxima, sums and the accumulated output are fp32; queries and
- * softmax weights enter the products as two (bf16) or three (fp16) e4m3 terms.
- * The keys' and values' codes enter the tensor cores as they are.
- * Outputs: out; row_status [B] int32: SPEC_ROW_CACHE where the sequence's lengths
- * are invalid (cu_tokens not rising or outside [0, T], more than max_tokens,
- * cache_len negative or beyond the table) or one of its blocks' ids is outside
- * the pool: rows that would read it, and all rows of a sequence with
- *       invalid lengths and valid cu_tokens, are NaN. Tokens of no
- * sequence are not written.
+ * Scores, maxima, sums and the accumulated output are fp32. Up to 64 rows
+ * (max_tokens * q_heads / kv_heads), queries and softmax weights enter the
+ * products as two (bf16) or three (fp16) e4m3 terms and the cache's codes as they
+ * are; above, queries, weights and codes enter as fp16 (codes exactly, queries over
+ * a power of two of their row). A product adds 128 positions in fp32.
+ * Outputs: out, which must not overlap queries; row_status [B] int32:
+ * SPEC_ROW_CACHE where the sequence's lengths are invalid (cu_tokens not rising
+ * or outside [0, T], more than max_tokens, cache_len negative or beyond the
+ * table): its rows are NaN where cu_tokens names some; or where the id of a block
+ * that it uses is outside the pool: the rows that see that block are NaN (rows that
+ * see none of its entries, but others of the same 128 positions, may be too).
+ * SPEC_ROW_TIMEOUT: see there; the rows hold nothing of use. Tokens of no sequence
+ * are not written.
  * workspace: spec_kv8_workspace_bytes(...) bytes, 256-byte aligned, needing no
  * initialisation. Errors: SPEC_ERR_ARG, SPEC_ERR_WORKSPACE as usual;
  * SPEC_ERR_UNSUPPORTED beyond the limits (T * q_heads < 2^31; with tree_mask
- * max_tokens <= 1024). */
+ * max_tokens <= 1024; B times the 256-row tiles of a sequence < 2^31). */
 size_t spec_kv8_workspace_bytes(const spec_kv8_cache* cache, int q_heads, int max_tokens, int dtype);
 int spec_kv8_attention(const spec_kv8_cache* cache, const void* queries, int64_t q_stride_token,
                        int64_t q_stride_head, int dtype, int T, int q_heads, const int32_t* cu_tokens, int max_tokens,

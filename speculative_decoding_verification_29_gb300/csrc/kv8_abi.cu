@@ -5,7 +5,6 @@
 
 #include <algorithm>
 
-
 #include "kv8.h"
 
 using namespace specv;
@@ -62,6 +61,7 @@ int vec16(const void* p, int64_t token, int64_t head, int size) {
 // doubles (1 / (2 pi) itself is given as one), exact to about 2^-100 before
 // the rounding.
 uint64_t turn_fraction(double f) {
+  if (f < 0) return 0 - turn_fraction(-f);  // below, floor must not round
   const double hi_c = 0.15915494309189535, lo_c = -9.8393383374256206e-18;  // 1 / (2 pi) = hi_c + lo_c
   double hi = f * hi_c;
   double lo = fma(f, hi_c, -hi) + f * lo_c;

@@ -110,6 +110,20 @@ def test_append_far_positions_and_tree_positions():
     assert (r["q_out"].cpu().double() - wq).abs().max() <= 4 * 2.0 ** -21
 
 
+def test_append_turns_backwards():
+    """Frequencies and positions below zero: turning by (-f, p) is turning by (f, -p), bit for bit, and right."""
+    c = plain.Cache([0], [5], 1, 128, 16)
+    g = torch.Generator().manual_seed(4)
+    k, q = randn(g, 5, 1, 128), randn(g, 5, 2, 128)
+    pos = torch.tensor([1, 3, 1000, 10 ** 6 + 1, 2 ** 31 - 1], dtype=torch.int32)
+    freq = [10.0 ** (-i / 4.0) for i in range(64)]  # down to 1.8e-16
+    a, b = (sv().spec_kv8_append(k.cuda(), k.cuda(), *c.to("cuda"), c.cu.cuda(), inv_freq=[s * f for f in freq],
+                                 positions=(-s * pos).cuda(), q=q.cuda())["q_out"].cpu() for s in (1, -1))
+    assert torch.equal(a, b)
+    wq = torch.stack([plain.rotate(q[t].double(), -int(pos[t]), freq, False) for t in range(5)])
+    assert (a.double() - wq).abs().max() <= 4 * 2.0 ** -21
+
+
 def test_append_special_values():
     """Zeros, infinities, NaN, and magnitudes outside the scales' range."""
     c = plain.Cache([0, 3], [8, 2], 2, 64, 16).fill(upto=[0, 3])
