@@ -517,14 +517,21 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
               l[q + 1] = s.y;
               uint16_t c;
               asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(w1), "f"(w0));
+              // Two terms keep 8 bits, so what is left of f16's 11 serves; three keep more, and their rest is taken in fp32.
               uint32_t rest;
-              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(rest) : "f"(w1), "f"(w0));
+              if (C::TERMS == 2) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(rest) : "f"(w1), "f"(w0));
 #pragma unroll
               for (int u = 0; u < C::TERMS; ++u) {
                 if (u > 0) {
                   uint32_t back;
                   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(c));
-                  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(rest) : "r"(back));
+                  if (C::TERMS > 2 && u == 1) {
+                    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&back));
+                    const float2 d = fma2(b, make_float2(-1.f, -1.f), make_float2(w0, w1));
+                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(rest) : "f"(d.y), "f"(d.x));
+                  } else {
+                    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(rest) : "r"(back));
+                  }
                   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(rest));
                 }
                 if (j == 0) code[u][j4 / 4] = c;
