@@ -112,16 +112,21 @@ __device__ __forceinline__ int kv8_exp(uint8_t byte) {
 
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// Four codes of x[0..3] * s: nearest even, clamped to +-448; an infinite or
-// NaN x gives the NaN code.
+// Four codes of x[0..3] * s: nearest even, clamped to +-448; NaN gives the NaN
+// code. No x is infinite.
+__device__ __forceinline__ uint32_t kv8_codes4_finite(const float* x, float s) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1] * s), "f"(x[0] * s));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3] * s), "f"(x[2] * s));
+  return static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
+}
+
+// The same for any x: an infinite one gives the NaN code.
 __device__ __forceinline__ uint32_t kv8_codes4(const float* x, float s) {
   float y[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) y[i] = fabsf(x[i]) < __int_as_float(0x7f800000) ? x[i] * s : __int_as_float(0x7fffffff);
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1]), "f"(y[0]));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[3]), "f"(y[2]));
-  return static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
+  for (int i = 0; i < 4; ++i) y[i] = fabsf(x[i]) < __int_as_float(0x7f800000) ? x[i] : __int_as_float(0x7fffffff);
+  return kv8_codes4_finite(y, s);
 }
 
 // Four codes as floats.

@@ -28,6 +28,8 @@ namespace specv {
 
 namespace {
 
+constexpr float kInf = __builtin_huge_valf();
+
 // ------------------------------------------------------------ elements --
 
 template <typename T>
@@ -226,6 +228,15 @@ __device__ __forceinline__ void row_floats(const Row16<T>& r, float* x) {
   for (int k = 0; k < 16; ++k) x[k] = Act<T>::get(&e[k]);
 }
 
+// The largest of the block's values (none negative, none NaN), in every thread.
+template <int NT>
+__device__ __forceinline__ float block_max(float v, uint32_t* s) {
+  const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v));  // magnitudes order as their bits
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = m;
+  __syncthreads();
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < NT / 32 ? s[threadIdx.x & 31] : 0u));
+}
+
 // A thread holds 16 elements of one slot (NT >= block * head_dim / 16). A thread block takes heads_per_cta heads in turn: the angles and the
 // block's place are found once, and a head's rows are loaded while the head
 // before is rotated and stored.
@@ -291,25 +302,37 @@ __global__ void __launch_bounds__(NT) kv8_append_kernel(const __grid_constant__ 
     row_floats(next, x);
     if (h + 1 < heads && written) next = load_row(src + (h + 1) * sh, d0, d1, vec);
     if (rotated) turn(a.rope, x, cs, sn);
-    if (written) {
+    if (written) {  // a maximum passes over NaN
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float m = fabsf(x[i]);
-        if (m < __int_as_float(0x7f800000)) amax = fmaxf(amax, m);
-      }
+      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
     }
-    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));  // magnitudes order as their bits
-    if ((tid & 31) == 0) s_amax[h & 1][tid >> 5] = m;
+    const bool infinite = amax == kInf;
     const uint8_t old_byte = scales[h];
-    __syncthreads();
-    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, (tid & 31) < NT / 32 ? s_amax[h & 1][tid & 31] : 0u));
+    amax = block_max<NT>(amax, s_amax[h & 1]);
+    if (amax == kInf) {  // the whole block: the largest finite magnitude again
+      amax = 0.f;
+      if (written) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float m = fabsf(x[i]);
+          if (m < kInf) amax = fmaxf(amax, m);
+        }
+      }
+      __syncthreads();  // the first maxima have been read
+      amax = block_max<NT>(amax, s_amax[h & 1]);
+    }
     const int old = kv8_exp(old_byte);
     const int need = kv8_need(amax);
     const int e = s_lo > 0 ? max(old, need) : need;
     if (written) {
       const float down = pow2i(-e);
-      *reinterpret_cast<uint2*>(dst + d0) = make_uint2(kv8_codes4(x, down), kv8_codes4(x + 4, down));
-      *reinterpret_cast<uint2*>(dst + d1) = make_uint2(kv8_codes4(x + 8, down), kv8_codes4(x + 12, down));
+      if (infinite) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (fabsf(x[i]) == kInf) x[i] = __int_as_float(0x7fffffff);
+      }
+      *reinterpret_cast<uint2*>(dst + d0) = make_uint2(kv8_codes4_finite(x, down), kv8_codes4_finite(x + 4, down));
+      *reinterpret_cast<uint2*>(dst + d1) = make_uint2(kv8_codes4_finite(x + 8, down), kv8_codes4_finite(x + 12, down));
     } else if (s < bs && s_lo > 0 && e > old) {  // codes of the block's other entries, rounded to the grown scale
       const float up = pow2i(old - e);
       uint4 w = *reinterpret_cast<const uint4*>(dst + 16 * c);
