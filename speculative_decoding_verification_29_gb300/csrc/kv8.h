@@ -15,6 +15,7 @@ namespace specv {
 constexpr int kKv8ExpLo = -40, kKv8ExpHi = 40;  // the scales' exponents
 constexpr float kKv8Max = 448.f;                // the largest e4m3 code
 constexpr int kKv8MaxPath = 64;
+constexpr int kSms = 152;
 
 struct Kv8Pool {
   uint8_t* k;

@@ -633,8 +633,19 @@ cudaError_t launch_rows(const Kv8AttnArgs& a, int rows, const CUtensorMap& k, co
 
 }  // namespace
 
+// Rows of an item, by the most rows that a sequence can have. A few rows are cheapest with slots as the products' rows: 16
+// rows need so little shared and tensor memory that two thread blocks share an SM and hide each other's waits. From 65 rows
+// on a row of scores a lane is cheaper, two row tiles of 128 to an item when there are more than 128.
+// B = 64, contexts of 1500 to 6500 tokens, 8 KV heads of 128, bf16, us (16 sequences from 132 rows on):
+//   rows of a sequence    4     16     32     36     48     52     64     68    128    132    256
+//   as chosen            91     88    127    143    147    175    178    193    209     87    114
+//   32 rows an item     121    113    127
+//   64                  164    157    170    164    165    176    178
+//   128 (kv8_wide)      167    159    174    172    168    178    181    192    209    107    121
+//   256 (kv8_wide)      204    191    212    206    195    210    215    226    234     87    113
 int kv8_attention_rows(int64_t max_rows) {
-  return max_rows <= 16 ? 16 : (max_rows <= 32 ? 32 : (max_rows <= 48 ? 48 : (max_rows <= 64 ? 64 : (max_rows <= 128 ? 128 : 256))));
+  if (max_rows <= 64) return max_rows <= 16 ? 16 : static_cast<int>((max_rows + 15) / 16 * 16);
+  return max_rows <= 128 ? 128 : 256;
 }
 
 int kv8_attention_parts(int rows) { return rows <= 16 ? 2 * kSms : kSms; }

@@ -394,7 +394,6 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
   }
 }
 
-constexpr int kSms = 152;
 
 // The join of an attention launch with row tiles of N rows.
 template <typename QT, int D, int N>
