@@ -71,6 +71,23 @@ struct Wide {
 __device__ __forceinline__ __half2 abs2(const __half* e) { return __habs2(__half2(e[0], e[1])); }
 __device__ __forceinline__ __nv_bfloat162 abs2(const __nv_bfloat16* e) { return __habs2(__nv_bfloat162(e[0], e[1])); }
 
+// u[k] of lane j of four neighbouring lanes becomes u[j] of its lane k.
+__device__ __forceinline__ void exchange4(uint4* u, int lane) {
+#pragma unroll
+  for (int o = 1; o <= 2; o *= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & o) continue;
+      const uint4 send = up ? u[k] : u[k + o];
+      const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, send.x, o), __shfl_xor_sync(0xffffffffu, send.y, o),
+                                   __shfl_xor_sync(0xffffffffu, send.z, o), __shfl_xor_sync(0xffffffffu, send.w, o));
+      if (up) u[k] = got;
+      else u[k + o] = got;
+    }
+  }
+}
+
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -522,57 +539,106 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (!whole && row < rows && (PAIR || b == 0)) a.part_ml[part * N + row] = make_float2(ref, l);
         const bool nan = sm.nan[seg & 3] != 0;  // set before the weights of its tile were used
-        // the streams of one row tile take half of the dimensions each
-        constexpr int kDims = PAIR ? D : D / 2;
-        const int d0 = PAIR ? 0 : b * kDims;
+        // the dimensions from d on in which a value that this row sees is NaN
+        auto mark_nan = [&](auto& v, int d) {
+          const int last = min(it.end, it.t1 * kTile);
+          for (int slot = max(t0, it.part) * kTile; slot < last; ++slot) {
+            if (slot >= ctx && !sees(a, it.b, tok, slot - ctx)) continue;
+            const int id = a.c.table[static_cast<int64_t>(it.b) * a.c.max_blocks + slot / a.c.block];
+            if (id < 0 || id >= a.c.num_blocks) continue;
+            const uint8_t* code = a.c.v + id * a.c.sb + it.h * a.c.sh + (slot % a.c.block) * a.c.ss + d;
+#pragma unroll
+            for (int k = 0; k < static_cast<int>(sizeof(v) / sizeof(v[0])); ++k)
+              if ((code[k] & 0x7f) == 0x7f) v[k] = __int_as_float(0x7fffffff);
+          }
+        };
+        if constexpr (PAIR) {
+          // Four lanes exchange 64 bytes of their rows, so that a store instruction meets eight rows, not 32. Where the
+          // streams add each other's sums (below) that costs more than it gives: 128 rows of 64 sequences, 216 and 206 us.
+          const int row4 = row & ~3, part4 = lane & 3;
+          QT* out4[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            out4[k] = reinterpret_cast<QT*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), (lane & ~3) + k));
 #pragma unroll 1
-        for (int d = d0; d < d0 + kDims; d += 16) {
-          uint32_t x[16], z[16];
-          float v[16];
-          if (steps_here > 0) tmem_ld<16>(o_at + d, x);
-          const bool both = !PAIR && n[0] > 0 && n[1] > 0;
-          if (both) tmem_ld<16>(lanes + kO + (1 - b) * kTile + d, z);
-          if (!PAIR && steps_here == 0) tmem_ld<16>(lanes + kO + (1 - b) * kTile + d, z);
-          wait_ld();
+          for (int d = 0; d < D; d += 32) {
+            uint32_t x[32];
+            float v[32];
+            tmem_ld<32>(o_at + d, x);
+            wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            v[k] = steps_here > 0 ? a0 * __uint_as_float(x[k]) : 0.f;
-            if (both || (!PAIR && steps_here == 0)) v[k] = fmaf(a1, __uint_as_float(z[k]), v[k]);
-          }
-          if (nan) {  // dimensions in which a value that this row sees is NaN
-            const int last = min(it.end, it.t1 * kTile);
-            for (int slot = max(t0, it.part) * kTile; slot < last; ++slot) {
-              if (slot >= ctx && !sees(a, it.b, tok, slot - ctx)) continue;
-              const int id = a.c.table[static_cast<int64_t>(it.b) * a.c.max_blocks + slot / a.c.block];
-              if (id < 0 || id >= a.c.num_blocks) continue;
-              const uint8_t* code = a.c.v + id * a.c.sb + it.h * a.c.sh + (slot % a.c.block) * a.c.ss + d;
+            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(x[k]);
+            if (nan) mark_nan(v, d);
+            __syncwarp();
+            if (!whole) {
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if ((code[k] & 0x7f) == 0x7f) v[k] = __int_as_float(0x7fffffff);
-            }
-          }
-          if (row >= rows) {
-          } else if (!whole) {
-            float4* to = reinterpret_cast<float4*>(a.part_o + (part * N + row) * D + d);
+              for (int half = 0; half < 2; ++half) {
+                uint4 u[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) to[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          } else {
-            QT h[16];
+                for (int k = 0; k < 4; ++k) memcpy(&u[k], v + 16 * half + 4 * k, 16);
+                exchange4(u, lane);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) h[k] = from_f<QT>(v[k] * inv);
-            if (vec) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                uint4 u;
-                memcpy(&u, h + 8 * k, 16);
-                *reinterpret_cast<uint4*>(out + d + 8 * k) = u;
+                for (int k = 0; k < 4; ++k)
+                  if (row4 + k < rows)
+                    *reinterpret_cast<uint4*>(a.part_o + (part * N + row4 + k) * D + d + 16 * half + 4 * part4) = u[k];
               }
             } else {
+              QT h[32];
 #pragma unroll
-              for (int k = 0; k < 16; ++k) out[d + k] = h[k];
+              for (int k = 0; k < 32; ++k) h[k] = from_f<QT>(v[k] * inv);
+              if (vec) {
+                uint4 u[4];
+                memcpy(u, h, 64);
+                exchange4(u, lane);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (row4 + k < rows) *reinterpret_cast<uint4*>(out4[k] + d + 8 * part4) = u[k];
+              } else if (row < rows) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) out[d + k] = h[k];
+              }
             }
+            __syncwarp();
           }
-          __syncwarp();
+        } else {
+          // the streams take half of the dimensions each
+          const bool both = n[0] > 0 && n[1] > 0;
+#pragma unroll 1
+          for (int d = b * (D / 2); d < (b + 1) * (D / 2); d += 16) {
+            uint32_t x[16], z[16];
+            float v[16];
+            if (steps_here > 0) tmem_ld<16>(o_at + d, x);
+            if (both || steps_here == 0) tmem_ld<16>(lanes + kO + (1 - b) * kTile + d, z);
+            wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              v[k] = steps_here > 0 ? a0 * __uint_as_float(x[k]) : 0.f;
+              if (both || steps_here == 0) v[k] = fmaf(a1, __uint_as_float(z[k]), v[k]);
+            }
+            if (nan) mark_nan(v, d);
+            if (row >= rows) {
+            } else if (!whole) {
+              float4* to = reinterpret_cast<float4*>(a.part_o + (part * N + row) * D + d);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) to[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            } else {
+              QT h[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) h[k] = from_f<QT>(v[k] * inv);
+              if (vec) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  uint4 u;
+                  memcpy(&u, h + 8 * k, 16);
+                  *reinterpret_cast<uint4*>(out + d + 8 * k) = u;
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) out[d + k] = h[k];
+              }
+            }
+            __syncwarp();
+          }
         }
       }
       fence_before();
@@ -584,15 +650,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
   };
 
-  // 512 threads of 128 registers; a softmax thread holds a row's 128 scores and takes from the others
+  // 512 threads of 128 registers; a softmax thread holds a row's 128 scores and takes from the others (176, 80 and 80:
+  // prompts 619 us, 591 with 168, 88 and 88)
   if (warp < kConvWarp) {
     more_registers<168>();
     if (work) softmax();
   } else if (warp < kLoadWarp) {
-    fewer_registers<80>();
+    fewer_registers<88>();
     if (work) convert_tiles();
   } else {
-    fewer_registers<96>();
+    fewer_registers<88>();
     if (work && warp == kLoadWarp) copy_tiles<N, D, NS>(a, start, my_tiles, kmap, vmap, ring, sm, gave_up);
     if (work && warp == kMmaWarp) products();
   }
