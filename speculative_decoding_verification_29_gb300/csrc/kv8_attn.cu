@@ -33,6 +33,14 @@
 // leave tensor memory together, each row's maximum crosses lanes by redux and
 // warps by shared memory, the weights are written, and the tile's product runs
 // while the next tiles are worked on.
+//
+// What bounds it. One row of 32 heads (decode, 64 sequences of 1500 to 6500
+// tokens, 8 KV heads of 128): memory, 548 MB in 91 us, 6.0 TB/s, 0.89 of a
+// copy. Nine rows (verification, the same cache): 143 us, 3.9 TB/s, where the
+// softmax groups' instructions (62% of issue slots) and the barrier between the
+// tile's four maxima and its weights set the step of 2100 clocks a tile; the
+// products take 700 of them. One sequence of 517 tokens: 11 us, a chain of
+// lengths, table, queries, one tile a thread block, and the join.
 #include <string.h>
 
 #include "kv8_attn.cuh"
@@ -638,11 +646,11 @@ cudaError_t launch_rows(const Kv8AttnArgs& a, int rows, const CUtensorMap& k, co
 // on a row of scores a lane is cheaper, two row tiles of 128 to an item when there are more than 128.
 // B = 64, contexts of 1500 to 6500 tokens, 8 KV heads of 128, bf16, us (16 sequences from 132 rows on):
 //   rows of a sequence    4     16     32     36     48     52     64     68    128    132    256
-//   as chosen            91     88    127    143    147    175    178    193    209     87    114
+//   as chosen            91     88    126    143    146    175    178    191    208     78     97
 //   32 rows an item     121    113    127
 //   64                  164    157    170    164    165    176    178
-//   128 (kv8_wide)      167    159    174    172    168    178    181    192    209    107    121
-//   256 (kv8_wide)      204    191    212    206    195    210    215    226    234     87    113
+//   128 (kv8_wide)      167    159    174    172    168    178    181    191    208    107    121
+//   256 (kv8_wide)      198    188    206    199    187    202    205    212    217     78     98
 int kv8_attention_rows(int64_t max_rows) {
   if (max_rows <= 64) return max_rows <= 16 ? 16 : static_cast<int>((max_rows + 15) / 16 * 16);
   return max_rows <= 128 ? 128 : 256;

@@ -15,6 +15,15 @@
 // Rotation. position * inv_freq in turns is an integer product modulo 2^64
 // (inv_freq / 2 pi as a 64-bit fraction), so the reduced angle loses nothing at
 // far positions and takes no 64-bit floating point.
+// What bounds it. Prompts (22,000 tokens, 8 KV heads of 128, fp16): 37.4 us, 4.0
+// TB/s read and written, 0.59 of a copy; instructions (60% of issue slots) and the
+// two barriers a head share the rest. 64 sequences x 9 tokens with queries: 10.1
+// us, launch and the lookup of each block's sequence; 9 tokens: 3.5 us, latency.
+//
+// Compaction. A warp owns one plane, keys or values and head of a sequence; entries move
+// through shared memory in path order, so that a destination is never read
+// after it was written. 32 planes x 16 sequences: 8.9 us, latency of lengths, path,
+// table, scales and entries, each read after the one before.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <string.h>
