@@ -36,7 +36,7 @@
 //
 // What bounds it. One row of 32 heads (decode, 64 sequences of 1500 to 6500
 // tokens, 8 KV heads of 128): memory, 548 MB in 91 us, 6.0 TB/s, 0.89 of a
-// copy. Nine rows (verification, the same cache): 143 us, 3.9 TB/s, where the
+// copy. Nine rows (verification, the same cache): 136 us, 4.1 TB/s, where the
 // softmax groups' instructions (62% of issue slots) and the barrier between the
 // tile's four maxima and its weights set the step of 2100 clocks a tile; the
 // products take 700 of them. One sequence of 517 tokens: 11 us, a chain of
@@ -50,6 +50,10 @@ namespace specv {
 namespace {
 
 // ---------------------------------------------------------- configuration --
+
+// Units of an item beside its tiles (see Runs). 64 sequences of 500 to 2000 tokens: 36 rows 73 us without, 66 with 2, 63
+// with 4; 16 rows 41, 39, 40.
+constexpr int kCost = 3;
 
 // D: head dimension. RW: rows of one softmax group of four warps, W: groups.
 template <int D_, int RW_, int W_, int TERMS_, int CTAS_>
@@ -175,14 +179,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   Runs runs;
   Start start;
   fence_before();
-  const bool work = uniform(find_run<N>(a, blockIdx.x, &runs, &start, sm.tmp)) != 0;
-  const int64_t my_tiles = work ? runs.begin(blockIdx.x + 1) - runs.begin(blockIdx.x) : 0;
+  const bool work = uniform(find_run<N, kCost>(a, blockIdx.x, &runs, &start, sm.tmp)) != 0;
+  const int64_t my_units = work ? runs.begin(blockIdx.x + 1) - runs.begin(blockIdx.x) : 0;
   __syncthreads();
   fence_after();
   const uint32_t tmem = uniform(sm.tmem);
 
   if (work && warp == kLoadWarp) {
-    copy_tiles<N, D, NS>(a, start, my_tiles, kmap, vmap, ring, sm, gave_up);
+    copy_tiles<N, kCost, D, NS>(a, start, my_units, kmap, vmap, ring, sm, gave_up);
   } else if (work && warp == kMmaWarp) {
     // ---- products: the warp waits together, one lane issues
     constexpr uint32_t kStride = 8 * D;
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   } else if (work && warp >= kQueryWarp && warp < kLoadWarp) {
     // ---- the items' queries, one item ahead: a thread owns a row
     const int own = tid - kQueryWarp * 32, quarter = warp - kQueryWarp;
-    Walk<N> it(a, start, my_tiles);
+    Walk<N, kCost> it(a, start, my_units);
     const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (a.qst * 2) | (a.qsh * 2)) & 15) == 0;
     int seg = 0;
     bool more;
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 1]), (seg >> 1) & 1, gave_up);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {  // the group's other warps may be a few barriers behind
-        for (int64_t k = 0; k < 2 * my_tiles + 2; ++k) named_arrive(3 + wg, 128);
+        for (int64_t k = 0; k < 2 * my_units + 2; ++k) named_arrive(3 + wg, 128);
         break;
       }
       const typename C::Item& it = sm.item[seg & 1];
@@ -646,11 +650,11 @@ cudaError_t launch_rows(const Kv8AttnArgs& a, int rows, const CUtensorMap& k, co
 // on a row of scores a lane is cheaper, two row tiles of 128 to an item when there are more than 128.
 // B = 64, contexts of 1500 to 6500 tokens, 8 KV heads of 128, bf16, us (16 sequences from 132 rows on):
 //   rows of a sequence    4     16     32     36     48     52     64     68    128    132    256
-//   as chosen            91     88    126    143    146    175    178    191    208     78     97
-//   32 rows an item     121    113    127
-//   64                  164    157    170    164    165    176    178
-//   128 (kv8_wide)      167    159    174    172    168    178    181    191    208    107    121
-//   256 (kv8_wide)      198    188    206    199    187    202    205    212    217     78     98
+//   as chosen            90     87    121    136    133    163    166    176    186     75     88
+//   32 rows an item     113    106    121
+//   64                  153    145    161    157    150    163    166
+//   128 (kv8_wide)      160    151    166    163    155    166    171    176    186     97    109
+//   256 (kv8_wide)      202    189    209    202    189    203    208    210    212     74     88
 int kv8_attention_rows(int64_t max_rows) {
   if (max_rows <= 64) return max_rows <= 16 ? 16 : static_cast<int>((max_rows + 15) / 16 * 16);
   return max_rows <= 128 ? 128 : 256;

@@ -66,31 +66,33 @@ __device__ __forceinline__ RowTile row_tile(const Kv8AttnArgs& a, int b, int rt)
   return r;
 }
 
-// Where a run of tiles begins.
+// Where a run begins: an item, and a unit of it.
 struct Start {
   int b, rt, h, t;
 };
 
-// Parts are equal runs of the tiles of all items, the first `more` of them one longer.
+// An item has COST units for its queries and results, then one for each tile. Parts are equal runs of the units of all
+// items, the first `more` of them one longer; an item begins in the part of its first tile.
 struct Runs {
-  int64_t all, each;  // tiles, tiles of a run
+  int64_t all, each;  // units, units of a run
   int parts, more;
   __device__ __forceinline__ int64_t begin(int part) const { return part * each + min(part, more); }
 };
 
-// All threads of the block: the runs, and where the part's first tile lies. False
-// where it has none. s_tmp: 64 words of shared memory.
-template <int N>
+// All threads of the block: the runs, and where the part's first unit lies. False
+// where it has no tile. s_tmp: 64 words of shared memory.
+template <int N, int COST>
 __device__ __forceinline__ bool find_run(const Kv8AttnArgs& a, int part, Runs* runs, Start* s, int* s_tmp) {
   const int nthr = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = nthr >> 5;
   const uint32_t cand = static_cast<uint32_t>(a.c.B) * static_cast<uint32_t>(a.row_tiles);  // below 2^31
-  // Sums over the candidates base .. base + nthr - 1, one a thread: up to this one's, and all.
-  auto scan = [&](uint32_t base, int* tiles, int64_t* upto, int64_t* sum) {
+  // Units of the candidates base .. base + nthr - 1, one a thread, their sums up to this one's, and all.
+  auto scan = [&](uint32_t base, int* units, int64_t* upto, int64_t* sum) {
     const uint32_t i = base + tid;
     int v = 0;
     if (i < cand) {
       const uint32_t b = i / static_cast<uint32_t>(a.row_tiles);
       v = row_tile<N>(a, static_cast<int>(b), static_cast<int>(i - b * a.row_tiles)).tiles;
+      if (v > 0) v += COST;
     }
     int64_t x = v;
 #pragma unroll 1
@@ -108,7 +110,7 @@ __device__ __forceinline__ bool find_run(const Kv8AttnArgs& a, int part, Runs* r
       total += at[w];
     }
     __syncthreads();
-    *tiles = v;
+    *units = v;
     *upto = x + before;
     *sum = total;
   };
@@ -159,27 +161,27 @@ __device__ __forceinline__ bool find_run(const Kv8AttnArgs& a, int part, Runs* r
   s->h = s_tmp[2];
   s->t = s_tmp[3];
   __syncthreads();
-  return found;
+  return found && runs->begin(part + 1) - runs->begin(part) > max(0, COST - s->t);
 }
 
 // Walks the items of a run: (r, h) with tiles [t0, t1).
-template <int N>
+template <int N, int COST>
 struct Walk {
   RowTile r;
   int h, t0, t1;
-  int64_t left;  // tiles of the run from t0 on
+  int64_t left;  // units of the run from t0 on
 
   __device__ __forceinline__ Walk(const Kv8AttnArgs& a, const Start& s, int64_t count) {
     r = row_tile<N>(a, s.b, s.rt);
     h = s.h;
-    t0 = s.t;
-    left = count;
+    t0 = max(0, s.t - COST);
+    left = count - max(0, COST - s.t);
     clip();
   }
   __device__ __forceinline__ void clip() { t1 = static_cast<int>(min(static_cast<int64_t>(r.tiles), t0 + left)); }
   // The next item, if any is left.
   __device__ __forceinline__ bool next(const Kv8AttnArgs& a) {
-    left -= t1 - t0;
+    left -= t1 - t0 + COST;
     if (left <= 0) return false;
     t0 = 0;
     if (++h == a.c.H) {
@@ -190,7 +192,7 @@ struct Walk {
           rt = 0;
           ++b;
         }
-        if (b >= a.c.B) {  // cannot be: the run's tiles were counted
+        if (b >= a.c.B) {  // cannot be: the run's units were counted
           left = 0;
           return false;
         }
@@ -237,11 +239,11 @@ __device__ __forceinline__ int4 cut_item(const Runs& runs, int part, const RowTi
 // The copying warp: the pages of each tile's keys, then of its values, into a
 // ring of NS slots, and of each page of the tile 2^ek (NaN for a page outside the
 // pool), ev and 2^-ev into sm.page.
-template <int N, int D, int NS, typename S>
+template <int N, int COST, int D, int NS, typename S>
 __device__ __forceinline__ void copy_tiles(const Kv8AttnArgs& a, const Start& start, int64_t count, const CUtensorMap& kmap,
                                            const CUtensorMap& vmap, uint8_t* ring, S& sm, volatile int* gave_up) {
   const int lane = threadIdx.x & 31;
-  Walk<N> it(a, start, count);
+  Walk<N, COST> it(a, start, count);
   const int bs = a.c.block, ppt = kTile / bs;
   uint32_t fill = 0, begun = 0;
   int i = 0;

@@ -24,13 +24,13 @@
 // Four more warps convert tiles and load queries, one copies, one issues.
 //
 // What bounds it. Prompts (three of 1500 to 4096 tokens behind up to 1000, 32
-// heads of 128, fp16): 592 us, 660 TFLOP/s, 0.35 of a library product's rate.
+// heads of 128, fp16): 381 us, 1025 TFLOP/s, 0.54 of a library product's rate.
 // Scores and weights of a pair of tiles hold the tensor pipe for 2112 clocks of a
-// step of about 3400 (50% over the whole kernel): a stream's weights must be
-// written before its product, and the product issued before its next scores,
-// and two streams do not cover that chain; tensor memory has no room for a
-// third. Trees of 61 nodes (16 sequences of 500 to 3500): 77 us, of which an item's
-// queries and results and the join of cut items are half.
+// step of about 3700: a stream's weights must be written before its product, and
+// the product issued before its next scores, and two streams do not cover that
+// chain; tensor memory has no room for a third. An item's queries and results
+// take 13,000 clocks more. Trees of 61 nodes (16 sequences of 500 to 3500): 69 us,
+// of which items' ends and the join of cut items are half.
 #include <string.h>
 
 #include <type_traits>
@@ -42,6 +42,9 @@ namespace specv {
 namespace {
 
 constexpr float kFar = 8.f;  // a tile moves the reference when it passes it by 2^8: weights stay below 2^8, far from 65504
+// Units of an item beside its tiles (see Runs): its queries and results take 13,000 clocks, a tile 3,700. Prompts whose
+// items have 1 to 40 tiles: 592 us without, 381 with 4, 386 with 8.
+constexpr int kCost = 4;
 constexpr int kItems = 4;    // items in flight between the query loads and the results
 
 template <int D_, bool PAIR_>
@@ -148,8 +151,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   Runs runs;
   Start start;
   fence_before();
-  const bool work = uniform(find_run<N>(a, blockIdx.x, &runs, &start, sm.tmp)) != 0;
-  const int64_t my_tiles = work ? runs.begin(blockIdx.x + 1) - runs.begin(blockIdx.x) : 0;
+  const bool work = uniform(find_run<N, kCost>(a, blockIdx.x, &runs, &start, sm.tmp)) != 0;
+  const int64_t my_units = work ? runs.begin(blockIdx.x + 1) - runs.begin(blockIdx.x) : 0;
   __syncthreads();
   fence_after();
   const uint32_t tmem = uniform(sm.tmem);
@@ -235,7 +238,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const int own = tid - kConvWarp * 32;
     const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (a.qst * 2) | (a.qsh * 2)) & 15) == 0;
     const uint32_t turn = static_cast<uint32_t>(own & 7) << 4;  // the swizzle of this row
-    Walk<N> it(a, start, my_tiles);
+    Walk<N, kCost> it(a, start, my_units);
     auto row_at = [&](const RowTile& r, int h, int row) {  // where a row's queries begin
       const uint32_t flat = static_cast<uint32_t>(r.rt * N + min(row, r.rows - 1)), tok = flat / static_cast<uint32_t>(a.group);
       return (r.first + static_cast<int64_t>(tok)) * a.qst + (h * a.group + static_cast<int>(flat - tok * a.group)) * a.qsh;
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 3]), (seg >> 2) & 1, gave_up);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {  // the other warps may be a few barriers behind
-        for (int64_t k = 0; k < my_tiles + 2; ++k) named_arrive(1, 256);
+        for (int64_t k = 0; k < my_units + 2; ++k) named_arrive(1, 256);
         break;
       }
       const typename C::Item& it = sm.item[seg & 3];
@@ -563,7 +566,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         };
         if constexpr (PAIR) {
           // Four lanes exchange 64 bytes of their rows, so that a store instruction meets eight rows, not 32. Where the
-          // streams add each other's sums (below) that costs more than it gives: 128 rows of 64 sequences, 216 and 206 us.
+          // streams add each other's sums (below) that costs more than it gives: 128 rows of 64 sequences, 216 against 206 us.
           const int row4 = row & ~3, part4 = lane & 3;
           QT* out4[4];
 #pragma unroll
@@ -660,7 +663,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   };
 
   // 512 threads of 128 registers; a softmax thread holds a row's 128 scores and takes from the others (176, 80 and 80:
-  // prompts 619 us, 591 with 168, 88 and 88)
+  // prompts 5% slower than with 168, 88 and 88)
   if (warp < kConvWarp) {
     more_registers<168>();
     if (work) softmax();
@@ -669,7 +672,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     if (work) convert_tiles();
   } else {
     fewer_registers<88>();
-    if (work && warp == kLoadWarp) copy_tiles<N, D, NS>(a, start, my_tiles, kmap, vmap, ring, sm, gave_up);
+    if (work && warp == kLoadWarp) copy_tiles<N, kCost, D, NS>(a, start, my_units, kmap, vmap, ring, sm, gave_up);
     if (work && warp == kMmaWarp) products();
   }
 

@@ -246,6 +246,16 @@ def test_attention_many_items(new, Hq, H, D, dt):
     check_attention(c, (randn(g, sum(c.new), Hq, D) * 2).to(dt))
 
 
+@pytest.mark.parametrize("new,Hq,H", [((1, 3), 2, 2), ((0, 9), 8, 1), ((3, 20), 16, 1), ((17, 34), 8, 1)])
+def test_attention_short_items(new, Hq, H):
+    """More thread blocks than tiles, and runs that end between an item's start and its first tile."""
+    rng = random.Random(6)
+    B = 90 if new[1] < 20 else 40
+    c = plain.Cache([rng.choice([0, rng.randint(0, 127), rng.randint(0, 300)]) for _ in range(B)],
+                    [rng.randint(*new) for _ in range(B)], H, 128, 32, seed=18).fill()
+    check_attention(c, randn(torch.Generator().manual_seed(16), sum(c.new), Hq, 128).to(BF))
+
+
 @pytest.mark.parametrize("dt", [BF, HF])
 def test_attention_sharp_and_flat_weights(dt):
     """One entry that takes nearly all of the weight, then hundreds that share it, and the reverse."""
