@@ -185,8 +185,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   fence_after();
   const uint32_t tmem = uniform(sm.tmem);
 
+  uint32_t begun = 0;
   if (work && warp == kLoadWarp) {
-    copy_tiles<N, kCost, D, NS>(a, start, my_units, kmap, vmap, ring, sm, gave_up);
+    begun = copy_tiles<N, kCost, D, NS>(a, start, my_units, kmap, vmap, ring, sm, gave_up);
   } else if (work && warp == kMmaWarp) {
     // ---- products: the warp waits together, one lane issues
     constexpr uint32_t kStride = 8 * D;
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         const uint32_t slot = uniform((2u * j) % NS), to = uniform(tmem + (j & 1) * N);
         bool ok = bar_wait(smem_addr(&sm.full[slot]), ((2u * j) / NS) & 1, gave_up);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
+        if (!ok) return false;
         fence_after();
         if (elect()) {
           const uint64_t kd = k_desc + (slot * C::kSlot >> 4), qd = q_desc + ((seg & 1) * C::kQ >> 4);
@@ -218,15 +219,19 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           commit(smem_addr(&sm.s_full[j & 1]));
         }
         __syncwarp();
+        return true;
       };
-      scores(i);
-      for (int t = t0; t < t1; ++t, ++i) {
-        if (t + 1 < t1) scores(i + 1);
+      ok = scores(i);
+      for (int t = t0; t < t1 && ok; ++t, ++i) {
+        if (t + 1 < t1 && !scores(i + 1)) {
+          ok = false;
+          break;
+        }
         const uint32_t slot = uniform((2u * i + 1) % NS), to = uniform(tmem + kO + (i & 1) * N);
         ok = bar_wait(smem_addr(&sm.full[slot]), ((2u * i + 1) / NS) & 1, gave_up) &&
              bar_wait(smem_addr(&sm.p_ready[i & 1]), (i >> 1) & 1, gave_up);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) continue;
+        if (!ok) break;
         fence_after();
         if (elect()) {
           const uint64_t vd = v_desc + (slot * C::kSlot >> 4), pd = p_desc + ((i & 1) * C::kP >> 4);
@@ -242,20 +247,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         }
         __syncwarp();
       }
+      if (!ok) break;
     }
-    if (*gave_up) {  // products that are still running write this block's tensor memory
-      if (elect()) commit(smem_addr(&sm.drain));
-      for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.drain), 0); ++k) {
-      }
-    }
-    __syncwarp();
   } else if (work && warp >= kQueryWarp && warp < kLoadWarp) {
     // ---- the items' queries, one item ahead: a thread owns a row
     const int own = tid - kQueryWarp * 32, quarter = warp - kQueryWarp;
     Walk<N, kCost> it(a, start, my_units);
     const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | (a.qst * 2) | (a.qsh * 2)) & 15) == 0;
     int seg = 0;
-    bool more;
+    bool more, ok = true;
     do {
       const RowTile r = it.r;
       const int r0 = r.rt * N;
@@ -307,8 +307,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       }
       const int eq = kv8_need(amax, -120, 120);
       const float down = a.negate ? -pow2i(-eq) : pow2i(-eq);
-      if (seg > 1) bar_wait(smem_addr(&sm.q_free[seg & 1]), ((seg >> 1) - 1) & 1, gave_up);
-      __syncwarp();
+      if (seg > 1) {
+        ok = bar_wait(smem_addr(&sm.q_free[seg & 1]), ((seg >> 1) - 1) & 1, gave_up);
+        ok = C::EW > 1 ? named_all(2, C::EW * 32, ok) : __all_sync(0xffffffffu, ok);
+        if (!ok) break;  // the item before the last may still be read
+      }
       uint8_t* q_to = q_smem + (seg & 1) * C::kQ;
 #pragma unroll 1
       for (int z0 = 0; z0 < kSteps; z0 += kBatch) {
@@ -342,10 +345,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       more = it.next(a);
       if (!more && own == 0) a.cut[blockIdx.x] = cut_item<N>(runs, blockIdx.x, last, h, t0, t1);
     } while (more);
-    if (seg > 1) bar_wait(smem_addr(&sm.q_free[seg & 1]), ((seg >> 1) - 1) & 1, gave_up);
-    if (own == 0) sm.item[seg & 1].t0 = sm.item[seg & 1].t1 = 0;  // no further item
-    __syncwarp();
-    if (lane == 0) bar_arrive(smem_addr(&sm.q_ready[seg & 1]));
+    if (ok && seg > 1) ok = bar_wait(smem_addr(&sm.q_free[seg & 1]), ((seg >> 1) - 1) & 1, gave_up);
+    if (__all_sync(0xffffffffu, ok)) {
+      if (own == 0) sm.item[seg & 1].t0 = sm.item[seg & 1].t1 = 0;  // no further item
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_addr(&sm.q_ready[seg & 1]));
+    }
   } else if (work && warp < kQueryWarp) {
     // ---- weights and sums: a thread owns a slot of the tile and a dimension of the result
     const int wg = uniform(warp >> 2), quarter = uniform(warp & 3);
@@ -356,12 +361,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     float l[RW], o[RW];
     static_assert(RW <= 16, "a lane holds a row's reference; sums over lanes");
     for (int i = 0, seg = 0;; ++seg) {  // tiles and items so far
-      bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 1]), (seg >> 1) & 1, gave_up);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {  // the group's other warps may be a few barriers behind
-        for (int64_t k = 0; k < 2 * my_units + 2; ++k) named_arrive(3 + wg, 128);
-        break;
-      }
+      const bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 1]), (seg >> 1) & 1, gave_up);
+      if (!named_all(3 + wg, 128, ok)) break;
       const typename C::Item& it = sm.item[seg & 1];
       const int t0 = uniform(it.t0), t1 = uniform(it.t1);
       if (t1 <= t0) break;
@@ -618,10 +619,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   fence_before();
   __syncthreads();
   fence_after();
+  if (sm.gave_up) drain<NS>(sm, warp == kLoadWarp, begun, warp == kMmaWarp);
   if (warp == kMmaWarp) tmem_free(tmem, C::kCols);
   if (tid == 0) {
     a.gave_up[blockIdx.x] = sm.gave_up;
-    if (!work) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (!work || sm.gave_up) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);  // what was begun is not to be joined
   }
   griddep_launch_dependents();
 }

@@ -238,15 +238,17 @@ __device__ __forceinline__ int4 cut_item(const Runs& runs, int part, const RowTi
 
 // The copying warp: the pages of each tile's keys, then of its values, into a
 // ring of NS slots, and of each page of the tile 2^ek (NaN for a page outside the
-// pool), ev and 2^-ev into sm.page.
+// pool), ev and 2^-ev into sm.page. Returns the number of ring slots that copies were begun into.
 template <int N, int COST, int D, int NS, typename S>
-__device__ __forceinline__ void copy_tiles(const Kv8AttnArgs& a, const Start& start, int64_t count, const CUtensorMap& kmap,
-                                           const CUtensorMap& vmap, uint8_t* ring, S& sm, volatile int* gave_up) {
+__device__ __forceinline__ uint32_t copy_tiles(const Kv8AttnArgs& a, const Start& start, int64_t count,
+                                               const CUtensorMap& kmap, const CUtensorMap& vmap, uint8_t* ring, S& sm,
+                                               volatile int* gave_up) {
   const int lane = threadIdx.x & 31;
   Walk<N, COST> it(a, start, count);
   const int bs = a.c.block, ppt = kTile / bs;
   uint32_t fill = 0, begun = 0;
   int i = 0;
+  bool ok = true;
   do {
     const int pages = (it.r.end + bs - 1) / bs;
     const int32_t* table = a.c.table + static_cast<int64_t>(it.r.b) * a.c.max_blocks;
@@ -265,7 +267,7 @@ __device__ __forceinline__ void copy_tiles(const Kv8AttnArgs& a, const Start& st
     int id = -1, id_next = page_id(it.t0 * ppt + lane);
     uint8_t ke = 127, ve = 127, ke_next = scale_at(a.c.ks, id_next), ve_next = scale_at(a.c.vs, id_next);
 #pragma unroll 1
-    for (int t = it.t0, g = 0; t < it.t1; ++t, g += ppt, ++i) {
+    for (int t = it.t0, g = 0; t < it.t1 && ok; ++t, g += ppt, ++i) {
       if ((g & 31) == 0) {
         id = id_next;
         ke = ke_next;
@@ -285,10 +287,9 @@ __device__ __forceinline__ void copy_tiles(const Kv8AttnArgs& a, const Start& st
 #pragma unroll 1
       for (int part = 0; part < 2; ++part, ++fill) {
         const uint32_t slot = fill % NS, bar = smem_addr(&sm.full[slot]);
-        bool ok = true;
         if (fill >= NS) ok = bar_wait(smem_addr(&sm.empty[slot]), (fill / NS - 1) & 1, gave_up);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) continue;  // a wait gave up: no copy is started any more
+        if (!ok) break;  // no copy is started any more
         begun = fill + 1;
         // the copies begin before the scales are there; the barrier's one arrival comes after both
         if (mine)
@@ -304,13 +305,27 @@ __device__ __forceinline__ void copy_tiles(const Kv8AttnArgs& a, const Start& st
         if (lane == 0) bar_expect(bar, bytes);
       }
     }
-  } while (it.next(a));
-  if (*gave_up)  // copies that are still in flight write this block's memory
+  } while (ok && it.next(a));
+  return begun;
+}
+
+// The end of a block in which a wait gave up, all threads: copies and products that are still in flight write this block's
+// memory, so the two warps that began them wait for them (with a limit).
+template <int NS, typename S>
+__device__ __forceinline__ void drain(S& sm, bool copied, uint32_t begun, bool issued) {
+  if (copied)
 #pragma unroll 1
     for (uint32_t f = begun > NS ? begun - NS : 0; f < begun; ++f)
 #pragma unroll 1
       for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.full[f % NS]), (f / NS) & 1); ++k) {
       }
+  if (issued) {
+    if (elect()) commit(smem_addr(&sm.drain));
+#pragma unroll 1
+    for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.drain), 0); ++k) {
+    }
+  }
+  __syncthreads();
 }
 
 // -------------------------------------------------------------------- join --

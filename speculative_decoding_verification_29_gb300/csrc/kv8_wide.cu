@@ -224,13 +224,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       count[0] += n[0];
       count[1] += n[1];
     }
-    if (*gave_up) {  // products that are still running write this block's tensor memory
-      if (elect()) commit(smem_addr(&sm.drain));
-#pragma unroll 1
-      for (int k = 0; k < (1 << 16) && !bar_try(smem_addr(&sm.drain), 0); ++k) {
-      }
-    }
-    __syncwarp();
   };
 
   auto convert_tiles = [&]() {
@@ -244,7 +237,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       return (r.first + static_cast<int64_t>(tok)) * a.qst + (h * a.group + static_cast<int>(flat - tok * a.group)) * a.qsh;
     };
     int seg = 0, i = 0;
-    bool more;
+    bool more, ok = true;
     do {
       const RowTile r = it.r;
       const int h = it.h, t0 = it.t0, t1 = it.t1, r0 = r.rt * N;
@@ -255,7 +248,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       static_assert(N % (kRows * kBatch) == 0, "whole batches");
       const int chunk = lane % kLanes, sub = own / kLanes;
       for (int row = own; row < N; row += 128) sm.qrow[row] = row_at(r, h, row);
-      named_sync(2, 128);
+      ok = named_all(2, 128, ok);
+      if (!ok) break;
       auto load = [&](int row, QT* e) {
         const QT* q = static_cast<const QT*>(a.q) + sm.qrow[row] + chunk * 8;
         if (vec) {
@@ -290,9 +284,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
       }
       __syncwarp();
-      if (seg > 0) bar_wait(smem_addr(&sm.q_free), (seg - 1) & 1, gave_up);
+      if (seg > 0) ok = bar_wait(smem_addr(&sm.q_free), (seg - 1) & 1, gave_up);
+      ok = __all_sync(0xffffffffu, ok);
 #pragma unroll 1
-      for (int row0 = 0; row0 < r.rows; row0 += kRows * kBatch) {
+      for (int row0 = 0; row0 < r.rows && ok; row0 += kRows * kBatch) {
         QT e[kBatch][8];
 #pragma unroll
         for (int z = 0; z < kBatch; ++z) load(row0 + z * kRows + sub, e[z]);
@@ -311,12 +306,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                                     (((chunk % 8) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
         }
       }
-      if (own == 0) {
+      if (own == 0 && ok) {
         sm.nan[seg & 3] = 0;
         sm.item[seg & 3] = {r.b, r.first, r.n, r.ctx, r.rows, r.end, r.part, r0, h, t0, t1, r.tiles};
       }
       fence_async_shared();
-      named_sync(2, 128);  // the flag is cleared before a tile of the item sets it
+      ok = named_all(2, 128, ok);  // and the flag is cleared before a tile of the item sets it
+      if (!ok) break;
       if (lane == 0) bar_arrive(smem_addr(&sm.q_ready[seg & 3]));
 
       more = it.next(a);
@@ -328,14 +324,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + d));
         }
 
-      for (int t = t0; t < t1; ++t, ++i) {
+      for (int t = t0; t < t1 && ok; ++t, ++i) {
         const int slot = t * kTile + own;
         const bool masked = t >= r.part;  // not every row sees every slot
 #pragma unroll 1
         for (int part = 0; part < 2; ++part) {
           const uint32_t j = 2u * i + part, from = j % NS, to = j % NF;
-          bar_wait(smem_addr(&sm.full[from]), (j / NS) & 1, gave_up);
-          if (j >= NF) bar_wait(smem_addr(&sm.empty16[to]), (j / NF - 1) & 1, gave_up);
+          ok = bar_wait(smem_addr(&sm.full[from]), (j / NS) & 1, gave_up);
+          if (j >= NF) ok = bar_wait(smem_addr(&sm.empty16[to]), (j / NF - 1) & 1, gave_up) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           const uint8_t* src = ring + from * C::kF8 + own * D;
           uint8_t* dst = f16 + to * C::kF16 + own * 128;
           // a row of D bytes is swizzled within 128 bytes, or within 64 by the row's second and third bit
@@ -388,10 +386,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       ++seg;
     } while (more);
-    bar_wait(smem_addr(&sm.q_free), (seg - 1) & 1, gave_up);
-    if (own == 0) sm.item[seg & 3].t0 = sm.item[seg & 3].t1 = 0;  // no further item
-    __syncwarp();
-    if (lane == 0) bar_arrive(smem_addr(&sm.q_ready[seg & 3]));
+    if (ok) ok = bar_wait(smem_addr(&sm.q_free), (seg - 1) & 1, gave_up);
+    if (__all_sync(0xffffffffu, ok)) {
+      if (own == 0) sm.item[seg & 3].t0 = sm.item[seg & 3].t1 = 0;  // no further item
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_addr(&sm.q_ready[seg & 3]));
+    }
   };
 
   auto softmax = [&]() {
@@ -403,15 +403,18 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const int page_shift = 31 - __clz(a.c.block) - 4;  // sixteen slots g are in page g >> page_shift
     int base = 0, count[2] = {0, 0};
     for (int seg = 0;; ++seg) {
-      bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 3]), (seg >> 2) & 1, gave_up);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {  // the other warps may be a few barriers behind
-        for (int64_t k = 0; k < my_units + 2; ++k) named_arrive(1, 256);
+      const bool ok = bar_wait(smem_addr(&sm.q_ready[seg & 3]), (seg >> 2) & 1, gave_up);
+      // The eight warps meet once an item (below), and leave together: whoever gets no item says so there.
+      if (!__all_sync(0xffffffffu, ok)) {
+        named_all(1, 256, false);
         break;
       }
       const typename C::Item& it = sm.item[seg & 3];
       const int t0 = uniform(it.t0), nt = uniform(it.t1) - t0, rows = uniform(it.rows);
-      if (nt <= 0) break;
+      if (nt <= 0) {
+        named_all(1, 256, true);
+        break;
+      }
       const int n[2] = {steps(nt, rows, 0), steps(nt, rows, 1)};
       const int steps_here = b == 0 ? n[0] : n[1], count_here = b == 0 ? count[0] : count[1];
       const int ctx = uniform(it.ctx);
@@ -528,8 +531,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         sm.ref[seg & 1][b][own] = ref;
         sm.sum[seg & 1][b][own] = l;
       }
+      // both streams' products are done; and a stream without steps does not run ahead
       fence_before();
-      named_sync(1, 256);  // both streams' products are done; and a stream without steps does not run ahead
+      if (!named_all(1, 256, true)) break;
       fence_after();
       float a0 = 1.f, a1 = 0.f;  // factors of the own and the other stream's sums
       if (!PAIR) {
@@ -664,6 +668,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 
   // 512 threads of 128 registers; a softmax thread holds a row's 128 scores and takes from the others (176, 80 and 80:
   // prompts 5% slower than with 168, 88 and 88)
+  uint32_t begun = 0;
   if (warp < kConvWarp) {
     more_registers<168>();
     if (work) softmax();
@@ -672,17 +677,18 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     if (work) convert_tiles();
   } else {
     fewer_registers<88>();
-    if (work && warp == kLoadWarp) copy_tiles<N, kCost, D, NS>(a, start, my_units, kmap, vmap, ring, sm, gave_up);
+    if (work && warp == kLoadWarp) begun = copy_tiles<N, kCost, D, NS>(a, start, my_units, kmap, vmap, ring, sm, gave_up);
     if (work && warp == kMmaWarp) products();
   }
 
   fence_before();
   __syncthreads();
   fence_after();
+  if (sm.gave_up) drain<NS>(sm, warp == kLoadWarp, begun, warp == kMmaWarp);
   if (warp == kMmaWarp) tmem_free(tmem, 512);
   if (tid == 0) {
     a.gave_up[blockIdx.x] = sm.gave_up;
-    if (!work) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (!work || sm.gave_up) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);  // what was begun is not to be joined
   }
   griddep_launch_dependents();
 }

@@ -21,7 +21,26 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// A wait gives up after two seconds. A build with a limit of less than a try's 20 us looks without suspending the thread, so
+// that waits run out at every place of a kernel.
+#ifndef SPECV_WAIT_NS
+#define SPECV_WAIT_NS 2000000000
+#endif
+constexpr uint64_t kWaitNs = SPECV_WAIT_NS;
+constexpr bool kLook = kWaitNs < 20000;
+__device__ __forceinline__ bool bar_look(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  if (kLook) return bar_look(bar, parity);
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -34,6 +53,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 }
 // The same, the thread suspended until the phase ends or some 20 us have passed.
 __device__ __forceinline__ bool bar_try_long(uint32_t bar, uint32_t parity) {
+  if (kLook) return bar_look(bar, parity);
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -49,11 +69,12 @@ __device__ __forceinline__ uint64_t now_ns() {
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
   return t;
 }
-constexpr uint64_t kWaitNs = 2000000000ull;  // a wait gives up after two seconds
 
 // Waits for the barrier's phase; false, with *gave_up set, when the limit ran
-// out. Once a wait of the block has given up no other waits: every role then
-// runs through its loop without touching the tensor core or starting copies.
+// out. Once a wait of the block has given up no other waits long. What follows
+// a failed wait: whoever copies, issues products or hands items over stops at
+// once, so that nothing that another warp may still read is written again;
+// warps that meet at named barriers leave a loop only together (named_all).
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
   if (bar_try(bar, parity)) return true;
   uint64_t t0 = 0;
@@ -83,8 +104,19 @@ __device__ __forceinline__ void fewer_registers() {
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-__device__ __forceinline__ void named_arrive(int id, int threads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+// A barrier that also says whether `ok` holds for each of its threads: they take the same branch on it. (A wait's
+// outcome alone may differ between warps: one gives up, and the phase ends before the next one looks.)
+__device__ __forceinline__ bool named_all(int id, int threads, bool ok) {
+  uint32_t all;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(ok)), "r"(id), "r"(threads)
+      : "memory");
+  return all != 0;
 }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void fence_bar_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
