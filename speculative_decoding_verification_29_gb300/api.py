@@ -412,19 +412,29 @@ def _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, plane
                          stride[-4], stride[-3], stride[-2]), dev
 
 
-def _int32(t, name, dev):
+def _int32(t, name, dev, n=0):
     if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor on {dev}")
+    if t.numel() < n:
+        raise ValueError(f"{name} must have {n} entries, not {t.numel()}")
 
 
-def _kv8_rows(t, name, D, dev):
-    """The token and head strides of a packed [T, heads, head_dim] activation."""
+def _kv8_rows(t, name, D, dev, written=False):
+    """The token and head strides of a packed [T, heads, head_dim] activation; one that is written has no rows that share
+    memory."""
     stride = t.stride()
     if t.device != dev or len(stride) != 3 or t.shape[2] != D or stride[2] != 1:
         raise ValueError(f"{name} must be a [tokens, heads, {D}] tensor on {dev}, head_dim contiguous")
     if t.dtype not in _KV8_DTYPES:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if written and (stride[0] < D and t.shape[0] > 1 or stride[1] < D and t.shape[1] > 1):
+        raise ValueError(f"{name} is written: its rows must not overlap")
     return stride[0], stride[1]
+
+
+def _kv8_workspace(t, dev):
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
 
 
 def _used_on(stream, *tensors):
@@ -475,7 +485,7 @@ def spec_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache
         qst, qsh = _kv8_rows(q, "q", D, dev)
         if q_out is None:
             q_out = made = torch.empty_like(q)
-        ost, osh = _kv8_rows(q_out, "q_out", D, dev)
+        ost, osh = _kv8_rows(q_out, "q_out", D, dev, True)
         if q.dtype != k.dtype or q_out.dtype != q.dtype or q.shape[0] != T or q_out.shape != q.shape:
             raise ValueError("q and q_out must be [tokens, q_heads, head_dim] of the keys' type")
         hq = q.shape[1]
@@ -491,6 +501,8 @@ def spec_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache
         out = dict(row_status=torch.empty(cache.B, dtype=torch.int32, device=dev))
         if stream is not None:
             _used_on(stream, out["row_status"])
+    else:
+        _int32(out["row_status"], "row_status", dev, cache.B)
     if made is not None and stream is not None:
         _used_on(stream, made)
     if q is not None:
@@ -525,7 +537,8 @@ def spec_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cache
     tree_mask [B, max_tokens, max_tokens] uint8 (as written by spec_merge_trees)
     those with tree_mask[b, i, j] != 0. max_tokens: no sequence has more step
     tokens. sm_scale: head_dim ** -0.5 when None. Returns out (like q) and
-    row_status [B]."""
+    row_status [B]; a caller's own out["out"] may have any token and head
+    strides, but must not be q."""
     lib = _lib.load()
     cache, dev = _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len)
     qst, qsh = _kv8_rows(q, "q", cache.head_dim, dev)
@@ -544,10 +557,14 @@ def spec_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cache
         out = dict(out=torch.empty_like(q), row_status=torch.empty(cache.B, dtype=torch.int32, device=dev))
         if stream is not None:
             _used_on(stream, *out.values())
+    else:
+        _int32(out["row_status"], "row_status", dev, cache.B)
     o = out["out"]
-    ost, osh = _kv8_rows(o, "out", cache.head_dim, dev)
+    ost, osh = _kv8_rows(o, "out", cache.head_dim, dev, True)
     if o.shape != q.shape or o.dtype != q.dtype:
         raise ValueError("out must have q's shape and type")
+    if T and o.data_ptr() == q.data_ptr():
+        raise ValueError("out must not be q: queries are read again after the first results were written")
     if workspace is None:
         nbytes = lib.spec_kv8_workspace_bytes(ctypes.byref(cache), hq, max_tokens, code)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
@@ -555,6 +572,8 @@ def spec_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cache
             workspace = alloc_workspace(nbytes, dev)
         if stream is not None:
             _used_on(stream, workspace)
+    else:
+        _kv8_workspace(workspace, dev)
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(cache.head_dim)
     check("spec_kv8_attention", lib.spec_kv8_attention(
@@ -595,6 +614,9 @@ def spec_kv8_compact(k_cache, v_cache, k_scale, v_scale, block_table, cache_len,
                    row_status=torch.empty(cache.B, dtype=torch.int32, device=dev))
         if stream is not None:
             _used_on(stream, *out.values())
+    else:
+        _int32(out["new_len"], "new_len", dev, cache.B)
+        _int32(out["row_status"], "row_status", dev, cache.B)
     check("spec_kv8_compact", lib.spec_kv8_compact(ctypes.byref(cache), planes, sp, ssp, _ptr(path), D,
                                                    accept_len.data_ptr(), out["new_len"].data_ptr(),
                                                    out["row_status"].data_ptr(), _stream(stream)))
