@@ -445,7 +445,9 @@ typedef struct {
  *       contiguous). Rows on 16-byte boundaries are read 16 bytes at a time.
  *   cu_tokens     device [B + 1] int32: sequence b has tokens cu_tokens[b] to
  *       cu_tokens[b + 1] - 1 (none is allowed); its i-th goes to position
- *       cache_len[b] + i. cache_len itself is not changed.
+ *       cache_len[b] + i. cache_len itself is not changed. Where cu_tokens falls,
+ *       sequences may share tokens: every one whose own range is sound gets all of
+ *       its tokens, and a shared token's query is turned for one of them.
  *   positions     device [T] int32 or NULL: the position that token t is
  *       rotated by (a tree node's: cache_len + its depth); NULL: the position
  *       it is stored at.
@@ -485,7 +487,7 @@ int spec_kv8_append(const spec_kv8_cache* cache, const void* keys, int64_t k_str
  * 0. Entries that a row does not see do not reach it, NaN or not.
  *   queries, out  device, dtype SPEC_BF16 or SPEC_F16: token t, head a at element
  *       t * stride_token + a * stride_head (any strides; head_dim contiguous)
- *   cu_tokens     as in spec_kv8_append
+ *   cu_tokens     as in spec_kv8_append; a token of several sequences gets one's result
  *   max_tokens    no sequence has more step tokens than this
  *   tree_mask     device [B][max_tokens][max_tokens] uint8 or NULL (as written by
  *       spec_merge_trees with N = max_tokens)
