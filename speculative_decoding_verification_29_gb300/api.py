@@ -12,6 +12,8 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
+import inspect
 import math
 from typing import Dict, Optional
 
@@ -52,6 +54,32 @@ def _stream(stream) -> int:
             return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on_stream(fn):
+    """`stream=` of a call that makes tensors of its own: they are made on that stream, where its kernels use them. From the
+    current stream's memory they could be a block that work queued there still reads or writes. The outputs are the caller's
+    on the current stream, so they are kept until that has passed the point at which they are dropped."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = kw.get("stream") if len(args) <= at else args[at]
+        if stream is None:
+            return fn(*args, **kw)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        current = torch.cuda.current_stream()
+        if stream.cuda_stream == current.cuda_stream:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            out = fn(*args, **kw)
+        for t in out.values():
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(current)
+        return out
+
+    return call
 
 
 def workspace_bytes(B: int, K: int, V: int, dtype) -> int:
@@ -437,15 +465,7 @@ def _kv8_workspace(t, dev):
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
 
 
-def _used_on(stream, *tensors):
-    """Tensors allocated here on the current stream but used on `stream`."""
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
-
-
+@_on_stream
 def spec_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, cu_tokens, *, inv_freq=None,
                     interleaved: bool = False, positions=None, q=None, q_out=None,
                     out: Optional[Dict[str, torch.Tensor]] = None, stream=None) -> Dict[str, torch.Tensor]:
@@ -480,11 +500,10 @@ def spec_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache
         if positions.numel() != T:
             raise ValueError("positions must have one entry per token")
     qst = qsh = ost = osh = hq = 0
-    made = None
     if q is not None:
         qst, qsh = _kv8_rows(q, "q", D, dev)
         if q_out is None:
-            q_out = made = torch.empty_like(q)
+            q_out = torch.empty_like(q)
         ost, osh = _kv8_rows(q_out, "q_out", D, dev, True)
         if q.dtype != k.dtype or q_out.dtype != q.dtype or q.shape[0] != T or q_out.shape != q.shape:
             raise ValueError("q and q_out must be [tokens, q_heads, head_dim] of the keys' type")
@@ -499,12 +518,8 @@ def spec_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache
             rot, freq = 2 * len(held), held.buffer_info()[0]
     if out is None:
         out = dict(row_status=torch.empty(cache.B, dtype=torch.int32, device=dev))
-        if stream is not None:
-            _used_on(stream, out["row_status"])
     else:
         _int32(out["row_status"], "row_status", dev, cache.B)
-    if made is not None and stream is not None:
-        _used_on(stream, made)
     if q is not None:
         out["q_out"] = q_out
     check("spec_kv8_append", lib.spec_kv8_append(
@@ -523,6 +538,7 @@ def kv8_workspace_bytes(k_cache, block_table, q_heads: int, max_tokens: int, dty
     return int(_lib.load().spec_kv8_workspace_bytes(ctypes.byref(cache), q_heads, max_tokens, code))
 
 
+@_on_stream
 def spec_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, cu_tokens, *, max_tokens: int,
                        sm_scale: Optional[float] = None, tree_mask=None,
                        out: Optional[Dict[str, torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None,
@@ -555,8 +571,6 @@ def spec_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cache
     code = _KV8_DTYPES[q.dtype]
     if out is None:
         out = dict(out=torch.empty_like(q), row_status=torch.empty(cache.B, dtype=torch.int32, device=dev))
-        if stream is not None:
-            _used_on(stream, *out.values())
     else:
         _int32(out["row_status"], "row_status", dev, cache.B)
     o = out["out"]
@@ -570,8 +584,6 @@ def spec_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cache
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         if workspace.data_ptr() % 256:
             workspace = alloc_workspace(nbytes, dev)
-        if stream is not None:
-            _used_on(stream, workspace)
     else:
         _kv8_workspace(workspace, dev)
     if sm_scale is None:
@@ -583,6 +595,7 @@ def spec_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cache
     return out
 
 
+@_on_stream
 def spec_kv8_compact(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, accept_len, path=None,
                      out: Optional[Dict[str, torch.Tensor]] = None, stream=None) -> Dict[str, torch.Tensor]:
     """Compaction of an 8-bit paged cache along the accepted path of a tree
@@ -612,8 +625,6 @@ def spec_kv8_compact(k_cache, v_cache, k_scale, v_scale, block_table, cache_len,
     if out is None:
         out = dict(new_len=torch.empty(cache.B, dtype=torch.int32, device=dev),
                    row_status=torch.empty(cache.B, dtype=torch.int32, device=dev))
-        if stream is not None:
-            _used_on(stream, *out.values())
     else:
         _int32(out["new_len"], "new_len", dev, cache.B)
         _int32(out["row_status"], "row_status", dev, cache.B)
