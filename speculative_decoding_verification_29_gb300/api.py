@@ -102,6 +102,7 @@ def alloc_workspace(nbytes: int, device) -> torch.Tensor:
     return buf[off: off + nbytes]
 
 
+@_on_stream
 def spec_verify_chain(target_logits, draft_logits, draft_tokens, u_accept, u_resample, temperature: float,
                       out: Optional[Dict[str, torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None,
                       device="cuda", stream=None, stats: bool = True) -> Dict[str, torch.Tensor]:
@@ -187,7 +188,9 @@ def prepare_verify_chain(target_logits, draft_logits, draft_tokens, u_accept, u_
     fp32 uniforms): the call keeps their addresses, so a tensor that would
     need a conversion is refused (ValueError) rather than silently replaced
     by a copy. The tensors must stay alive and keep their shapes; their
-    contents may change between calls."""
+    contents may change between calls. Outputs and workspace are made here, on
+    the current stream: a stream that the function is given later has to be
+    ordered behind it."""
     B, K, V = _prepared_inputs(target_logits, draft_logits, draft_tokens, u_accept, u_resample)
     lib = _lib.load()
     dev = target_logits.device
@@ -235,6 +238,7 @@ def _host(t: torch.Tensor, name: str, dtype=None) -> torch.Tensor:
     return t
 
 
+@_on_stream
 def spec_verify_chain_host(target_logits, draft_logits, draft_tokens, u_accept, u_resample, temperature: float,
                            out: Optional[Dict[str, torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None,
                            device="cuda", stream=None, synchronize: bool = True) -> Dict[str, torch.Tensor]:
@@ -306,6 +310,7 @@ def spec_chain_sample(target_logits, draft_logits, draft_tokens, u_accept, u_res
            workspace, stream)
 
 
+@_on_stream
 def spec_verify_chain_greedy(target_logits, draft_tokens, out: Optional[Dict[str, torch.Tensor]] = None,
                              workspace: Optional[torch.Tensor] = None, device="cuda",
                              stream=None) -> Dict[str, torch.Tensor]:
@@ -332,6 +337,7 @@ def spec_verify_chain_greedy(target_logits, draft_tokens, out: Optional[Dict[str
     return out
 
 
+@_on_stream
 def spec_verify_tree_greedy(node_logits, node_tokens, retrieve_indices, n1: int, tree_mask=None,
                             out: Optional[Dict[str, torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None,
                             device="cuda", stream=None) -> Dict[str, torch.Tensor]:
@@ -364,6 +370,7 @@ def spec_verify_tree_greedy(node_logits, node_tokens, retrieve_indices, n1: int,
     return out
 
 
+@_on_stream
 def spec_tree_confidence(node_conf, n1: int, out: Optional[Dict[str, torch.Tensor]] = None, device="cuda",
                          stream=None) -> Dict[str, torch.Tensor]:
     """Confidence routing: scores [B, 2] and choice [B] (1 or 2)."""
@@ -379,6 +386,7 @@ def spec_tree_confidence(node_conf, n1: int, out: Optional[Dict[str, torch.Tenso
     return out
 
 
+@_on_stream
 def spec_kv_compact(kv: torch.Tensor, base_pos, accept_len, path=None, out: Optional[Dict[str, torch.Tensor]] = None,
                     stream=None) -> Dict[str, torch.Tensor]:
     """KV-cache compaction after verification, in place on ``kv``.
@@ -634,6 +642,7 @@ def spec_kv8_compact(k_cache, v_cache, k_scale, v_scale, block_table, cache_len,
     return out
 
 
+@_on_stream
 def spec_tree_entropy(draft_logits, n1: int, temperature: float = 1.0, out: Optional[Dict[str, torch.Tensor]] = None,
                       workspace: Optional[torch.Tensor] = None, device="cuda", stream=None,
                       node_entropy: bool = True) -> Dict[str, torch.Tensor]:
@@ -660,6 +669,7 @@ def spec_tree_entropy(draft_logits, n1: int, temperature: float = 1.0, out: Opti
     return out
 
 
+@_on_stream
 def spec_tree_expand(draft_logits, logc, M: int, temperature: float = 1.0,
                      out: Optional[Dict[str, torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None,
                      device="cuda", stream=None) -> Dict[str, torch.Tensor]:
@@ -692,6 +702,7 @@ def spec_tree_expand(draft_logits, logc, M: int, temperature: float = 1.0,
     return out
 
 
+@_on_stream
 def spec_merge_trees(tokens1, mask1, retrieve1, pos1, tokens2, mask2, retrieve2, pos2, device="cuda",
                      stream=None) -> Dict[str, torch.Tensor]:
     """Merge B pairs of drafter trees under one shared root on the device.
@@ -720,6 +731,7 @@ def spec_merge_trees(tokens1, mask1, retrieve1, pos1, tokens2, mask2, retrieve2,
     return out
 
 
+@_on_stream
 def spec_verify_chain_warped(target_logits, draft_logits, draft_tokens, u_accept, u_resample, temperature: float,
                              top_k: int = 0, top_p: float = 1.0, out: Optional[Dict[str, torch.Tensor]] = None,
                              workspace: Optional[torch.Tensor] = None, device="cuda",

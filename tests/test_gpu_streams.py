@@ -4,6 +4,7 @@ stream, and stays the caller's for as long as the current stream reads it."""
 import pytest
 import torch
 
+import gen
 import kv8_plain as plain
 from gpu_helpers import need_gpu
 
@@ -34,6 +35,10 @@ def kv8_calls():
             lambda **kw: sv().spec_kv8_compact(*args, acc, **kw)]
 
 
+def bits(t):
+    return t.contiguous().view(torch.uint8)
+
+
 def check_call(call):
     want = {k: v.clone() for k, v in call().items() if isinstance(v, torch.Tensor)}
     sizes = [v.numel() * v.element_size() for v in want.values()]
@@ -50,7 +55,7 @@ def check_call(call):
         got = call(stream=s)
         torch.cuda.synchronize()
         for k, v in want.items():
-            assert torch.equal(got[k], v), k
+            assert torch.equal(bits(got[k]), bits(v)), k
         # outputs dropped while the current stream has still to read them
         torch.cuda._sleep(WAIT)
         kept = {k: got[k].clone() for k in want}
@@ -59,9 +64,44 @@ def check_call(call):
             junk = [torch.full((n,), 0x55, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
         torch.cuda.synchronize()
         for k, v in want.items():
-            assert torch.equal(kept[k], v), k
+            assert torch.equal(bits(kept[k]), bits(v)), k
 
 
 @pytest.mark.parametrize("which", range(3))
 def test_kv8_calls(which):
     check_call(kv8_calls()[which])
+
+
+def verification_calls():
+    def dev(*t):
+        return [x.cuda() for x in t]
+
+    c, c0 = gen.chain_tiny(0), gen.chain_tiny(1, T=0.0)
+    chain = dev(c.Lp, c.Lq, c.x.long(), c.ua.double(), c.ur)  # some inputs are converted on the way
+    tb = gen.tree_batch(4, n_per_tree=6, V=500, dtype=torch.float32, seed=0, max_depth=4)
+    tree = dev(tb.Lt, tb.tok.long(), tb.R)
+    conf, draft = tb.conf.cuda(), gen.tree_draft_logits(tb, 0).cuda()
+    Ld, logc = dev(*gen.expand_frontier(2, 3, 5000, torch.bfloat16, seed=1))
+    kv = torch.randn(2, 3, 20, 64, generator=torch.Generator().manual_seed(3)).cuda()
+    base, acc = dev(torch.tensor([0, 5, 9]), torch.tensor([3, -1, 0]))
+    R, mask, pos = gen.tree_from_parents([-1, 0, 0, 1])
+    one = [torch.tensor([[7, 8, 9, 10]], dtype=torch.int32), torch.as_tensor(mask)[None], torch.as_tensor(R)[None],
+           torch.as_tensor(pos)[None]]
+    two = [torch.tensor([[7, 8, 11, 12]], dtype=torch.int32), *one[1:]]
+    merge = dev(*one, *two)
+    return dict(
+        chain=lambda **kw: sv().spec_verify_chain(*chain, c.T, **kw),
+        greedy=lambda **kw: sv().spec_verify_chain_greedy(c0.Lp.cuda(), c0.x.long().cuda(), **kw),
+        warped=lambda **kw: sv().spec_verify_chain_warped(*chain, c.T, top_k=8, top_p=0.9, **kw),
+        tree=lambda **kw: sv().spec_verify_tree_greedy(*tree, tb.n1, **kw),
+        confidence=lambda **kw: sv().spec_tree_confidence(conf, tb.n1, **kw),
+        entropy=lambda **kw: sv().spec_tree_entropy(draft, tb.n1, 1.0, **kw),
+        expand=lambda **kw: sv().spec_tree_expand(Ld, logc, 5, **kw),
+        merge=lambda **kw: sv().spec_merge_trees(*merge, **kw),
+        compact=lambda **kw: sv().spec_kv_compact(kv, base, acc, **kw),
+    )
+
+
+@pytest.mark.parametrize("name", ["chain", "greedy", "warped", "tree", "confidence", "entropy", "expand", "merge", "compact"])
+def test_verification_calls(name):
+    check_call(verification_calls()[name])
