@@ -494,10 +494,11 @@ int spec_kv8_append(const spec_kv8_cache* cache, const void* keys, int64_t k_str
  *   sm_scale      finite
  *   q_heads       a multiple of kv_heads, at most 64 * kv_heads
  * Scores, maxima, sums and the accumulated output are fp32. Up to 64 rows
- * (max_tokens * q_heads / kv_heads), queries and softmax weights enter the
- * products as two (bf16) or three (fp16) e4m3 terms and the cache's codes as they
- * are; above, queries, weights and codes enter as fp16 (codes exactly, queries over
- * a power of two of their row). A product adds 128 positions in fp32.
+ * (max_tokens * q_heads / kv_heads), softmax weights enter the products as two (bf16)
+ * or three (fp16) e4m3 terms, the cache's codes as they are, and queries as three e5m2
+ * terms over a power of two of the KV head's rows: exactly down to 2^-31 of their
+ * largest element. Above, queries, weights and codes enter as fp16 (codes exactly,
+ * queries over a power of two of their row). A product adds 128 positions in fp32.
  * Outputs: out, which must not overlap queries; row_status [B] int32:
  * SPEC_ROW_CACHE where the sequence's lengths are invalid (cu_tokens not rising
  * or outside [0, T], more than max_tokens, cache_len negative or beyond the

@@ -9,11 +9,19 @@
 // largest y rounded up to a whole number; tiles add up with factors 2^(E - ref),
 // exact powers of two, so the accumulators are rescaled only when a tile passes
 // the row's reference by 2^60.
-// Operands. The products are e4m3 x e4m3 -> fp32. A bf16 query element is the sum
-// of two e4m3 terms (4 bits and a sign each), an fp16 one of three, exactly down
-// to 2^-17 of the item's largest; a weight is split likewise, its relative error
-// about 2^-9 rms for bf16 results and 2^-12 for fp16. Because E is the tile's own
+// Operands. The products are e4m3 x e5m2 -> fp32 (scores) and e4m3 x e4m3 -> fp32.
+// A query element over a power of two is the sum of three e5m2 terms (3 bits and a
+// sign each: 8 bits of bf16 and 11 of fp16 leave nothing). The power is one for the
+// rows of an item, and e5m2's wide range keeps them apart: elements are exact down
+// to 2^-31 of the item's largest, for a row 2^14 times smaller than another still
+// 2^-17 of its own. A weight is the sum of two e4m3 terms for bf16 results and three
+// for fp16, its relative error about 2^-9 rms and 2^-12. Because E is the tile's own
 // largest, the codes' floor costs no more than 2^-17 of a weight in the same tile.
+// 64 sequences of 9 tokens, bf16, 140 us. With e4m3 terms, of which bf16 takes two
+// (135), a row 2^10 times smaller than another lost 0.6% of its result (fp16: 1%);
+// a power of two for each row, as a factor of its scores, costs 12 instructions a
+// tile (144); two terms and a third for rows far apart only (138), but 32 and 64
+// rows are slower by 2%.
 //
 // Orientation. Slots are the 128 rows of both products' first operand: scores
 // are K (128 slots x D) times Q^T (D x N rows), results are V^T (D x 128 slots)
@@ -64,7 +72,8 @@ struct Cfg {
   static constexpr int kThreads = W * 128 + EW * 32 + 64;  // softmax, queries, copies and products
   static constexpr int kCtas = CTAS_;                  // resident on an SM
   static constexpr int kSlot = kTile * D;
-  static constexpr int kQ = TERMS * N * D;  // one item's queries; two are kept
+  static constexpr int kQTerms = 3;  // e5m2 terms of a query element
+  static constexpr int kQ = kQTerms * N * D;  // one item's queries; two are kept
   static constexpr int kTerm = N == 48 ? 64 : N;  // a term's columns in a row of weights: none crosses a panel of 128
   static constexpr int kPanels = (TERMS * kTerm + 127) / 128, kP = kPanels * kTile * 128;  // one tile's weights; two are kept
   static_assert(128 % kTerm == 0, "terms within panels");
@@ -90,8 +99,8 @@ struct Cfg {
     alignas(8) uint64_t full[12], empty[12], s_full[2], p_ready[2], o_full[2], q_ready[2], q_free[2], drain;
     uint32_t tmem;
     int gave_up;
-    alignas(8) int tmp[64];
   };
+  static_assert(sizeof(Small::smax) >= 64 * sizeof(int), "the search for the run uses these words before the roles begin");
   static constexpr int kBudget = kCtas == 2 ? 115712 : 231424;
   static constexpr int kFixed = 1024 + 2 * kQ + 2 * kP + static_cast<int>(sizeof(Small));
   static constexpr int kFit = (kBudget - kFixed) / kSlot;
@@ -102,19 +111,25 @@ struct Cfg {
   static_assert(kMetaRing >= (kRing + 1) / 2 + 1, "meta entries live as long as a tile's slots");
 };
 
-// The e4m3 terms of eight query elements (already divided by the item's scale).
+// The e5m2 terms of eight query elements (already divided by the item's scale). An infinite one gives NaN, as its scores
+// would in any sum.
 template <int TERMS>
 __device__ __forceinline__ void split8(float* x, uint2* out) {
 #pragma unroll
-  for (int t = 0; t < TERMS; ++t) {
-    out[t] = make_uint2(kv8_codes4(x, 1.f), kv8_codes4(x + 4, 1.f));
-    if (t + 1 < TERMS) {
-      float y[8];
-      kv8_values4(out[t].x, y);
-      kv8_values4(out[t].y, y + 4);
+  for (int i = 0; i < 8; ++i) x[i] = fabsf(x[i]) < -kNegInf ? x[i] : __int_as_float(0x7fffffff);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] -= y[i];
+  for (int t = 0; t < TERMS; ++t) {
+    uint16_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(c[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+      uint32_t back;
+      asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(back) : "h"(c[i]));
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&back));
+      x[2 * i] -= y.x;
+      x[2 * i + 1] -= y.y;
     }
+    out[t] = make_uint2(c[0] | static_cast<uint32_t>(c[1]) << 16, c[2] | static_cast<uint32_t>(c[3]) << 16);
   }
 }
 
@@ -179,7 +194,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   Runs runs;
   Start start;
   fence_before();
-  const bool work = uniform(find_run<N, kCost>(a, blockIdx.x, &runs, &start, sm.tmp)) != 0;
+  const bool work = uniform(find_run<N, kCost>(a, blockIdx.x, &runs, &start, reinterpret_cast<int*>(sm.smax))) != 0;
   const int64_t my_units = work ? runs.begin(blockIdx.x + 1) - runs.begin(blockIdx.x) : 0;
   __syncthreads();
   fence_after();
@@ -202,7 +217,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       const int t0 = uniform(sm.item[seg & 1].t0), t1 = uniform(sm.item[seg & 1].t1);
       if (!ok || t1 <= t0) break;
       fence_after();
-      constexpr uint32_t id_s = instr_desc(kTile, N, false), id_o = instr_desc(kTile, N, true);
+      constexpr uint32_t id_s = instr_desc(kTile, N, false, true), id_o = instr_desc(kTile, N, true, false);
       auto scores = [&](int j) {  // S[j & 1] = K tile x Q^T
         const uint32_t slot = uniform((2u * j) % NS), to = uniform(tmem + (j & 1) * N);
         bool ok = bar_wait(smem_addr(&sm.full[slot]), ((2u * j) / NS) & 1, gave_up);
@@ -212,7 +227,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         if (elect()) {
           const uint64_t kd = k_desc + (slot * C::kSlot >> 4), qd = q_desc + ((seg & 1) * C::kQ >> 4);
 #pragma unroll
-          for (int t = 0; t < C::TERMS; ++t)
+          for (int t = 0; t < C::kQTerms; ++t)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) mma_f8(to, kd + 2 * k, qd + (2 * k + (t * N * D >> 4)), id_s, t > 0 || k > 0);
           commit(smem_addr(&sm.empty[slot]));
@@ -259,7 +274,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     do {
       const RowTile r = it.r;
       const int r0 = r.rt * N;
-      // Queries into shared memory, as e4m3 terms of q / 2^eq: kLanes lanes a row. Up to eight loads a lane are in
+      // Queries into shared memory, as e5m2 terms of q / 2^eq: kLanes lanes a row. Up to eight loads a lane are in
       // flight at once; an item of more rows is read a second time, from L2, when its scale is known.
       constexpr int kLanes = D / 8, kRows = C::EW * 32 / kLanes, kSteps = (N + kRows - 1) / kRows,
                     kBatch = kSteps <= 8 ? kSteps : kSteps / 2;
@@ -305,7 +320,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         named_sync(2, C::EW * 32);
         amax = fmaxf(sm.red[0], sm.red[1]);
       }
-      const int eq = kv8_need(amax, -120, 120);
+      const int eq = kv8_need(amax, -113, 120) - 7;  // amax <= 57344 * 2^eq, e5m2's largest
       const float down = a.negate ? -pow2i(-eq) : pow2i(-eq);
       if (seg > 1) {
         ok = bar_wait(smem_addr(&sm.q_free[seg & 1]), ((seg >> 1) - 1) & 1, gave_up);
@@ -324,11 +339,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           float x[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) x[k] = row < r.rows ? to_f(e[k]) * down : 0.f;
-          uint2 codes[C::TERMS];
-          split8<C::TERMS>(x, codes);
+          uint2 codes[C::kQTerms];
+          split8<C::kQTerms>(x, codes);
           const uint32_t o = swz<D>(row, d);
 #pragma unroll
-          for (int t = 0; t < C::TERMS; ++t) *reinterpret_cast<uint2*>(q_to + t * N * D + o) = codes[t];
+          for (int t = 0; t < C::kQTerms; ++t) *reinterpret_cast<uint2*>(q_to + t * N * D + o) = codes[t];
         }
       }
       if (own == 0) {

@@ -159,9 +159,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
 // and loops the compiler knows to be uniform: an issue then takes three
 // instructions, and some twenty where it has to move addresses between registers.
 // Instruction descriptor: e4m3 operands, fp32 accumulators, M x N; `major_mn`:
-// both operands lie with M (N) contiguous rather than K.
-__host__ __device__ constexpr uint32_t instr_desc(int m, int n, bool major_mn) {
-  return 1u << 4 | (major_mn ? 3u << 15 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(m >> 4) << 24;
+// both operands lie with M (N) contiguous rather than K; `b_e5m2`: the second
+// operand is e5m2.
+__host__ __device__ constexpr uint32_t instr_desc(int m, int n, bool major_mn, bool b_e5m2) {
+  return 1u << 4 | (b_e5m2 ? 1u << 10 : 0u) | (major_mn ? 3u << 15 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(m >> 4) << 24;
 }
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
