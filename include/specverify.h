@@ -503,8 +503,7 @@ int spec_kv8_append(const spec_kv8_cache* cache, const void* keys, int64_t k_str
  * SPEC_ROW_CACHE where the sequence's lengths are invalid (cu_tokens not rising
  * or outside [0, T], more than max_tokens, cache_len negative or beyond the
  * table): its rows are NaN where cu_tokens names some; or where the id of a block
- * that it uses is outside the pool: the rows that see that block are NaN (rows that
- * see none of its entries, but others of the same 128 positions, may be too).
+ * that it uses is outside the pool: the rows that see an entry of that block are NaN.
  * SPEC_ROW_TIMEOUT: see there; the rows hold nothing of use. Tokens of no sequence
  * are not written.
  * workspace: spec_kv8_workspace_bytes(...) bytes, 256-byte aligned, needing no

@@ -75,7 +75,7 @@ struct Kv8AttnArgs {
   int row_tiles;        // row tiles a sequence has at most
   int parts;            // thread blocks the cache is split over
   int order;            // tensor maps' dimensions 1..3: 2-bit fields naming slot (0), head (1), block (2)
-  int32_t* gave_up;     // workspace [parts]: a wait of the block ran out
+  int32_t* gave_up;     // workspace [parts]: what a part met (kGaveUp, kOutside)
   int4* cut;            // workspace [parts]: the item that begins in the part and ends behind it: sequence, row tile, KV
                         // head, shares (0: none)
   float2* part_ml;      // workspace [2 parts][rows]: exponent reference, sum of weights

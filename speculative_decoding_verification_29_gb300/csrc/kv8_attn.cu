@@ -98,7 +98,7 @@ struct Cfg {
     alignas(16) float4 page[kMetaRing][kMaxPages];
     alignas(8) uint64_t full[12], empty[12], s_full[2], p_ready[2], o_full[2], q_ready[2], q_free[2], drain;
     uint32_t tmem;
-    int gave_up;
+    int gave_up, outside;
   };
   static_assert(sizeof(Small::smax) >= 64 * sizeof(int), "the search for the run uses these words before the roles begin");
   static constexpr int kBudget = kCtas == 2 ? 115712 : 231424;
@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     bar_init(smem_addr(&sm.drain), 1);
     fence_bar_init();
     sm.gave_up = 0;
+    sm.outside = 0;
     prefetch_map(&kmap);
     prefetch_map(&vmap);
   }
@@ -637,7 +638,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   if (sm.gave_up) drain<NS>(sm, warp == kLoadWarp, begun, warp == kMmaWarp);
   if (warp == kMmaWarp) tmem_free(tmem, C::kCols);
   if (tid == 0) {
-    a.gave_up[blockIdx.x] = sm.gave_up;
+    a.gave_up[blockIdx.x] = (sm.gave_up ? kGaveUp : 0) | (sm.outside ? kOutside : 0);
     if (!work || sm.gave_up) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);  // what was begun is not to be joined
   }
   griddep_launch_dependents();

@@ -17,6 +17,7 @@ using namespace tc;
 
 constexpr int kTile = 128;
 constexpr int kMetaRing = 8;
+constexpr int kGaveUp = 1, kOutside = 2;  // of a part: a wait ran out; it met a page outside the pool
 constexpr int kMaxPages = kTile / 16;
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -237,8 +238,9 @@ __device__ __forceinline__ int4 cut_item(const Runs& runs, int part, const RowTi
 }
 
 // The copying warp: the pages of each tile's keys, then of its values, into a
-// ring of NS slots, and of each page of the tile 2^ek (NaN for a page outside the
-// pool), ev and 2^-ev into sm.page. Returns the number of ring slots that copies were begun into.
+// ring of NS slots, and of each page of the tile 2^ek, ev and 2^-ev into sm.page (of
+// a page outside the pool 1, 0 and 1: its slots hold what was there before, and the
+// join finds the rows that see them). Returns the number of ring slots that copies were begun into.
 template <int N, int COST, int D, int NS, typename S>
 __device__ __forceinline__ uint32_t copy_tiles(const Kv8AttnArgs& a, const Start& start, int64_t count,
                                                const CUtensorMap& kmap, const CUtensorMap& vmap, uint8_t* ring, S& sm,
@@ -273,6 +275,7 @@ __device__ __forceinline__ uint32_t copy_tiles(const Kv8AttnArgs& a, const Start
         ke = ke_next;
         ve = ve_next;
         id_next = page_id(t * ppt + 32 + lane);
+        if (__any_sync(0xffffffffu, id == -2)) sm.outside = 1;
       }
       if ((g & 31) == 16) {
         ke_next = scale_at(a.c.ks, id_next);
@@ -298,8 +301,7 @@ __device__ __forceinline__ uint32_t copy_tiles(const Kv8AttnArgs& a, const Start
           const int my_ke = kv8_exp(static_cast<uint8_t>(__shfl_sync(0xffffffffu, static_cast<int>(ke), from))),
                     my_ve = kv8_exp(static_cast<uint8_t>(__shfl_sync(0xffffffffu, static_cast<int>(ve), from)));
           if (lane < ppt)
-            sm.page[i % kMetaRing][lane] = make_float4(my_id != -2 ? pow2i(my_ke) : __int_as_float(0x7fffffff),
-                                                       static_cast<float>(my_ve), pow2i(-my_ve), 0.f);
+            sm.page[i % kMetaRing][lane] = make_float4(pow2i(my_ke), static_cast<float>(my_ve), pow2i(-my_ve), 0.f);
         }
         __syncwarp();
         if (lane == 0) bar_expect(bar, bytes);
@@ -332,7 +334,23 @@ __device__ __forceinline__ void drain(S& sm, bool copied, uint32_t begun, bool i
 //
 // Adds the shares of items that runs cut. Block x takes the item that begins in
 // part x and ends behind it, a warp one row at a time: shares in the order of the
-// parts, each times 2^(its reference - the largest). The last blocks check sequences.
+// parts, each times 2^(its reference - the largest). The last blocks check sequences,
+// and make the rows NaN that see an entry of a page outside the pool. (A cut item's
+// rows are made so by both.)
+
+// Whether step token i of sequence b (ctx tokens before the step, n in it) sees an entry of a page outside the pool; a warp.
+__device__ __forceinline__ bool sees_outside(const Kv8AttnArgs& a, int b, int ctx, int n, int i) {
+  const int bs = a.c.block, pages = (ctx + n + bs - 1) / bs;
+  bool hit = false;
+#pragma unroll 1
+  for (int p = threadIdx.x & 31; p < pages; p += 32) {
+    const int id = a.c.table[static_cast<int64_t>(b) * a.c.max_blocks + p];
+    if (id >= 0 && id < a.c.num_blocks) continue;
+    hit |= p * bs < ctx;
+    for (int j = max(0, p * bs - ctx); j < min(n, (p + 1) * bs - ctx); ++j) hit |= sees(a, b, i, j);
+  }
+  return __any_sync(0xffffffffu, hit);
+}
 
 constexpr int kJoinThreads = 256;
 
@@ -345,7 +363,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
     const int b = (blockIdx.x - a.parts) * (kJoinThreads / 32) + warp;
     if (blockIdx.y > 0 || b >= a.c.B) return;
     bool late = false;
-    for (int i = lane; i < a.parts; i += 32) late |= a.gave_up[i] != 0;
+    for (int i = lane; i < a.parts; i += 32) late |= (a.gave_up[i] & kGaveUp) != 0;
     const int lo = a.cu[b], hi = a.cu[b + 1], len = a.c.len[b];
     const bool sound = kv8_seq_ok(a.c, a.T, lo, hi, len) && hi - lo <= a.max_tokens;
     bool bad = !sound;
@@ -359,13 +377,15 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
     bad = __any_sync(0xffffffffu, bad);
     late = __any_sync(0xffffffffu, late);
     if (lane == 0) a.row_status[b] = (bad ? SPEC_ROW_CACHE : 0) | (late ? SPEC_ROW_TIMEOUT : 0);
-    if (!sound && lo >= 0 && hi > lo && hi <= a.T) {
+    if (bad && lo >= 0 && hi > lo && hi <= a.T) {
 #pragma unroll 1
-      for (int t = lo; t < hi; ++t)
+      for (int t = lo; t < hi; ++t) {
+        if (sound && !sees_outside(a, b, len, hi - lo, t - lo)) continue;
 #pragma unroll 1
         for (int h = 0; h < a.q_heads; ++h)
           for (int d = lane; d < D; d += 32)
             static_cast<QT*>(a.out)[t * a.ost + h * a.osh + d] = from_f<QT>(__int_as_float(0x7fffffff));
+      }
     }
     return;
   }
@@ -375,6 +395,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
   if (n == 0) return;
   const RowTile r = row_tile<N>(a, item.x, item.y);
   const int64_t first = blockIdx.x;
+  bool outside = false;
+  for (int i = lane; i < n; i += 32) outside |= (a.gave_up[first + i] & kOutside) != 0;
+  outside = __any_sync(0xffffffffu, outside);
 #pragma unroll 1
   for (int row = blockIdx.y * (kJoinThreads / 32) + warp; row < r.rows; row += gridDim.y * (kJoinThreads / 32)) {
     auto share = [&](int i) { return (2 * (first + i) + (i == 0 ? 1 : 0)) * N + row; };
@@ -405,7 +428,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
     const int item_row = item.y * N + row, tok = item_row / a.group;
     QT* out = static_cast<QT*>(a.out) + (r.first + static_cast<int64_t>(tok)) * a.ost +
               (item.z * a.group + (item_row - tok * a.group)) * a.osh + lane * V;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (outside && sees_outside(a, item.x, r.ctx, r.n, tok)) inv = __int_as_float(0x7fffffff);
 #pragma unroll
     for (int k = 0; k < V; ++k) out[k] = from_f<QT>(acc[k] * inv);
   }

@@ -69,7 +69,7 @@ struct Wide {
     alignas(8) uint64_t full[8], empty[8], full16[4], empty16[4], s_full[2], p_ready[2], o_full[2], q_ready[kItems], q_free,
         done, drain;
     uint32_t tmem;
-    int gave_up;
+    int gave_up, outside;
     alignas(8) int tmp[64];
   };
   static constexpr int kFixed = 1024 + kQ + NF * kF16 + static_cast<int>(sizeof(Small));
@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     bar_init(smem_addr(&sm.done), 8);
     fence_bar_init();
     sm.gave_up = 0;
+    sm.outside = 0;
     prefetch_map(&kmap);
     prefetch_map(&vmap);
   }
@@ -687,7 +688,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   if (sm.gave_up) drain<NS>(sm, warp == kLoadWarp, begun, warp == kMmaWarp);
   if (warp == kMmaWarp) tmem_free(tmem, 512);
   if (tid == 0) {
-    a.gave_up[blockIdx.x] = sm.gave_up;
+    a.gave_up[blockIdx.x] = (sm.gave_up ? kGaveUp : 0) | (sm.outside ? kOutside : 0);
     if (!work || sm.gave_up) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);  // what was begun is not to be joined
   }
   griddep_launch_dependents();
