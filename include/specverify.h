@@ -423,7 +423,8 @@ int spec_kv_compact(void* kv, int elem_bytes, int n_planes, int B, int S, int W,
  * weights take the scale as an exponent.
  *
  * Limits: block 16, 32, 64 or 128; head_dim 64 or 128; 1 <= kv_heads <= 1024;
- * 1 <= B <= 65535; num_blocks, max_blocks >= 1, num_blocks * kv_heads < 2^31.
+ * 1 <= B <= 65535; num_blocks, max_blocks >= 1, num_blocks * kv_heads < 2^31,
+ * max_blocks * block <= 2^31 - 128.
  * Alignment: k and v 16 bytes and the three strides (bytes) multiples of 16;
  * stride_slot >= head_dim. Blocks, heads and slots may lie in any order. */
 typedef struct {

@@ -12,6 +12,7 @@ using namespace specv;
 namespace {
 
 constexpr int kMaxB = 65535;
+constexpr int64_t kMaxTokens = (1LL << 31) - 128;  // of a sequence: positions rounded up to a tile of 128 stay below 2^31
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -27,7 +28,7 @@ int take_pool(const spec_kv8_cache* s, Kv8Pool* c) {
   if (s->head_dim != 64 && s->head_dim != 128) return SPEC_ERR_UNSUPPORTED;
   if (s->B > kMaxB || s->kv_heads > 1024) return SPEC_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(s->num_blocks) * s->kv_heads > 0x7fffffffLL) return SPEC_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(s->max_blocks) * s->block > 0x7fffffffLL) return SPEC_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(s->max_blocks) * s->block > kMaxTokens) return SPEC_ERR_UNSUPPORTED;
   if (s->stride_block >= (1LL << 40) || s->stride_head >= (1LL << 40) || s->stride_slot >= (1LL << 40))
     return SPEC_ERR_UNSUPPORTED;
   c->k = static_cast<uint8_t*>(s->k);

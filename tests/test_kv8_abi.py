@@ -177,3 +177,12 @@ def test_python_refuses_host_tensors():
         sv.spec_kv8_attention(x, *args, torch.tensor([0, 1], dtype=torch.int32), max_tokens=1)
     with pytest.raises(ValueError):
         sv.spec_kv8_compact(*args, i)
+
+
+@pytest.mark.parametrize("block", [16, 32, 64, 128])
+def test_longest_sequence(lib, block):
+    """A position rounded up to a whole tile of 128 slots stays below 2^31, whatever cache_len says."""
+    most = (2 ** 31 - 128) // block
+    for call in (append, attention, compact):
+        assert call(lib, cache(block=block, max_blocks=most)) == CUDA
+        assert call(lib, cache(block=block, max_blocks=most + 1)) == LIMIT
