@@ -429,6 +429,9 @@ def _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, plane
     shape, stride = k_cache.shape, k_cache.stride()
     if dev.type != "cuda" or v_cache.device != dev:
         raise ValueError("k_cache and v_cache must be CUDA tensors of one device (the cache lives there)")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {dev}, the current device is cuda:{torch.cuda.current_device()}: kernels are "
+                         f"launched there (torch.cuda.device)")
     if len(shape) != 4 + planes or v_cache.shape != shape or v_cache.stride() != stride:
         raise ValueError("k_cache and v_cache must both be [blocks, kv_heads, block, head_dim], with the same strides")
     if k_cache.element_size() != 1 or v_cache.element_size() != 1 or stride[-1] != 1:

@@ -133,3 +133,9 @@ def test_compact_arguments():
     planes = [z(3, 6, 2, 32, 128), z(3, 6, 2, 32, 128), z(3, 6, 2), z(4, 6, 3)[:3, :, :2]]
     with pytest.raises(ValueError):
         sv().spec_kv8_compact(*planes, *cache()[4:], i)
+
+
+def test_another_device_is_refused(monkeypatch):
+    """Kernels are launched on the current device; a cache on another one is refused (one GPU: the current device is faked)."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    everywhere(cache())
