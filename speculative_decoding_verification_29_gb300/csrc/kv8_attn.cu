@@ -43,12 +43,12 @@
 // while the next tiles are worked on.
 //
 // What bounds it. One row of 32 heads (decode, 64 sequences of 1500 to 6500
-// tokens, 8 KV heads of 128): memory, 548 MB in 91 us, 6.0 TB/s, 0.89 of a
-// copy. Nine rows (verification, the same cache): 136 us, 4.1 TB/s, where the
-// softmax groups' instructions (62% of issue slots) and the barrier between the
-// tile's four maxima and its weights set the step of 2100 clocks a tile; the
-// products take 700 of them. One sequence of 517 tokens: 11 us, a chain of
-// lengths, table, queries, one tile a thread block, and the join.
+// tokens, 8 KV heads of 128): memory, 547 MB in 92 us, 5.9 TB/s, 0.87 of a
+// copy. Nine rows (verification, the same cache): 140 us, 4.0 TB/s, where the
+// softmax groups' instructions (61% of issue slots) and the barrier between the
+// tile's four maxima and its weights set the step of 2200 clocks a tile; the
+// tensor pipe is busy for 21% of them. One sequence of 517 tokens: 11 us, a chain
+// of lengths, table, queries, one tile a thread block, and the join.
 #include <string.h>
 
 #include "kv8_attn.cuh"
@@ -59,8 +59,8 @@ namespace {
 
 // ---------------------------------------------------------- configuration --
 
-// Units of an item beside its tiles (see Runs). 64 sequences of 500 to 2000 tokens: 36 rows 73 us without, 66 with 2, 63
-// with 4; 16 rows 41, 39, 40.
+// Units of an item beside its tiles (see Runs). 64 sequences of 500 to 2000 tokens: 36 rows 76 us without, 68 with 2, 65
+// with 3 and 4; 16 rows 43, 40, 41.
 constexpr int kCost = 3;
 
 // D: head dimension. RW: rows of one softmax group of four warps, W: groups.
@@ -107,7 +107,6 @@ struct Cfg {
   static constexpr int kRing = kFit > 12 ? 12 : kFit;
   static constexpr int kSmem = kFixed + kRing * kSlot;
   static_assert(kRing >= 3, "ring of tile slots");
-  static_assert(N * D + kRing * kSlot >= kTile * D, "128 query rows are read, whatever lies behind them");
   static_assert(kMetaRing >= (kRing + 1) / 2 + 1, "meta entries live as long as a tile's slots");
 };
 
@@ -668,11 +667,11 @@ cudaError_t launch_rows(const Kv8AttnArgs& a, int rows, const CUtensorMap& k, co
 // on a row of scores a lane is cheaper, two row tiles of 128 to an item when there are more than 128.
 // B = 64, contexts of 1500 to 6500 tokens, 8 KV heads of 128, bf16, us (16 sequences from 132 rows on):
 //   rows of a sequence    4     16     32     36     48     52     64     68    128    132    256
-//   as chosen            90     87    121    136    133    163    166    176    186     75     88
-//   32 rows an item     113    106    121
-//   64                  153    145    161    157    150    163    166
-//   128 (kv8_wide)      160    151    166    163    155    166    171    176    186     97    109
-//   256 (kv8_wide)      202    189    209    202    189    203    208    210    212     74     88
+//   as chosen            92     88    123    140    135    160    164    181    190     75     89
+//   32 rows an item     114    108    123
+//   64                  151    145    161    155    148    160    164
+//   128 (kv8_wide)      166    157    172    168    159    172    175    181    190    100    112
+//   256 (kv8_wide)      205    193    211    204    191    205    210    212    212     75     89
 int kv8_attention_rows(int64_t max_rows) {
   if (max_rows <= 64) return max_rows <= 16 ? 16 : static_cast<int>((max_rows + 15) / 16 * 16);
   return max_rows <= 128 ? 128 : 256;

@@ -17,15 +17,19 @@
 // Rotation. position * inv_freq in turns is an integer product modulo 2^64
 // (inv_freq / 2 pi as a 64-bit fraction), so the reduced angle loses nothing at
 // far positions and takes no 64-bit floating point.
-// What bounds it. Prompts (22,000 tokens, 8 KV heads of 128, fp16): 37.4 us, 4.0
+// What bounds it. Prompts (22,000 tokens, 8 KV heads of 128, fp16): 37.6 us, 4.0
 // TB/s read and written, 0.59 of a copy; instructions (60% of issue slots) and the
-// two barriers a head share the rest. 64 sequences x 9 tokens with queries: 10.1
-// us, launch and the lookup of each block's sequence; 9 tokens: 3.5 us, latency.
+// barrier of each head's maximum share the rest (fp32: 56 us, 4.0 TB/s). 64
+// sequences x 9 tokens with queries: 10.5 us, launch and the lookup of each block's
+// sequence; 9 tokens: 3.4 us, latency.
 //
 // Compaction. A warp owns one plane, keys or values and head of a sequence; entries move
 // through shared memory in path order, so that a destination is never read
-// after it was written. 32 planes x 16 sequences: 8.9 us, latency of lengths, path,
-// table, scales and entries, each read after the one before.
+// after it was written. 32 planes x 16 sequences: 7.9 us. A block's room for 64
+// entries a warp (33 KB) lets six blocks on an SM, 2.2 rounds of the 2048, and in
+// each three warps wait for the one that checks the path (the barrier is the first
+// stall); then lengths, path, table, scales and entries are read one after the
+// other.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <string.h>
@@ -396,8 +400,8 @@ cudaError_t launch_append(const Kv8AppendArgs& args, cudaStream_t st) {
   const int tpr = a.c.D / 16;
   // Heads to a thread block: as many as leave 1024 threads for every other SM, so that what is found once for a block's
   // heads (its sequence, its place, the angles) is shared; a step of few tokens spends most of its time on that.
-  // 64 sequences x 9 tokens x 8 heads with queries: 10.1 us, 20.0 us where up to 8 times as many threads were asked for;
-  // 22,000 tokens x 8 heads: 37.4 us and 52.7 us, 75 us with one head to a thread block.
+  // 64 sequences x 9 tokens x 8 heads with queries: 10.5 us, 21.3 us where up to 8 times as many threads were asked for;
+  // 22,000 tokens x 8 heads: 37.7 us and 42.4 us, 83 us with one head to a thread block.
   const int64_t candidates = a.T / a.c.block + 2 * static_cast<int64_t>(a.c.B);
   a.heads_per_cta = static_cast<int>(std::min<int64_t>(a.c.H, std::max<int64_t>(1, candidates * 2 * a.c.H / (kSms / 2 * (1024 / NT)))));
   a.head_groups = (a.c.H + a.heads_per_cta - 1) / a.heads_per_cta;

@@ -24,7 +24,8 @@
 // Four more warps convert tiles and load queries, one copies, one issues.
 //
 // What bounds it. Prompts (three of 1500 to 4096 tokens behind up to 1000, 32
-// heads of 128, fp16): 381 us, 1025 TFLOP/s, 0.54 of a library product's rate.
+// heads of 128, fp16): 376 us, 1040 TFLOP/s, 0.54 of a library product's rate
+// (bf16: 403).
 // Scores and weights of a pair of tiles hold the tensor pipe for 2112 clocks of a
 // step of about 3700: a stream's weights must be written before its product, and
 // the product issued before its next scores, and two streams do not cover that
