@@ -45,6 +45,14 @@ def _dev(t: torch.Tensor, device, dtype=None) -> torch.Tensor:
     return t.contiguous()
 
 
+def _here(dev: torch.device) -> torch.device:
+    """A call's device. Kernels are launched on the current one, which cannot use another's pointers."""
+    if dev.index is not None and dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}: kernels are "
+                         f"launched there (torch.cuda.device)")
+    return dev
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -113,7 +121,7 @@ def spec_verify_chain(target_logits, draft_logits, draft_tokens, u_accept, u_res
     Returns accept_len, out_tokens, row_status and (with ``stats``)
     lse_target, lse_draft, p_at_x, q_at_x."""
     lib = _lib.load()
-    dev = target_logits.device if target_logits.is_cuda else torch.device(device)
+    dev = _here(target_logits.device if target_logits.is_cuda else torch.device(device))
     Lp = _dev(target_logits, dev)
     Lq = _dev(draft_logits, dev)
     x = _dev(draft_tokens, dev, torch.int32)
@@ -316,7 +324,7 @@ def spec_verify_chain_greedy(target_logits, draft_tokens, out: Optional[Dict[str
                              stream=None) -> Dict[str, torch.Tensor]:
     """Greedy chain verification: accept_len, out_tokens, argmax_ids, row_status."""
     lib = _lib.load()
-    dev = target_logits.device if target_logits.is_cuda else torch.device(device)
+    dev = _here(target_logits.device if target_logits.is_cuda else torch.device(device))
     Lp = _dev(target_logits, dev)
     x = _dev(draft_tokens, dev, torch.int32)
     B, K1, V = Lp.shape
@@ -344,7 +352,7 @@ def spec_verify_tree_greedy(node_logits, node_tokens, retrieve_indices, n1: int,
     """Merged-tree greedy verification: accept_len, best_row, path_nodes,
     out_tokens, subtree, row_status."""
     lib = _lib.load()
-    dev = node_logits.device if node_logits.device.type == "cuda" else torch.device(device)
+    dev = _here(node_logits.device if node_logits.device.type == "cuda" else torch.device(device))
     Lt = _dev(node_logits, dev)
     tok = _dev(node_tokens, dev, torch.int32)
     R = _dev(retrieve_indices, dev, torch.int32)
@@ -375,7 +383,7 @@ def spec_tree_confidence(node_conf, n1: int, out: Optional[Dict[str, torch.Tenso
                          stream=None) -> Dict[str, torch.Tensor]:
     """Confidence routing: scores [B, 2] and choice [B] (1 or 2)."""
     lib = _lib.load()
-    dev = node_conf.device if node_conf.device.type == "cuda" else torch.device(device)
+    dev = _here(node_conf.device if node_conf.device.type == "cuda" else torch.device(device))
     c = _dev(node_conf, dev, torch.float32)
     B, N = c.shape
     if out is None:
@@ -403,7 +411,7 @@ def spec_kv_compact(kv: torch.Tensor, base_pos, accept_len, path=None, out: Opti
         raise ValueError("kv must be viewed as [planes, B, S, W] with a contiguous last dimension")
     P_, B, S, W = kv.shape
     sp, sb, ss, _ = kv.stride()
-    dev = kv.device
+    dev = _here(kv.device)
     base = _dev(torch.as_tensor(base_pos), dev, torch.int32)
     acc = _dev(torch.as_tensor(accept_len), dev, torch.int32)
     pth = None if path is None else _dev(torch.as_tensor(path), dev, torch.int32)
@@ -429,9 +437,7 @@ def _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, plane
     shape, stride = k_cache.shape, k_cache.stride()
     if dev.type != "cuda" or v_cache.device != dev:
         raise ValueError("k_cache and v_cache must be CUDA tensors of one device (the cache lives there)")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {dev}, the current device is cuda:{torch.cuda.current_device()}: kernels are "
-                         f"launched there (torch.cuda.device)")
+    _here(dev)
     if len(shape) != 4 + planes or v_cache.shape != shape or v_cache.stride() != stride:
         raise ValueError("k_cache and v_cache must both be [blocks, kv_heads, block, head_dim], with the same strides")
     if k_cache.element_size() != 1 or v_cache.element_size() != 1 or stride[-1] != 1:
@@ -653,7 +659,7 @@ def spec_tree_entropy(draft_logits, n1: int, temperature: float = 1.0, out: Opti
     (bf16 or fp32). Returns scores [B, 2], choice [B], row_status [B] and
     (with ``node_entropy``) the per-node entropies [B, N]."""
     lib = _lib.load()
-    dev = draft_logits.device if draft_logits.device.type == "cuda" else torch.device(device)
+    dev = _here(draft_logits.device if draft_logits.device.type == "cuda" else torch.device(device))
     Ld = _dev(draft_logits, dev)
     B, N, V = Ld.shape
     code = _dtype_code(Ld)
@@ -681,7 +687,7 @@ def spec_tree_expand(draft_logits, logc, M: int, temperature: float = 1.0,
     their paths' log cumulative probabilities. Returns the M best children
     as parent, token [B, M] int32, score [B, M] fp32 and row_status [B]."""
     lib = _lib.load()
-    dev = draft_logits.device if draft_logits.device.type == "cuda" else torch.device(device)
+    dev = _here(draft_logits.device if draft_logits.device.type == "cuda" else torch.device(device))
     Ld = _dev(draft_logits, dev)
     B, F, V = Ld.shape
     lc = _dev(logc, dev, torch.float32)
@@ -714,7 +720,7 @@ def spec_merge_trees(tokens1, mask1, retrieve1, pos1, tokens2, mask2, retrieve2,
     int32, pos* [B, n+1] int32. Returns tokens [B, N], mask [B, N, N],
     retrieve [B, R1+R2, max(D1, D2)], pos [B, N] and n1."""
     lib = _lib.load()
-    dev = tokens1.device if tokens1.device.type == "cuda" else torch.device(device)
+    dev = _here(tokens1.device if tokens1.device.type == "cuda" else torch.device(device))
     t1, t2 = _dev(tokens1, dev, torch.int32), _dev(tokens2, dev, torch.int32)
     m1, m2 = _dev(mask1, dev, torch.uint8), _dev(mask2, dev, torch.uint8)
     r1, r2 = _dev(retrieve1, dev, torch.int32), _dev(retrieve2, dev, torch.int32)
@@ -742,7 +748,7 @@ def spec_verify_chain_warped(target_logits, draft_logits, draft_tokens, u_accept
     """Chain verification with top-k / top-p applied to p and q (0 and 1.0:
     off). Returns accept_len, out_tokens, row_status, p_at_x, q_at_x."""
     lib = _lib.load()
-    dev = target_logits.device if target_logits.is_cuda else torch.device(device)
+    dev = _here(target_logits.device if target_logits.is_cuda else torch.device(device))
     Lp, Lq = _dev(target_logits, dev), _dev(draft_logits, dev)
     B, K1, V = Lp.shape
     K = K1 - 1

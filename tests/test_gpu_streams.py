@@ -102,6 +102,18 @@ def verification_calls():
     )
 
 
-@pytest.mark.parametrize("name", ["chain", "greedy", "warped", "tree", "confidence", "entropy", "expand", "merge", "compact"])
+NAMES = ["chain", "greedy", "warped", "tree", "confidence", "entropy", "expand", "merge", "compact"]
+
+
+@pytest.mark.parametrize("name", NAMES)
 def test_verification_calls(name):
     check_call(verification_calls()[name])
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_another_device_is_refused(name, monkeypatch):
+    """Tensors on a device that is not the current one (one GPU: the current device is faked)."""
+    call = verification_calls()[name]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError):
+        call()
