@@ -274,8 +274,8 @@ def _own(s):
     if op == "compact":
         r = sv.spec_latent_compact(s["cache"], s["block_table"], s["cache_len"], s["accept_len"], s["path"])
         return [s["cache"], r["new_len"]]
-    r = sv.spec_pages_update(s["block_table"], s["cache_len"], s["refs"], [s["cache"]], keep_len=s["keep_len"],
-                             source=s["source_dev"], need=s["need"])
+    r = sv.spec_pages_update(s["block_table"], s["cache_len"], s["refs"], [s["cache"]], planes=True,
+                             keep_len=s["keep_len"], source=s["source_dev"], need=s["need"])
     s["block_table"], s["cache_len"] = r["block_table"], r["cache_len"]  # the loop goes on with these
     return [s["cache"], r["block_table"], r["cache_len"], s["refs"], r["row_status"]]
 
