@@ -535,6 +535,136 @@ int spec_kv8_compact(const spec_kv8_cache* cache, int n_planes, int64_t stride_p
                      const int32_t* path, int D, const int32_t* accept_len, int32_t* new_len, int32_t* row_status,
                      void* stream);
 
+/* ------------------------------------------------------------------------
+ * A paged cache of latent vectors (one layer), in 16 bits.
+ *
+ * A token has one entry for all heads: a latent vector of latent_dim elements,
+ * from which the model makes every head's key and value, and rot_dim rotated
+ * elements that the heads' keys share. The pool has num_blocks blocks of
+ * `block` tokens; slot s of block i is an entry of latent_dim + rot_dim
+ * contiguous elements of type dtype (SPEC_BF16 or SPEC_F16) at byte
+ * i * stride_block + s * stride_slot. block_table and cache_len as in
+ * spec_kv8_cache: the token at position t of sequence b lies in slot t mod
+ * block of block block_table[b][t / block].
+ *
+ * Limits: block 16, 32, 64 or 128; latent_dim 128, 256, 384 or 512; rot_dim 16,
+ * 32, 48 or 64; 1 <= B <= 65535; max_blocks * block <= 2^31 - 128.
+ * Alignment: data 16 bytes, the strides (bytes) multiples of 16; stride_slot >= an
+ * entry. Blocks and slots may lie in any order. */
+typedef struct {
+  void* data;                 /* device, entries */
+  const int32_t* block_table; /* device [B][max_blocks] */
+  const int32_t* cache_len;   /* device [B] */
+  int32_t B, num_blocks, max_blocks, block, latent_dim, rot_dim, dtype;
+  int64_t stride_block, stride_slot; /* bytes, multiples of 16 */
+} spec_latent_cache;
+
+/* Append the step's latent vectors, normalised, and their shared dimensions,
+ * rotated; optionally rotate the queries' last rot_dim dimensions in the same
+ * launch.
+ *   latents, rope_keys  device, `dtype` (SPEC_F32 or the cache's): token t's
+ *       latent_dim and rot_dim contiguous elements at t * its stride (elements)
+ *   cu_tokens, positions, inv_freq, interleaved  as in spec_kv8_append, the
+ *       rotated dimensions being the entry's last rot_dim ones; inv_freq (HOST
+ *       [rot_dim / 2] fp64) is required
+ *   norm_weight   device [latent_dim], norm_dtype SPEC_F32 or `dtype`, or NULL:
+ *       the vector is stored as it is; else as x / sqrt(mean(x^2) + eps) *
+ *       weight (eps >= 0, finite)
+ *   queries, queries_out  device or NULL: [T][q_heads] rows of rot_dim elements
+ *       of type `dtype` with strides of their own, for example the tails of the
+ *       rows that spec_latent_attention reads (queries_out may be queries)
+ * Computed in fp32 and rounded once. Output: row_status [B] int32 as by
+ * spec_kv8_append. Two sequences must not write the same slot.
+ * Errors: SPEC_ERR_ARG for NULL pointers, sizes, types or strides outside the
+ * above; SPEC_ERR_UNSUPPORTED beyond the limits (T < 2^26; q_heads <= 65536,
+ * T * q_heads < 2^31). */
+int spec_latent_append(const spec_latent_cache* cache, const void* latents, int64_t l_stride_token, const void* rope_keys,
+                       int64_t r_stride_token, int dtype, int T, const int32_t* cu_tokens, const int32_t* positions,
+                       const double* inv_freq, int interleaved, const void* norm_weight, int norm_dtype, float eps,
+                       const void* queries, int64_t q_stride_token, int64_t q_stride_head, void* queries_out,
+                       int64_t qo_stride_token, int64_t qo_stride_head, int q_heads, int32_t* row_status, void* stream);
+
+/* Attention of the step's queries over the cache, all heads over the same
+ * entries: for sequence b, its token i and each query head,
+ *     out = sum_t softmax_t(sm_scale * q . entry_t) latent_t
+ * over the context and those of the step's tokens (appended before) that token i
+ * sees, as in spec_kv8_attention. The keys' up-projection is absorbed into q by
+ * the caller, the values' is applied to out. A row that sees nothing is 0.
+ * Entries that a row does not see do not reach it, finite or not; a row that sees
+ * an entry with an infinite or NaN element is NaN, or (an entry of the context
+ * whose score is -infinity) NaN in that entry's infinite dimensions only.
+ *   queries       device, the cache's type: [T][q_heads] rows of latent_dim +
+ *       rot_dim contiguous elements, any strides (elements)
+ *   out           device, the cache's type: [T][q_heads] rows of latent_dim
+ *   cu_tokens, max_tokens, tree_mask, sm_scale  as in spec_kv8_attention
+ *   q_heads       at most 1024
+ * Scores, maxima, sums and the accumulated output are fp32. The weights enter the
+ * second product rounded to the cache's type, and the sum that divides is that of
+ * the rounded weights; a weight is relative to a reference that the row's largest
+ * score passes by at most 2^8.
+ * Outputs, workspace (spec_latent_workspace_bytes(...) bytes, 256-byte aligned,
+ * no initialisation) and errors as in spec_kv8_attention. */
+size_t spec_latent_workspace_bytes(const spec_latent_cache* cache, int q_heads, int max_tokens);
+int spec_latent_attention(const spec_latent_cache* cache, const void* queries, int64_t q_stride_token, int64_t q_stride_head,
+                          int T, int q_heads, const int32_t* cu_tokens, int max_tokens, const uint8_t* tree_mask,
+                          float sm_scale, void* out, int64_t o_stride_token, int64_t o_stride_head, int32_t* row_status,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* spec_kv8_compact for this cache, in every one of n_planes pools (layers) that
+ * share the block table, stride_plane bytes apart (a multiple of 16). Entries keep
+ * their bytes. D <= 256; n_planes < 2^24. */
+int spec_latent_compact(const spec_latent_cache* cache, int n_planes, int64_t stride_plane, const int32_t* path, int D,
+                        const int32_t* accept_len, int32_t* new_len, int32_t* row_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The pages of a paged cache between two steps, for any pools that share a
+ * block table: sequences are cut back, forked, ended and given blocks, without
+ * the host learning a length.
+ *
+ * A sequence holds the blocks that its row of block_table names up to the first
+ * entry behind them; entries behind are -1. refs[i] is the number of rows that
+ * hold block i, 0 a free block. For every sequence b, with s = source[b] (b
+ * where source is NULL):
+ *   1. b keeps the first keep_len[b] tokens of sequence s as it was before the
+ *      call (cache_len[s] where keep_len is NULL; 0 ends b): its row becomes the
+ *      blocks of those tokens. Blocks that it held and no longer holds lose a
+ *      reference, those that it holds anew gain one.
+ *   2. where need[b] > 0 (NULL: 0), blocks are taken until need[b] more tokens
+ *      fit. If the last of the kept tokens lies inside a block that other rows
+ *      hold too, a block is taken in its place and the kept block is copied into
+ *      it, in every pool; of the sequences that go on writing the same block and
+ *      are all that hold it, the last keeps it.
+ * Blocks are taken lowest id first, in the order of the sequences; blocks freed in
+ * step 1 can be taken in step 2. Where they do not suffice, that sequence and all
+ * later ones that need room take none.
+ *   block_table   device [B][max_blocks] int32
+ *   new_table     device, the rows after the call: block_table itself, unless
+ *       source is given, or memory that does not overlap it
+ *   cache_len     device [B] int32; keep_len, source, need: device [B] int32 or NULL
+ *   refs          device [num_blocks] int32, brought up to date in place
+ *   pools         HOST, n_pools <= 8 of them: n_planes planes of num_blocks blocks
+ *       of block_bytes contiguous bytes. Copies are 16 bytes wide where data, the
+ *       strides and block_bytes allow it.
+ *   new_len       device [B] int32: the tokens kept; not cache_len
+ *   row_status    device [B] int32: SPEC_ROW_CACHE where source, keep_len (below 0
+ *       or above cache_len[s]) or need (below 0) is unsound, which leaves b without
+ *       blocks, where a kept entry is no block's id, or where room was asked for
+ *       and not had: such a sequence must not be appended to.
+ *   workspace     spec_pages_workspace_bytes(...) bytes, 256-byte aligned, needing
+ *       no initialisation
+ * Errors: SPEC_ERR_ARG, SPEC_ERR_WORKSPACE as usual; SPEC_ERR_UNSUPPORTED for B >
+ * 65535, max_blocks > 2^27, max_blocks * block > 2^31 - 128 or n_pools > 8. */
+typedef struct {
+  void* data; /* device */
+  int32_t n_planes;
+  int64_t stride_plane, stride_block, block_bytes; /* bytes */
+} spec_pages_pool;
+size_t spec_pages_workspace_bytes(int B, int max_blocks, int num_blocks);
+int spec_pages_update(const int32_t* block_table, int32_t* new_table, const int32_t* cache_len, const int32_t* keep_len,
+                      const int32_t* source, const int32_t* need, int32_t* refs, int B, int max_blocks, int num_blocks,
+                      int block, const spec_pages_pool* pools, int n_pools, int32_t* new_len, int32_t* row_status,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a return code. */
 const char* spec_status_string(int status);
 

@@ -1,8 +1,8 @@
 """GB300-native speculative-sampling verification.
 
 The compute path is libspecverify.so (hand-written CUDA for sm_103a, C ABI in
-include/specverify.h); ``api`` marshals torch tensors into it. Import of the
-API is lazy so that the package can be inspected without a GPU.
+include/specverify.h); ``api`` and ``latent`` marshal torch tensors into it.
+Import of the API is lazy so that the package can be inspected without a GPU.
 """
 
 __all__ = [
@@ -23,6 +23,11 @@ __all__ = [
     "spec_kv8_attention",
     "spec_kv8_compact",
     "kv8_workspace_bytes",
+    "spec_latent_append",
+    "spec_latent_attention",
+    "spec_latent_compact",
+    "spec_pages_update",
+    "latent_workspace_bytes",
     "workspace_bytes",
     "warped_workspace_bytes",
     "host_workspace_bytes",
@@ -32,8 +37,8 @@ __all__ = [
 
 def __getattr__(name):
     if name in __all__:
-        from . import api
+        from . import api, latent
 
-        value = globals()[name] = getattr(api, name)  # found directly from the next use on
+        value = globals()[name] = getattr(latent if name in vars(latent) else api, name)  # found directly from the next use on
         return value
     raise AttributeError(name)

@@ -33,6 +33,20 @@ class Kv8Cache(ctypes.Structure):
                 [(n, ctypes.c_int32) for n in ("B", "num_blocks", "max_blocks", "block", "kv_heads", "head_dim")] +
                 [(n, L) for n in ("stride_block", "stride_head", "stride_slot")])
 
+class LatentCache(ctypes.Structure):
+    """spec_latent_cache of include/specverify.h."""
+
+    _fields_ = ([(n, P) for n in ("data", "block_table", "cache_len")] +
+                [(n, ctypes.c_int32) for n in ("B", "num_blocks", "max_blocks", "block", "latent_dim", "rot_dim", "dtype")] +
+                [(n, L) for n in ("stride_block", "stride_slot")])
+
+
+class PagesPool(ctypes.Structure):
+    """spec_pages_pool of include/specverify.h."""
+
+    _fields_ = [("data", P), ("n_planes", ctypes.c_int32)] + [(n, L) for n in ("stride_plane", "stride_block", "block_bytes")]
+
+
 SIGNATURES = {
     "spec_workspace_bytes": (Z, [I, I, I, I]),
     "spec_warped_workspace_bytes": (Z, [I, I, I, I]),
@@ -56,6 +70,12 @@ SIGNATURES = {
     "spec_kv8_workspace_bytes": (Z, [P, I, I, I]),
     "spec_kv8_attention": (I, [P, P, L, L, I, I, I, P, I, P, F, P, L, L, P, P, Z, P]),
     "spec_kv8_compact": (I, [P, I, L, L, P, I, P, P, P, P]),
+    "spec_latent_append": (I, [P, P, L, P, L, I, I, P, P, P, I, P, I, F, P, L, L, P, L, L, I, P, P]),
+    "spec_latent_workspace_bytes": (Z, [P, I, I]),
+    "spec_latent_attention": (I, [P, P, L, L, I, I, P, I, P, F, P, L, L, P, P, Z, P]),
+    "spec_latent_compact": (I, [P, I, L, P, I, P, P, P, P]),
+    "spec_pages_workspace_bytes": (Z, [I, I, I]),
+    "spec_pages_update": (I, [P, P, P, P, P, P, P, I, I, I, I, P, I, P, P, P, Z, P]),
     "spec_status_string": (ctypes.c_char_p, [I]),
 }
 

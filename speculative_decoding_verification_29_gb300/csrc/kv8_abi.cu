@@ -6,15 +6,11 @@
 #include <algorithm>
 
 #include "kv8.h"
+#include "paged.h"
 
 using namespace specv;
 
 namespace {
-
-constexpr int kMaxB = 65535;
-constexpr int64_t kMaxTokens = (1LL << 31) - 128;  // of a sequence: positions rounded up to a tile of 128 stay below 2^31
-
-bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The pool's checks; fills `c`.
 int take_pool(const spec_kv8_cache* s, Kv8Pool* c) {
@@ -49,30 +45,6 @@ int take_pool(const spec_kv8_cache* s, Kv8Pool* c) {
   return SPEC_OK;
 }
 
-// Strides of an activation tensor, in elements; a head's row must fit its stride where it has one.
-bool strides_ok(int64_t token, int64_t head) {
-  return token >= 0 && head >= 0 && token < (1LL << 40) && head < (1LL << 40);
-}
-
-int vec16(const void* p, int64_t token, int64_t head, int size) {
-  return on16(p) && (token * size) % 16 == 0 && (head * size) % 16 == 0;
-}
-
-// frequency / (2 pi) modulo 1 in units of 2^-64: the quotient as a sum of two
-// doubles (1 / (2 pi) itself is given as one), exact to about 2^-100 before
-// the rounding.
-uint64_t turn_fraction(double f) {
-  if (f < 0) return 0 - turn_fraction(-f);  // below, floor must not round
-  const double hi_c = 0.15915494309189535, lo_c = -9.8393383374256206e-18;  // 1 / (2 pi) = hi_c + lo_c
-  double hi = f * hi_c;
-  double lo = fma(f, hi_c, -hi) + f * lo_c;
-  hi -= floor(hi);  // exact
-  const double a = floor(ldexp(hi, 32));
-  lo += hi - ldexp(a, -32);
-  const double rest = ldexp(lo, 64);  // below 2^32 in magnitude, may be negative
-  return (static_cast<uint64_t>(a) << 32) + static_cast<uint64_t>(static_cast<int64_t>(llrint(rest)));
-}
-
 // The attention's workspace: a flag and a cut item per part, then each part's two shares of
 // cut items (exponent references and sums, weighted sums).
 struct AttnLayout {
@@ -87,21 +59,6 @@ AttnLayout attn_layout(int rows, int D) {
   l.o = l.ml + up(2 * parts * rows * sizeof(float2));
   l.total = l.o + up(2 * parts * rows * D * sizeof(float));
   return l;
-}
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled encode_tiled() {
-  static const EncodeTiled fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      return static_cast<EncodeTiled>(nullptr);
-    return reinterpret_cast<EncodeTiled>(p);
-  }();
-  return fn;
 }
 
 // The pool as a tensor of bytes, one block of one head a copy. Its dimensions
@@ -130,8 +87,6 @@ bool pool_map(const Kv8Pool& c, void* codes, CUtensorMap* map, int* order) {
                 c.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA; }
 
 }  // namespace
 

@@ -36,6 +36,7 @@
 
 #include <algorithm>
 
+#include "act.cuh"
 #include "kv8.h"
 #include "internal.h"
 
@@ -44,73 +45,6 @@ namespace specv {
 namespace {
 
 constexpr float kInf = __builtin_huge_valf();
-
-// ------------------------------------------------------------ elements --
-
-template <typename T>
-struct Act;
-template <>
-struct Act<float> {
-  static __device__ __forceinline__ float get(const float* p) { return *p; }
-  static __device__ __forceinline__ void load8(const float* p, float* x) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  }
-  static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
-  static __device__ __forceinline__ void store8(float* p, const float* x) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-  }
-};
-template <>
-struct Act<__nv_bfloat16> {
-  static __device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-  static __device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
-  }
-  static __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-  static __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
-    uint4 u;
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    *reinterpret_cast<uint4*>(p) = u;
-  }
-};
-template <>
-struct Act<__half> {
-  static __device__ __forceinline__ float get(const __half* p) { return __half2float(*p); }
-  static __device__ __forceinline__ void load8(const __half* p, float* x) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const __half2* h = reinterpret_cast<const __half2*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(h[i]);
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
-    }
-  }
-  static __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
-  static __device__ __forceinline__ void store8(__half* p, const float* x) {
-    uint4 u;
-    __half2* h = reinterpret_cast<__half2*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-    *reinterpret_cast<uint4*>(p) = u;
-  }
-};
-
-template <typename T>
-__device__ __forceinline__ void load_chunk(const T* p, bool vec, float* x) {
-  if (vec) {
-    Act<T>::load8(p, x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = Act<T>::get(p + i);
-  }
-}
 
 // -------------------------------------------------------------- rotation --
 
