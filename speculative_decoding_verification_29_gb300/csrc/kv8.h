@@ -70,7 +70,7 @@ struct Kv8AttnArgs {
   const int32_t* cu;
   const uint8_t* tree;  // [B][max_tokens][max_tokens] or NULL
   float scale;          // |sm_scale| * log2(e)
-  int negate;           // sm_scale < 0: the queries change sign
+  int negate;           // sm_scale < 0: the queries change sign (2, latent cache only: they are zero)
   int32_t* row_status;
   int row_tiles;        // row tiles a sequence has at most
   int parts;            // thread blocks the cache is split over

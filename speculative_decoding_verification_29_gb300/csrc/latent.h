@@ -47,10 +47,13 @@ struct LatentCompactArgs {
 };
 cudaError_t launch_latent_compact(const LatentCompactArgs& a, cudaStream_t st);
 
+// c.H: items that the value dimensions of one row tile are shared out to, item_dims each. gang: thread blocks that walk the
+// same tiles, one for each item of a sequence; 0: none do.
 struct LatentAttnArgs : Kv8AttnArgs {
-  int rot;
+  int rot, item_dims, gang;
 };
 int latent_attention_rows(int64_t max_rows);
+cudaError_t launch_latent_wide(const LatentAttnArgs& a, int dtype, const CUtensorMap& pool, cudaStream_t st);
 cudaError_t launch_latent_attention(const LatentAttnArgs& a, int dtype, int rows, const CUtensorMap& pool, cudaStream_t st);
 
 struct PagesPool {

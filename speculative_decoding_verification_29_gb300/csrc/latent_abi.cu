@@ -57,16 +57,16 @@ AttnLayout attn_layout(int rows, int C) {
   return l;
 }
 
-// The pool as a tensor of 16-bit elements: 64 of them by the slots of one block a copy. Elements behind an entry's last read
+// The pool as a tensor of 16-bit elements: 64 of them by `slots` slots of one block a copy. Elements behind an entry's last read
 // as zero. Slots and blocks are ordered by their strides; `order` names them.
-bool pool_map(const Kv8Pool& c, int rot, int dtype, CUtensorMap* map, int* order) {
+bool pool_map(const Kv8Pool& c, int rot, int dtype, int slots, CUtensorMap* map, int* order) {
   const EncodeTiled encode = encode_tiled();
   if (!encode) return false;
   struct Dim {
     cuuint64_t size, stride;
     cuuint32_t box;
     int name;
-  } d[2] = {{static_cast<cuuint64_t>(c.block), static_cast<cuuint64_t>(c.ss), static_cast<cuuint32_t>(c.block), 0},
+  } d[2] = {{static_cast<cuuint64_t>(c.block), static_cast<cuuint64_t>(c.ss), static_cast<cuuint32_t>(slots), 0},
             {static_cast<cuuint64_t>(c.num_blocks), static_cast<cuuint64_t>(c.sb), 1, 1}};
   if (d[1].size == 1) d[1].stride = std::max<cuuint64_t>(d[1].stride, d[0].size * d[0].stride);  // never stepped
   if (d[1].stride < d[0].stride) std::swap(d[0], d[1]);
@@ -135,7 +135,8 @@ int spec_latent_append(const spec_latent_cache* cache, const void* latents, int6
 size_t spec_latent_workspace_bytes(const spec_latent_cache* cache, int q_heads, int max_tokens) {
   Kv8Pool c;
   if (take_pool(cache, &c) != SPEC_OK || q_heads < 1 || max_tokens < 1) return 0;
-  return attn_layout(latent_attention_rows(static_cast<int64_t>(max_tokens) * q_heads), c.D).total;
+  const int rows = latent_attention_rows(static_cast<int64_t>(max_tokens) * q_heads);
+  return attn_layout(rows, rows == 128 && c.D > 256 ? c.D / 2 : c.D).total;
 }
 
 int spec_latent_attention(const spec_latent_cache* cache, const void* queries, int64_t q_stride_token, int64_t q_stride_head,
@@ -168,20 +169,30 @@ int spec_latent_attention(const spec_latent_cache* cache, const void* queries, i
   a.tree = tree_mask;
   a.scale = static_cast<float>(fabs(sm_scale * 1.4426950408889634));
   a.negate = sm_scale < 0.f;
+  if (a.scale == 0.f) a.scale = 1.f, a.negate = 2;  // scores of zeroed queries: a masked -infinity is not multiplied by 0
   a.row_status = row_status;
   const int64_t most = static_cast<int64_t>(std::min(max_tokens, std::max(T, 1))) * q_heads;  // no sequence has more than T
   const int rows = latent_attention_rows(static_cast<int64_t>(max_tokens) * q_heads);
   a.row_tiles = static_cast<int>((most + rows - 1) / rows);
   if (static_cast<int64_t>(a.row_tiles) * a.c.B >= (1LL << 31)) return SPEC_ERR_UNSUPPORTED;
-  a.parts = kSms;
-  const AttnLayout l = attn_layout(rows, a.c.D);
+  a.c.H = rows == 128 && a.c.D > 256 ? 2 : 1;
+  a.item_dims = a.c.D / a.c.H;
+  // In gangs where all sequences have as many items and the gangs fill the SMs.
+  a.gang = 0;
+  const int64_t items = static_cast<int64_t>(a.row_tiles) * a.c.H;
+  if (items > 1 && items <= kSms && static_cast<int64_t>(a.c.B) * max_tokens == T && kSms / items * items >= kSms * 7 / 8)
+    a.gang = static_cast<int>(items);
+  a.parts = a.gang ? kSms / a.gang * a.gang : kSms;
+  const AttnLayout l = attn_layout(rows, a.item_dims);
   char* ws = static_cast<char*>(workspace);
   a.gave_up = reinterpret_cast<int32_t*>(ws);
   a.cut = reinterpret_cast<int4*>(ws + l.cut);
   a.part_ml = reinterpret_cast<float2*>(ws + l.ml);
   a.part_o = reinterpret_cast<float*>(ws + l.o);
   CUtensorMap map;
-  if (!pool_map(a.c, a.rot, cache->dtype, &map, &a.order)) return SPEC_ERR_CUDA;
+  if (!pool_map(a.c, a.rot, cache->dtype, rows == 128 ? std::min(a.c.block, 64) : a.c.block, &map, &a.order))
+    return SPEC_ERR_CUDA;
+  if (rows == 128) return cuda_status(launch_latent_wide(a, cache->dtype, map, static_cast<cudaStream_t>(stream)));
   return cuda_status(launch_latent_attention(a, cache->dtype, rows, map, static_cast<cudaStream_t>(stream)));
 }
 

@@ -22,8 +22,7 @@
 // weights once the scores are there.
 #include <string.h>
 
-#include "kv8_attn.cuh"
-#include "latent.h"
+#include "latent_attn.cuh"
 
 namespace specv {
 
@@ -35,8 +34,6 @@ namespace {
 constexpr int kCost = 2;
 constexpr int kPiece = kTile * 256, kShared = kTile * 128;  // bytes: 128 dimensions of a tile, its shared dimensions
 constexpr int kMaxPieces = 6, kMaxShared = 2;
-constexpr float kUnset = -3.0e38f;  // the reference of a row that has seen nothing
-constexpr float kPass = 8.f;        // by how much (log2) scores may pass it
 
 template <int N_>
 struct LCfg {
@@ -65,38 +62,6 @@ struct LCfg {
   }
   static __host__ __device__ int shared(int pieces) { return room(pieces) - ring(pieces) * kPiece >= 2 * kShared ? 2 : 1; }
 };
-
-template <typename T>
-struct Bits;
-template <>
-struct Bits<__nv_bfloat16> {
-  static constexpr uint32_t kFormat = 1, kExp = 0x7f807f80u;
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-  }
-  static __device__ __forceinline__ float2 unpack(uint32_t w) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  }
-};
-template <>
-struct Bits<__half> {
-  static constexpr uint32_t kFormat = 0, kExp = 0x7c007c00u;
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-  }
-  static __device__ __forceinline__ float2 unpack(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
-};
-
-__device__ __forceinline__ void load_3d(uint32_t dst, const void* map, uint32_t bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
 
 // HN columns of the warp's lanes: 8, 16, 24 or 32.
 template <int HN>
@@ -170,9 +135,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   griddep_wait();
   Runs runs;
   Start start;
+  const int part_of_run = a.gang ? blockIdx.x / a.gang : blockIdx.x;
   fence_before();
-  const bool work = uniform(find_run<N, kCost>(a, blockIdx.x, &runs, &start, sm.tmp)) != 0;
-  const int64_t my_units = work ? runs.begin(blockIdx.x + 1) - runs.begin(blockIdx.x) : 0;
+  const bool work = uniform(find_items<N, kCost>(a, &runs, &start, sm.tmp)) != 0;
+  const int64_t my_units = work ? runs.begin(part_of_run + 1) - runs.begin(part_of_run) : 0;
   __syncthreads();
   fence_after();
   const uint32_t tmem = uniform(sm.tmem);
@@ -180,10 +146,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   uint32_t fill = 0, sh_fill = 0;  // ring slots that copies were begun into
   if (work && warp == kLoadWarp) {
     // ---- copies: a tile's pieces, then its shared dimensions
-    Walk<N, kCost> it(a, start, my_units);
+    Items<N, kCost> it(a, start, my_units);
     const int bs = a.c.block, ppt = kTile / bs;
     bool ok = true;
     do {
+      if (it.t0 >= it.t1) continue;
       const int pages = (it.r.end + bs - 1) / bs;
       const int32_t* table = a.c.table + static_cast<int64_t>(it.r.b) * a.c.max_blocks;
       auto page_id = [&](int page) {
@@ -235,11 +202,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const uint64_t e_desc = smem_desc(smem_addr(ring), 16, 1024, 2), s_desc = smem_desc(smem_addr(sh), 16, 1024, 2),
                    q_desc = smem_desc(smem_addr(q_smem), 16, 1024, 2), c_desc = smem_desc(smem_addr(ring), kTile * 128, 1024, 2),
                    p_desc = smem_desc(smem_addr(sh), kTile * 128, 1024, 2);
-    Walk<N, kCost> it(a, start, my_units);
+    Items<N, kCost> it(a, start, my_units);
     bool ok = true;
     uint32_t f = 0;  // pieces so far
     int i = 0, seg = 0;
     do {
+      if (it.t0 >= it.t1) continue;
       ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.q_full), seg & 1, gave_up));
       if (!ok) break;
       const int t0 = uniform(it.t0), t1 = uniform(it.t1);
@@ -251,8 +219,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.full[slot]), ((f + p) / NP) & 1, gave_up));
           if (!ok) break;
           fence_after();
+          const uint64_t ed = moved(e_desc, slot * kPiece), qd = moved(q_desc, 2 * p * N * 128);
           if (elect()) {
-            const uint64_t ed = e_desc + (slot * kPiece >> 4), qd = q_desc + (2 * p * N * 128 >> 4);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               mma_f16(tmem, ed + (k >> 2) * (kTile * 128 >> 4) + 2 * (k & 3), qd + (k >> 2) * (N * 128 >> 4) + 2 * (k & 3), id_s,
@@ -265,8 +233,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.sh_full[slot]), (i / NS) & 1, gave_up));
         if (!ok) break;
         fence_after();
+        const uint64_t ed = moved(s_desc, slot * kShared), qd = moved(q_desc, 2 * pieces * N * 128), pd = moved(p_desc, slot * kShared);
         if (elect()) {
-          const uint64_t ed = s_desc + (slot * kShared >> 4), qd = q_desc + (2 * pieces * N * 128 >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma_f16(tmem, ed + 2 * k, qd + 2 * k, id_s, true);
           commit(smem_addr(&sm.s_full));
@@ -278,10 +246,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll 1
         for (int p = 0; p < pieces; ++p) {
           const uint32_t from = uniform((f + p) % NP);
+          const uint64_t cd = moved(c_desc, from * kPiece);
+          const uint32_t to = uniform(tmem + C::kO + 64 * p);
           if (elect()) {
-            const uint64_t cd = c_desc + (from * kPiece >> 4), pd = p_desc + (slot * kShared >> 4);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) mma_f16(tmem + C::kO + 64 * p, cd + 128 * k, pd + 128 * k, id_o, t > t0 || k > 0);
+            for (int k = 0; k < 8; ++k) mma_f16(to, cd + 128 * k, pd + 128 * k, id_o, t > t0 || k > 0);
             commit(smem_addr(&sm.empty[from]));
           }
           __syncwarp();
@@ -302,7 +271,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const bool vec_q = ((reinterpret_cast<uintptr_t>(a.q) | (a.qst * 2) | (a.qsh * 2)) & 15) == 0;
     const bool vec_o = ((reinterpret_cast<uintptr_t>(a.out) | (a.ost * 2) | (a.osh * 2)) & 3) == 0;
     const int chunks = dims / 8 + 8, used = (dims + a.rot) / 8;  // 16-byte chunks of a row of queries, of an entry
-    Walk<N, kCost> it(a, start, my_units);
+    Items<N, kCost> it(a, start, my_units);
 
     // The item's queries into shared memory. The products that read the last item's are over.
     auto load_queries = [&]() {
@@ -315,7 +284,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         for (int k = 0; k < 6; ++k) {
           const int c = c0 + k * C::kSoft, row = c / chunks, d = c - row * chunks;
           u[k] = make_uint4(0, 0, 0, 0);
-          if (c < all && row < r.rows && d < used) {
+          if (c < all && row < r.rows && d < used && a.negate < 2) {
             const uint32_t flat = static_cast<uint32_t>(r.rt * N + row), tok = flat / static_cast<uint32_t>(a.group);
             const QT* q = static_cast<const QT*>(a.q) + (r.first + static_cast<int64_t>(tok)) * a.qst +
                           static_cast<int>(flat - tok * a.group) * a.qsh + 8 * d;
@@ -333,7 +302,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         for (int k = 0; k < 6; ++k) {
           const int c = c0 + k * C::kSoft, row = c / chunks, d = c - row * chunks;
           if (c >= all) continue;
-          if (a.negate) u[k].x ^= 0x80008000u, u[k].y ^= 0x80008000u, u[k].z ^= 0x80008000u, u[k].w ^= 0x80008000u;
+          if (a.negate == 1) u[k].x ^= 0x80008000u, u[k].y ^= 0x80008000u, u[k].z ^= 0x80008000u, u[k].w ^= 0x80008000u;
           *reinterpret_cast<uint4*>(q_smem + (d >> 3) * (N * 128) + row * 128 + (((d & 7) ^ (row & 7)) << 4)) = u[k];
         }
       }
@@ -341,10 +310,17 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(smem_addr(&sm.q_full));
     };
-    load_queries();
+    auto next_item = [&]() {  // that has a tile
+      bool more;
+      while ((more = it.next(a)) && it.t0 >= it.t1) {
+      }
+      return more;
+    };
     int i = 0;
     uint32_t f = 0;  // pieces so far
-    bool more = true;
+    int4 cut = make_int4(0, 0, 0, 0);  // the last item's
+    bool more = it.t0 < it.t1 || next_item();
+    if (more) load_queries();
     for (int seg = 0; more; ++seg) {
       const RowTile r = it.r;
       const int t0 = uniform(it.t0), t1 = uniform(it.t1), r0 = r.rt * N + half * HN;  // r0: the thread's first row
@@ -411,6 +387,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           __syncwarp();
         }
         wait_ld();
+        settle<HN>(x);
         float y[HN];  // scores over the reference
         bool pass = t == t0;
         float top = kNegInf;
@@ -465,6 +442,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               uint32_t o[HN];
               ld_cols<HN>(lanes + C::kO + 64 * p, o);
               wait_ld();
+              settle<HN>(o);
 #pragma unroll
               for (int j = 0; j < HN; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fac[j]);
               st_cols<HN>(lanes + C::kO + 64 * p, o);
@@ -494,10 +472,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 
       // ---- the next item's queries, then this one's results or its share of them
       const bool whole = t0 == 0 && t1 == r.tiles;
-      const int h = it.h;
-      more = it.next(a);
+      cut = it.cut(a, runs);
+      more = next_item();
       if (more) load_queries();
-      else if (tid == 0) a.cut[blockIdx.x] = cut_item<N>(runs, blockIdx.x, r, h, t0, t1);
       const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (t0 > 0 ? 0 : 1);
       {
         const float s = sums_of<HN>(l, lane);
@@ -530,9 +507,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       __syncwarp();
 #pragma unroll 1
       for (int p = 0; p < pieces; ++p) {
+        __syncwarp();
         uint32_t x[HN];
         ld_cols<HN>(lanes + C::kO + 64 * p, x);
         wait_ld();
+        settle<HN>(x);
         int tok = r0 / a.group, sub = r0 - tok * a.group;
         if (!whole) {
           float* o = a.part_o + (part * N + half * HN) * dims + 128 * p + own;
@@ -560,6 +539,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       fence_before();
     }
+    if (tid == 0) a.cut[blockIdx.x] = cut;
   }
 
   fence_before();
@@ -594,121 +574,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   griddep_launch_dependents();
 }
 
-// -------------------------------------------------------------------- join --
-//
-// As kv8_join_kernel, for rows of up to 512 dimensions: block x adds the shares of the item that begins in part x and ends
-// behind it, a warp one row at a time; the last blocks check sequences, and make the rows NaN that see an entry of a page
-// outside the pool.
-
-template <typename QT, int N>
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_constant__ LatentAttnArgs a) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = a.c.D;
-  griddep_launch_dependents();
-  griddep_wait();
-  if (blockIdx.x >= static_cast<unsigned>(a.parts)) {  // a warp per sequence: row_status
-    const int b = (blockIdx.x - a.parts) * (kJoinThreads / 32) + warp;
-    if (blockIdx.y > 0 || b >= a.c.B) return;
-    bool late = false;
-    for (int i = lane; i < a.parts; i += 32) late |= (a.gave_up[i] & kGaveUp) != 0;
-    const int lo = a.cu[b], hi = a.cu[b + 1], len = a.c.len[b];
-    const bool sound = kv8_seq_ok(a.c, a.T, lo, hi, len) && hi - lo <= a.max_tokens;
-    bool bad = !sound;
-    if (sound && hi > lo) {
-      const int pages = (len + (hi - lo) + a.c.block - 1) / a.c.block;
-      for (int j = lane; j < pages; j += 32) {
-        const int id = a.c.table[static_cast<int64_t>(b) * a.c.max_blocks + j];
-        bad |= id < 0 || id >= a.c.num_blocks;
-      }
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    late = __any_sync(0xffffffffu, late);
-    if (lane == 0) a.row_status[b] = (bad ? SPEC_ROW_CACHE : 0) | (late ? SPEC_ROW_TIMEOUT : 0);
-    if (bad && lo >= 0 && hi > lo && hi <= a.T) {
-#pragma unroll 1
-      for (int t = lo; t < hi; ++t) {
-        if (sound && !sees_outside(a, b, len, hi - lo, t - lo)) continue;
-#pragma unroll 1
-        for (int h = 0; h < a.q_heads; ++h)
-          for (int d = lane; d < C; d += 32)
-            static_cast<QT*>(a.out)[t * a.ost + h * a.osh + d] = from_f<QT>(__int_as_float(0x7fffffff));
-      }
-    }
-    return;
-  }
-  const int4 item = a.cut[blockIdx.x];
-  const int n = item.w;
-  if (n == 0) return;
-  const RowTile r = row_tile<N>(a, item.x, item.y);
-  const int64_t first = blockIdx.x;
-  bool outside = false;
-  for (int i = lane; i < n; i += 32) outside |= (a.gave_up[first + i] & kOutside) != 0;
-  outside = __any_sync(0xffffffffu, outside);
-#pragma unroll 1
-  for (int row = blockIdx.y * (kJoinThreads / 32) + warp; row < r.rows; row += gridDim.y * (kJoinThreads / 32)) {
-    auto share = [&](int i) { return (2 * (first + i) + (i == 0 ? 1 : 0)) * N + row; };
-    float top = kNegInf;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, a.part_ml[share(i)].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float4 acc[4] = {};
-    float sum = 0.f;
-#pragma unroll 2
-    for (int i = 0; i < n; ++i) {
-      const float2 ml = a.part_ml[share(i)];
-      const float* p = a.part_o + share(i) * C + 4 * lane;
-      const float w = ml.x == top ? 1.f : ex2_fast(ml.x - top);
-      sum = fmaf(w, ml.y, sum);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (128 * k >= C) break;
-        const float4 u = *reinterpret_cast<const float4*>(p + 128 * k);
-        acc[k].x = fmaf(w, u.x, acc[k].x), acc[k].y = fmaf(w, u.y, acc[k].y);
-        acc[k].z = fmaf(w, u.z, acc[k].z), acc[k].w = fmaf(w, u.w, acc[k].w);
-      }
-    }
-    const int item_row = item.y * N + row, tok = item_row / a.group;
-    QT* out = static_cast<QT*>(a.out) + (r.first + static_cast<int64_t>(tok)) * a.ost + (item_row - tok * a.group) * a.osh + 4 * lane;
-    float inv = sum == 0.f ? 0.f : 1.f / sum;
-    if (outside && sees_outside(a, item.x, r.ctx, r.n, tok)) inv = __int_as_float(0x7fffffff);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (128 * k >= C) break;
-      out[128 * k] = from_f<QT>(acc[k].x * inv), out[128 * k + 1] = from_f<QT>(acc[k].y * inv);
-      out[128 * k + 2] = from_f<QT>(acc[k].z * inv), out[128 * k + 3] = from_f<QT>(acc[k].w * inv);
-    }
-  }
-}
-
-template <typename QT, int N>
-cudaError_t launch_latent_join(const LatentAttnArgs& a, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(a.max_tokens) * a.group;
-  const int y = static_cast<int>((rows < N ? rows : N) + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-  const int checks = (a.c.B + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-  return launch_pdl(latent_join_kernel<QT, N>, dim3(static_cast<unsigned>(a.parts + checks), static_cast<unsigned>(y)),
-                    dim3(kJoinThreads), st, a);
-}
-
 // ------------------------------------------------------------------ launch --
 
 template <typename QT, int N>
 cudaError_t launch_attention(const LatentAttnArgs& a, const CUtensorMap& map, cudaStream_t st) {
   using C = LCfg<N>;
-  auto kernel = latent_attention_kernel<QT, C>;
-  constexpr int smem = C::kBudget + 1024;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.parts));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, a, map);
-  return e != cudaSuccess ? e : launch_latent_join<QT, N>(a, st);
+  return launch_items<QT, N>(latent_attention_kernel<QT, C>, a, C::kThreads, C::kBudget + 1024, map, st);
 }
 
 template <typename QT>
@@ -721,7 +592,11 @@ cudaError_t launch_rows(const LatentAttnArgs& a, int rows, const CUtensorMap& ma
 
 }  // namespace
 
-int latent_attention_rows(int64_t max_rows) { return max_rows > 48 ? 64 : static_cast<int>((max_rows + 15) / 16 * 16); }
+// Rows of an item, by the most rows that a sequence can have.
+int latent_attention_rows(int64_t max_rows) {
+  if (max_rows > 64) return 128;
+  return max_rows > 48 ? 64 : static_cast<int>((max_rows + 15) / 16 * 16);
+}
 
 cudaError_t launch_latent_attention(const LatentAttnArgs& a, int dtype, int rows, const CUtensorMap& map, cudaStream_t st) {
   return dtype == SPEC_BF16 ? launch_rows<__nv_bfloat16>(a, rows, map, st) : launch_rows<__half>(a, rows, map, st);
