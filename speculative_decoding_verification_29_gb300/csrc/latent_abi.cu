@@ -192,7 +192,6 @@ int spec_latent_attention(const spec_latent_cache* cache, const void* queries, i
   CUtensorMap map;
   if (!pool_map(a.c, a.rot, cache->dtype, rows == 128 ? std::min(a.c.block, 64) : a.c.block, &map, &a.order))
     return SPEC_ERR_CUDA;
-  if (rows == 128) return cuda_status(launch_latent_wide(a, cache->dtype, map, static_cast<cudaStream_t>(stream)));
   return cuda_status(launch_latent_attention(a, cache->dtype, rows, map, static_cast<cudaStream_t>(stream)));
 }
 

@@ -16,7 +16,7 @@ template <typename T>
 struct Bits;
 template <>
 struct Bits<__nv_bfloat16> {
-  static constexpr uint32_t kFormat = 1, kExp = 0x7f807f80u;
+  static constexpr uint32_t kFormat = 1, kExp = 0x7f807f80u, kStep = 0x00800080u;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -28,7 +28,7 @@ struct Bits<__nv_bfloat16> {
 };
 template <>
 struct Bits<__half> {
-  static constexpr uint32_t kFormat = 0, kExp = 0x7c007c00u;
+  static constexpr uint32_t kFormat = 0, kExp = 0x7c007c00u, kStep = 0x04000400u;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -36,6 +36,27 @@ struct Bits<__half> {
   }
   static __device__ __forceinline__ float2 unpack(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 };
+
+// Clears a slot's chunks of 16 bytes in shared memory where the slot lies behind the rows' last; else only the elements that
+// are not finite. True where it met such a one. An exponent of ones carries into the sign's place.
+template <typename B, int CHUNKS>
+__device__ __forceinline__ bool clean_chunks(uint4* row, bool behind) {
+  uint32_t hit = 0;
+#pragma unroll
+  for (int k = 0; k < CHUNKS; ++k) {
+    if (behind) {
+      row[k] = make_uint4(0, 0, 0, 0);
+    } else {
+      const uint4 u = row[k];
+      hit |= ((u.x & B::kExp) + B::kStep) | ((u.y & B::kExp) + B::kStep) | ((u.z & B::kExp) + B::kStep) | ((u.w & B::kExp) + B::kStep);
+    }
+  }
+  if (!(hit & 0x80008000u)) return false;
+  uint32_t* w = reinterpret_cast<uint32_t*>(row);
+#pragma unroll 1
+  for (int k = 0; k < 4 * CHUNKS; ++k) w[k] &= ~__vcmpeq2(w[k] & B::kExp, B::kExp);
+  return true;
+}
 
 // A descriptor of smem_desc's, its address moved by `bytes`; the sum is known to be the warp's, so that it stays in uniform
 // registers and an issue takes few instructions (see tc.cuh).

@@ -25,7 +25,7 @@ namespace specv {
 namespace {
 
 // Units of an item beside its tiles (see Runs): its queries and results.
-constexpr int kCost = 2;
+constexpr int kCost = 4;
 constexpr int kRows = 128, kSlots = 64;  // rows of an item, slots of a tile
 constexpr int kChunk = kSlots * 128, kQChunk = kRows * 128;  // bytes of 64 dimensions of a tile, of the queries
 constexpr int kPieces = 4, kShared = 2;  // ring: two tiles' pieces and shared dimensions
@@ -284,27 +284,35 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         return u;
       };
       fence_after();
+      // 16 or 24 loads are in flight at once
+      constexpr int kBatch = vd / 8 % 16 == 0 ? 16 : 24;
 #pragma unroll 1
-      for (int c = 0; c < vd / 8; c += 8) {
-        uint32_t w[32];
+      for (int c = 0; c < vd / 8; c += kBatch) {
+        uint32_t w[4 * kBatch];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kBatch; ++k) {
           const uint4 u = load(it.h * (vd / 8) + c + k);
           w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
         }
         const uint32_t to = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kQAt + 4 * c;
-        tmem_st16(to, w);
-        tmem_st16(to + 16, w + 16);
+#pragma unroll
+        for (int k = 0; k < kBatch / 4; ++k) tmem_st16(to + 16 * k, w + 16 * k);
       }
 #pragma unroll 1
-      for (int c = 0; c < (halves - 1) * pc + 1; ++c) {
-        const int from = c < (halves - 1) * pc ? (1 - it.h) * (vd / 8) + 8 * c : dims / 8;
-        uint4 u[8];
+      for (int c = 0; c < (halves - 1) * pc + 1; c += 2) {
+        uint4 u[16];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) u[k] = load(from + k);
-        uint8_t* to = q_smem + c * kQChunk + own * 128;
+        for (int k = 0; k < 16; ++k) {
+          const int chunk = c + (k >> 3);
+          if (chunk < (halves - 1) * pc) u[k] = load((1 - it.h) * (vd / 8) + 8 * chunk + (k & 7));
+          else if (chunk == (halves - 1) * pc) u[k] = load(dims / 8 + (k & 7));
+        }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(to + ((k ^ (own & 7)) << 4)) = u[k];
+        for (int k = 0; k < 16; ++k) {
+          const int chunk = c + (k >> 3);
+          if (chunk <= (halves - 1) * pc)
+            *reinterpret_cast<uint4*>(q_smem + chunk * kQChunk + own * 128 + (((k & 7) ^ (own & 7)) << 4)) = u[k];
+        }
       }
       wait_st();
       fence_async_shared();
@@ -345,26 +353,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const uint32_t value = static_cast<uint32_t>(i) * halves + halves - 1;
           ok = bar_wait(smem_addr(&sm.full[value % kPieces]), (value / kPieces) & 1, gave_up) && ok;
           uint8_t* row = ring + (value % kPieces) * piece + in * 128;
+          if (slot >= r.ctx) {  // every row sees those before
 #pragma unroll 1
-          for (int c = own >> 6; c < pc; c += 2)
-#pragma unroll 4
-            for (int k = 0; k < 8; ++k) {
-              uint4* e = reinterpret_cast<uint4*>(row + c * kChunk) + k;
-              if (slot >= r.end) {
-                *e = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              uint4 u = *e;
-              uint32_t* w = &u.x;
-              uint32_t any = 0;
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const uint32_t bad = __vcmpeq2(w[z] & B::kExp, B::kExp);
-                any |= bad;
-                w[z] &= ~bad;
-              }
-              if (any) *e = u, sm.odd[seg & 1] = seg + 1;
-            }
+            for (int c = own >> 6; c < pc; c += 2)
+              if (clean_chunks<B, 8>(reinterpret_cast<uint4*>(row + c * kChunk), slot >= r.end)) sm.odd[seg & 1] = seg + 1;
+          }
           __syncwarp();
         }
         wait_ld();
