@@ -37,6 +37,29 @@ struct Bits<__half> {
   static __device__ __forceinline__ float2 unpack(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 };
 
+// 16 bytes from global to shared memory, asynchronously; zeros where `take` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Four lanes hold four rows' 16-byte units u[0 .. 3]; afterwards lane l of them holds unit l of each row, so that four lanes
+// store 64 bytes of a row together.
+__device__ __forceinline__ void turn_units(uint4* u, int lane) {
+  auto swap = [&](uint4& a, uint4& b, int bit) {  // the lane without the bit gives b for the other's a
+    const bool up = lane & bit;
+    uint4 v = up ? a : b;
+    v.x = __shfl_xor_sync(0xffffffffu, v.x, bit), v.y = __shfl_xor_sync(0xffffffffu, v.y, bit);
+    v.z = __shfl_xor_sync(0xffffffffu, v.z, bit), v.w = __shfl_xor_sync(0xffffffffu, v.w, bit);
+    if (up) a = v;
+    else b = v;
+  };
+  swap(u[0], u[1], 1);
+  swap(u[2], u[3], 1);
+  swap(u[0], u[2], 2);
+  swap(u[1], u[3], 2);
+}
+
 // Clears a slot's chunks of 16 bytes in shared memory where the slot lies behind the rows' last; else only the elements that
 // are not finite. True where it met such a one. An exponent of ones carries into the sign's place.
 template <typename B, int CHUNKS>

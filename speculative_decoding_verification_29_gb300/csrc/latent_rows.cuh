@@ -274,41 +274,34 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const bool vec_o = ((reinterpret_cast<uintptr_t>(a.out) | (a.ost * 2) | (a.osh * 2)) & 3) == 0;
     constexpr int chunks = dims / 8 + 8;
     const int used = (dims + a.rot) / 8;  // 16-byte chunks of a row of queries, of an entry
+    const float scale = a.negate == 1 ? -a.scale : a.scale;
     Items<N, kCost> it(a, start, my_units);
 
     // The item's queries into shared memory. The products that read the last item's are over.
     auto load_queries = [&]() {
       const RowTile& r = it.r;
-      constexpr int all = N * chunks, kLoads = (all + C::kSoft - 1) / C::kSoft, kBatch = kLoads > 18 ? 9 : kLoads;
 #pragma unroll 1
-      for (int c0 = tid; c0 < all; c0 += kBatch * C::kSoft) {
-        uint4 u[kBatch];
+      for (int c = tid; c < N * chunks; c += C::kSoft) {
+        const int row = c / chunks, d = c - row * chunks;
+        const uint32_t flat = static_cast<uint32_t>(r.rt * N + row), tok = flat / static_cast<uint32_t>(a.group);
+        const QT* q = static_cast<const QT*>(a.q) + (r.first + static_cast<int64_t>(tok)) * a.qst +
+                      static_cast<int>(flat - tok * a.group) * a.qsh + 8 * d;
+        const bool take = row < r.rows && d < used && a.negate < 2;
+        uint8_t* to = q_smem + (d >> 3) * (N * 128) + row * 128 + (((d & 7) ^ (row & 7)) << 4);
+        if (vec_q) {
+          copy16(smem_addr(to), take ? q : static_cast<const QT*>(a.q), take);
+        } else {
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (take) {
+            QT e[8];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int c = c0 + k * C::kSoft, row = c / chunks, d = c - row * chunks;
-          u[k] = make_uint4(0, 0, 0, 0);
-          if (c < all && row < r.rows && d < used && a.negate < 2) {
-            const uint32_t flat = static_cast<uint32_t>(r.rt * N + row), tok = flat / static_cast<uint32_t>(a.group);
-            const QT* q = static_cast<const QT*>(a.q) + (r.first + static_cast<int64_t>(tok)) * a.qst +
-                          static_cast<int>(flat - tok * a.group) * a.qsh + 8 * d;
-            if (vec_q) {
-              u[k] = *reinterpret_cast<const uint4*>(q);
-            } else {
-              QT e[8];
-#pragma unroll
-              for (int x = 0; x < 8; ++x) e[x] = q[x];
-              memcpy(&u[k], e, 16);
-            }
+            for (int x = 0; x < 8; ++x) e[x] = q[x];
+            memcpy(&u, e, 16);
           }
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int c = c0 + k * C::kSoft, row = c / chunks, d = c - row * chunks;
-          if (c >= all) continue;
-          if (a.negate == 1) u[k].x ^= 0x80008000u, u[k].y ^= 0x80008000u, u[k].z ^= 0x80008000u, u[k].w ^= 0x80008000u;
-          *reinterpret_cast<uint4*>(q_smem + (d >> 3) * (N * 128) + row * 128 + (((d & 7) ^ (row & 7)) << 4)) = u[k];
+          *reinterpret_cast<uint4*>(to) = u;
         }
       }
+      copies_done();
       fence_async_shared();
       __syncwarp();
       if (lane == 0) bar_arrive(smem_addr(&sm.q_full));
@@ -384,7 +377,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < HN; j += 4) {
           const float4 ref = t == t0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(&sm.ref[group * HN + j]);
-          const float2 sc = make_float2(a.scale, a.scale);
+          const float2 sc = make_float2(scale, scale);
           const float2 u = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), sc, make_float2(-ref.x, -ref.y));
           const float2 v = fma2(make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), sc, make_float2(-ref.z, -ref.w));
           y[j] = u.x, y[j + 1] = u.y, y[j + 2] = v.x, y[j + 3] = v.y;
@@ -404,7 +397,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           }
           // the rows' largest scores: over the lanes, then over the four warps; references move, sums and results follow
 #pragma unroll
-          for (int j = 0; j < HN; ++j) y[j] = (vis >> j) & 1 ? __uint_as_float(x[j]) * a.scale : kNegInf;
+          for (int j = 0; j < HN; ++j) y[j] = (vis >> j) & 1 ? __uint_as_float(x[j]) * scale : kNegInf;
           float mine = kNegInf;
 #pragma unroll
           for (int j = 0; j < HN; ++j) {

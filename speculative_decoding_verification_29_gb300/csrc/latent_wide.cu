@@ -261,16 +261,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     do {
       const RowTile& r = it.r;
       if (it.t0 >= it.t1) continue;
-      if (seg > 0) ok = bar_wait(smem_addr(&sm.q_free), (seg - 1) & 1, gave_up);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
       const uint32_t flat = static_cast<uint32_t>(r.rt * kRows + min(own, r.rows - 1)), tok = flat / static_cast<uint32_t>(a.group);
       const QT* q = static_cast<const QT*>(a.q) + (r.first + static_cast<int64_t>(tok)) * a.qst +
                     static_cast<int>(flat - tok * a.group) * a.qsh;
-      const uint32_t flip = a.negate == 1 ? 0x80008000u : 0u;
+      const bool mine = own < r.rows && a.negate < 2;
       auto load = [&](int c) {
         uint4 u = make_uint4(0, 0, 0, 0);
-        if (own < r.rows && c < used && a.negate < 2) {
+        if (mine && c < used) {
           if (vec) {
             u = *reinterpret_cast<const uint4*>(q + 8 * c);
           } else {
@@ -280,40 +277,41 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             memcpy(&u, e, 16);
           }
         }
-        u.x ^= flip, u.y ^= flip, u.z ^= flip, u.w ^= flip;
         return u;
       };
+      // The item's value dimensions are fetched while the last item's queries are still in use, the rest is brought to L2.
+      uint32_t w[vd / 2];
+#pragma unroll
+      for (int k = 0; k < vd / 8; ++k) {
+        const uint4 u = load(it.h * (vd / 8) + k);
+        w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
+      }
+      if (halves == 2 && seg > 0)
+#pragma unroll
+        for (int k = 0; k < vd; k += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + (1 - it.h) * vd + k));
+      if (seg > 0) ok = bar_wait(smem_addr(&sm.q_free), (seg - 1) & 1, gave_up);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
       fence_after();
-      // 16 or 24 loads are in flight at once
-      constexpr int kBatch = vd / 8 % 16 == 0 ? 16 : 24;
 #pragma unroll 1
-      for (int c = 0; c < vd / 8; c += kBatch) {
-        uint32_t w[4 * kBatch];
+      for (int c = 0; c < (halves - 1) * pc + 1; ++c) {
+        const int from = c < (halves - 1) * pc ? (1 - it.h) * (vd / 8) + 8 * c : dims / 8;
+        uint8_t* to = q_smem + c * kQChunk + own * 128;
+        if (vec) {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const uint4 u = load(it.h * (vd / 8) + c + k);
-          w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
-        }
-        const uint32_t to = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kQAt + 4 * c;
-#pragma unroll
-        for (int k = 0; k < kBatch / 4; ++k) tmem_st16(to + 16 * k, w + 16 * k);
-      }
+          for (int k = 0; k < 8; ++k) {
+            const bool take = mine && from + k < used;
+            copy16(smem_addr(to + ((k ^ (own & 7)) << 4)), take ? q + 8 * (from + k) : q, take);
+          }
+        } else {
 #pragma unroll 1
-      for (int c = 0; c < (halves - 1) * pc + 1; c += 2) {
-        uint4 u[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int chunk = c + (k >> 3);
-          if (chunk < (halves - 1) * pc) u[k] = load((1 - it.h) * (vd / 8) + 8 * chunk + (k & 7));
-          else if (chunk == (halves - 1) * pc) u[k] = load(dims / 8 + (k & 7));
-        }
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int chunk = c + (k >> 3);
-          if (chunk <= (halves - 1) * pc)
-            *reinterpret_cast<uint4*>(q_smem + chunk * kQChunk + own * 128 + (((k & 7) ^ (own & 7)) << 4)) = u[k];
+          for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(to + ((k ^ (own & 7)) << 4)) = load(from + k);
         }
       }
+      const uint32_t q_to = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kQAt;
+#pragma unroll
+      for (int k = 0; k < vd / 2; k += 16) tmem_st16(q_to + k, w + k);
+      copies_done();
       wait_st();
       fence_async_shared();
       fence_before();
@@ -362,6 +360,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         wait_ld();
         settle<64>(x);
+        if (a.negate == 1) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) x[k] ^= 0x80000000u;
+        }
         if (masked) {
           const int from = s * kSlots - r.ctx;  // token of the step in the tile's first slot
           uint64_t vis;
@@ -450,33 +452,55 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       if (!whole && own < r.rows) a.part_ml[part * kRows + own] = make_float2(ref, sum);
+      int64_t at[4];  // of the rows that the lane stores a part of: results, or shares in the workspace
+      uint32_t here = 0;
+      {
+        const int64_t to = whole ? (r.first + static_cast<int64_t>(tok)) * a.ost + head * a.osh + h * vd : (part * kRows + own) * vd;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          at[k] = __shfl_sync(0xffffffffu, to, (lane & ~3) + k);
+          here |= ((own & ~3) + k < r.rows ? 1u : 0u) << k;
+        }
+      }
 #pragma unroll 1
       for (int c = 0; c < vd; c += 32) {
         uint32_t x[32];
         tmem_ld<32>(lanes + c, x);
         wait_ld();
         settle<32>(x);
-        if (own < r.rows && !whole) {
-          float4* o = reinterpret_cast<float4*>(a.part_o + (part * kRows + own) * vd + c);
+        if (!whole) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            o[k] = make_float4(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]), __uint_as_float(x[4 * k + 2]),
-                               __uint_as_float(x[4 * k + 3]));
-        } else if (own < r.rows) {
-          QT* o = static_cast<QT*>(a.out) + (r.first + static_cast<int64_t>(tok)) * a.ost + head * a.osh + h * vd + c;
+          for (int g = 0; g < 32; g += 16) {
+            uint4 u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[k] = make_uint4(x[g + 4 * k], x[g + 4 * k + 1], x[g + 4 * k + 2], x[g + 4 * k + 3]);
+            turn_units(u, lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if ((here >> k) & 1) *reinterpret_cast<uint4*>(a.part_o + at[k] + c + g + 4 * (lane & 3)) = u[k];
+          }
+        } else {
+          uint4 u[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t w[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z)
               w[z] = B::pack(__uint_as_float(x[8 * k + 2 * z]) * inv, __uint_as_float(x[8 * k + 2 * z + 1]) * inv);
+            u[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          turn_units(u, lane);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (!((here >> k) & 1)) continue;
+            QT* o = static_cast<QT*>(a.out) + at[k] + c + 8 * (lane & 3);
             if (vec) {
-              reinterpret_cast<uint4*>(o)[k] = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(o) = u[k];
             } else {
               QT e[8];
-              memcpy(e, w, 16);
+              memcpy(e, &u[k], 16);
 #pragma unroll
-              for (int z = 0; z < 8; ++z) o[8 * k + z] = e[z];
+              for (int z = 0; z < 8; ++z) o[z] = e[z];
             }
           }
         }
