@@ -52,7 +52,7 @@ cudaError_t launch_latent_compact(const LatentCompactArgs& a, cudaStream_t st);
 struct LatentAttnArgs : Kv8AttnArgs {
   int rot, item_dims, gang;
 };
-int latent_attention_rows(int64_t max_rows);
+int latent_attention_rows(int64_t max_rows, int dims);
 cudaError_t launch_latent_rows_f16(const LatentAttnArgs& a, int rows, const CUtensorMap& pool, cudaStream_t st);
 cudaError_t launch_latent_wide(const LatentAttnArgs& a, int dtype, const CUtensorMap& pool, cudaStream_t st);
 cudaError_t launch_latent_attention(const LatentAttnArgs& a, int dtype, int rows, const CUtensorMap& pool, cudaStream_t st);

@@ -135,7 +135,7 @@ int spec_latent_append(const spec_latent_cache* cache, const void* latents, int6
 size_t spec_latent_workspace_bytes(const spec_latent_cache* cache, int q_heads, int max_tokens) {
   Kv8Pool c;
   if (take_pool(cache, &c) != SPEC_OK || q_heads < 1 || max_tokens < 1) return 0;
-  const int rows = latent_attention_rows(static_cast<int64_t>(max_tokens) * q_heads);
+  const int rows = latent_attention_rows(static_cast<int64_t>(max_tokens) * q_heads, c.D);
   return attn_layout(rows, rows == 128 && c.D > 256 ? c.D / 2 : c.D).total;
 }
 
@@ -172,7 +172,7 @@ int spec_latent_attention(const spec_latent_cache* cache, const void* queries, i
   if (a.scale == 0.f) a.scale = 1.f, a.negate = 2;  // scores of zeroed queries: a masked -infinity is not multiplied by 0
   a.row_status = row_status;
   const int64_t most = static_cast<int64_t>(std::min(max_tokens, std::max(T, 1))) * q_heads;  // no sequence has more than T
-  const int rows = latent_attention_rows(static_cast<int64_t>(max_tokens) * q_heads);
+  const int rows = latent_attention_rows(static_cast<int64_t>(max_tokens) * q_heads, a.c.D);
   a.row_tiles = static_cast<int>((most + rows - 1) / rows);
   if (static_cast<int64_t>(a.row_tiles) * a.c.B >= (1LL << 31)) return SPEC_ERR_UNSUPPORTED;
   a.c.H = rows == 128 && a.c.D > 256 ? 2 : 1;

@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       bool ok = true;
 #pragma unroll 1
       for (int t = t0; t < t1; ++t, ++i, f += pieces) {
-        ok = bar_wait(smem_addr(&sm.s_full), i & 1, gave_up);
+        ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.s_full), i & 1, gave_up));
         fence_after();
         uint32_t x[HN];
         ld_cols<HN>(lanes, x);

@@ -339,7 +339,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       bool ok = true;
 #pragma unroll 1
       for (int s = s0; s < s1; ++s, ++i) {
-        ok = bar_wait(smem_addr(&sm.s_full[i & 1]), (i >> 1) & 1, gave_up);
+        ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.s_full[i & 1]), (i >> 1) & 1, gave_up));
+        if (!ok) break;
         fence_after();
         const uint32_t at = lanes + kSAt + (i & 1) * kSlots;
         uint32_t x[64];
@@ -349,7 +350,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           // As in latent_attn.cu: slots behind the rows' last, and values that are not finite, are cleared. Two threads a slot.
           const int in = own & 63, slot = s * kSlots + in;
           const uint32_t value = static_cast<uint32_t>(i) * halves + halves - 1;
-          ok = bar_wait(smem_addr(&sm.full[value % kPieces]), (value / kPieces) & 1, gave_up) && ok;
+          ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.full[value % kPieces]), (value / kPieces) & 1, gave_up));
+          if (!ok) break;
           uint8_t* row = ring + (value % kPieces) * piece + in * 128;
           if (slot >= r.ctx) {  // every row sees those before
 #pragma unroll 1
@@ -396,7 +398,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           ref = now;
           sum *= by;
           if (s > s0) {
-            bar_wait(smem_addr(&sm.pv_done[(i - 1) & 1]), ((i - 1) >> 1) & 1, gave_up);
+            ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.pv_done[(i - 1) & 1]), ((i - 1) >> 1) & 1, gave_up));
+            if (!ok) break;
             fence_after();
 #pragma unroll 1
             for (int c = 0; c < vd; c += 32) {
