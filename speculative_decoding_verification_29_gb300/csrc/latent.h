@@ -22,7 +22,7 @@ struct LatentAppendArgs {
   void* qo;
   int64_t xst, rst, qst, qsh, ost, osh;  // strides in elements
   int T, q_heads;
-  int vec_x, vec_q;  // rows on 16-byte boundaries
+  int vec_x, vec_q, vec_w;  // rows on 16-byte boundaries
   int w_fp32;
   float eps;
   const int32_t* cu;

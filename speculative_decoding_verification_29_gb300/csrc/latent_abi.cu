@@ -115,6 +115,7 @@ int spec_latent_append(const spec_latent_cache* cache, const void* latents, int6
   a.vec_x = vec16(latents, l_stride_token, 0, size);
   a.w = norm_weight;
   a.w_fp32 = norm_dtype == SPEC_F32;
+  a.vec_w = on16(norm_weight);
   a.eps = eps;
   a.q = queries;
   a.qst = q_stride_token;
