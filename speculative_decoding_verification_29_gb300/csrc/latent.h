@@ -77,7 +77,8 @@ struct PagesArgs {
   int32_t *sharers, *last_sharer;  // [num_blocks]: sequences that go on writing a partly filled block, the last of them
   int32_t* unsound;                // [B][chunks]: bad ids among a row's kept blocks
   int32_t* free_ids;               // [num_blocks]
-  int2* take;                      // [B]: rank of the first block taken, blocks
+  int4* take;                      // [2 B]: rank of the first block taken, blocks, first place in the row, block copied;
+                                   // tokens kept, whether unsound, whether it asks for room, whether that passes the table
   int2* copies;                    // [B]: source and destination
   int32_t* n_copies;               // [1]
   int chunks;

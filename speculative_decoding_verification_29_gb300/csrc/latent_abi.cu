@@ -43,7 +43,7 @@ int take_pool(const spec_latent_cache* s, Kv8Pool* c) {
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-// As the 8-bit cache's attention: a flag and a cut item per part, then two shares a part.
+// As the 8-bit cache's attention: a flag and a cut item (with its sequence) per part, then two shares a part.
 struct AttnLayout {
   size_t cut, ml, o, total;
 };
@@ -51,7 +51,7 @@ AttnLayout attn_layout(int rows, int C) {
   const size_t parts = kSms;
   AttnLayout l{};
   l.cut = up256(parts * sizeof(int32_t));
-  l.ml = l.cut + up256(parts * sizeof(int4));
+  l.ml = l.cut + up256(2 * parts * sizeof(int4));
   l.o = l.ml + up256(2 * parts * rows * sizeof(float2));
   l.total = l.o + up256(2 * parts * rows * C * sizeof(float));
   return l;
@@ -219,7 +219,7 @@ int spec_latent_compact(const spec_latent_cache* cache, int n_planes, int64_t st
 size_t spec_pages_workspace_bytes(int B, int max_blocks, int num_blocks) {
   if (B < 1 || max_blocks < 1 || num_blocks < 1 || B > kMaxB || max_blocks > (1 << 27)) return 0;
   const size_t chunks = (max_blocks + kPagesChunk - 1) / kPagesChunk, n = num_blocks;
-  return 3 * up256(n * 4) + up256(B * chunks * 4) + 2 * up256(B * sizeof(int2)) + 256;
+  return 3 * up256(n * 4) + up256(B * chunks * 4) + up256(2 * B * sizeof(int4)) + up256(B * sizeof(int2)) + 256;
 }
 
 int spec_pages_update(const int32_t* block_table, int32_t* new_table, const int32_t* cache_len, const int32_t* keep_len,
@@ -275,7 +275,7 @@ int spec_pages_update(const int32_t* block_table, int32_t* new_table, const int3
   a.last_sharer = reinterpret_cast<int32_t*>(room(static_cast<size_t>(num_blocks) * 4));
   a.free_ids = reinterpret_cast<int32_t*>(room(static_cast<size_t>(num_blocks) * 4));
   a.unsound = reinterpret_cast<int32_t*>(room(static_cast<size_t>(B) * a.chunks * 4));
-  a.take = reinterpret_cast<int2*>(room(static_cast<size_t>(B) * sizeof(int2)));
+  a.take = reinterpret_cast<int4*>(room(2 * static_cast<size_t>(B) * sizeof(int4)));
   a.copies = reinterpret_cast<int2*>(room(static_cast<size_t>(B) * sizeof(int2)));
   a.n_copies = reinterpret_cast<int32_t*>(room(4));
   return cuda_status(launch_pages_update(a, static_cast<cudaStream_t>(stream)));

@@ -174,20 +174,23 @@ struct Items {
     return true;
   }
   // What the join needs to know where the item begins in the run and ends behind it.
-  __device__ __forceinline__ int4 cut(const LatentAttnArgs& a, const Runs& runs) const {
-    if (t0 > 0 || t1 == r.tiles) return make_int4(0, 0, 0, 0);
+  __device__ __forceinline__ void cut(const LatentAttnArgs& a, const Runs& runs) const {
+    int4* at = a.cut + 2 * blockIdx.x;
+    at[0] = make_int4(0, 0, 0, 0);
+    if (t0 > 0 || t1 == r.tiles) return;
     const int part = a.gang ? blockIdx.x / a.gang : blockIdx.x;
     const int64_t end = runs.begin(part + 1) - to + r.tiles;
     int n = 2;
     while (runs.begin(part + n) < end) ++n;
-    return make_int4(r.b, r.rt, h, n);
+    at[0] = make_int4(r.b, r.rt, h, n);
+    at[1] = make_int4(r.first, r.rows, r.ctx, r.n);
   }
 };
 
 // -------------------------------------------------------------------- join --
 //
 // As kv8_join_kernel, for items of up to 512 dimensions (item.z of a row's a.c.D): block x adds the shares of the item that begins in part x and ends
-// behind it, a warp one row at a time; the last blocks check sequences, and make the rows NaN that see an entry of a page
+// behind it, a warp 128 dimensions of one row at a time; the last blocks check sequences, and make the rows NaN that see an entry of a page
 // outside the pool.
 
 template <typename QT, int N>
@@ -225,47 +228,51 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
     }
     return;
   }
-  const int4 item = a.cut[blockIdx.x];
+  const int4 item = a.cut[2 * blockIdx.x], seq = a.cut[2 * blockIdx.x + 1];  // seq: first token, rows, context, step tokens
   const int n = item.w;
   if (n == 0) return;
-  const RowTile r = row_tile<N>(a, item.x, item.y);
   const int64_t first = blockIdx.x, step = a.gang ? a.gang : 1;  // shares of an item lie `step` parts apart
+  const int chunks = (D + 127) / 128, units = seq.y * chunks;
   bool outside = false;
   for (int i = lane; i < n; i += 32) outside |= (a.gave_up[first + i * step] & kOutside) != 0;
   outside = __any_sync(0xffffffffu, outside);
 #pragma unroll 1
-  for (int row = blockIdx.y * (kJoinThreads / 32) + warp; row < r.rows; row += gridDim.y * (kJoinThreads / 32)) {
+  for (int unit = blockIdx.y * (kJoinThreads / 32) + warp; unit < units; unit += gridDim.y * (kJoinThreads / 32)) {
+    const int row = unit / chunks, d = (unit - row * chunks) * 128 + 4 * lane;
     auto share = [&](int i) { return (2 * (first + i * step) + (i == 0 ? 1 : 0)) * N + row; };
     float top = kNegInf;
     for (int i = lane; i < n; i += 32) top = fmaxf(top, a.part_ml[share(i)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float4 acc[4] = {};
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-#pragma unroll 2
-    for (int i = 0; i < n; ++i) {
-      const float2 ml = a.part_ml[share(i)];
-      const float* p = a.part_o + share(i) * D + 4 * lane;
-      const float w = ml.x == top ? 1.f : ex2_fast(ml.x - top);
-      sum = fmaf(w, ml.y, sum);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (128 * k + 4 * lane >= D) break;
-        const float4 u = *reinterpret_cast<const float4*>(p + 128 * k);
-        acc[k].x = fmaf(w, u.x, acc[k].x), acc[k].y = fmaf(w, u.y, acc[k].y);
-        acc[k].z = fmaf(w, u.z, acc[k].z), acc[k].w = fmaf(w, u.w, acc[k].w);
+#pragma unroll 1
+    for (int base = 0; base < n; base += 32) {  // a share a lane, then all lanes through the shares
+      float w = 0.f;
+      if (base + lane < n) {
+        const float2 ml = a.part_ml[share(base + lane)];
+        w = ml.x == top ? 1.f : ex2_fast(ml.x - top);
+        sum = fmaf(w, ml.y, sum);
+      }
+      const int many = min(32, n - base);
+#pragma unroll 8
+      for (int j = 0; j < many; ++j) {
+        const float by = __shfl_sync(0xffffffffu, w, j);
+        const float4 u = d < D ? *reinterpret_cast<const float4*>(a.part_o + share(base + j) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        acc.x = fmaf(by, u.x, acc.x), acc.y = fmaf(by, u.y, acc.y);
+        acc.z = fmaf(by, u.z, acc.z), acc.w = fmaf(by, u.w, acc.w);
       }
     }
-    const int item_row = item.y * N + row, tok = item_row / a.group;
-    QT* out = static_cast<QT*>(a.out) + (r.first + static_cast<int64_t>(tok)) * a.ost + (item_row - tok * a.group) * a.osh +
-              item.z * D + 4 * lane;
-    float inv = sum == 0.f ? 0.f : 1.f / sum;
-    if (outside && sees_outside(a, item.x, r.ctx, r.n, tok)) inv = __int_as_float(0x7fffffff);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (128 * k + 4 * lane >= D) break;
-      out[128 * k] = from_f<QT>(acc[k].x * inv), out[128 * k + 1] = from_f<QT>(acc[k].y * inv);
-      out[128 * k + 2] = from_f<QT>(acc[k].z * inv), out[128 * k + 3] = from_f<QT>(acc[k].w * inv);
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int item_row = item.y * N + row, tok = item_row / a.group;
+    QT* out = static_cast<QT*>(a.out) + (seq.x + static_cast<int64_t>(tok)) * a.ost + (item_row - tok * a.group) * a.osh +
+              item.z * D + d;
+    float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (outside && sees_outside(a, item.x, seq.z, seq.w, tok)) inv = __int_as_float(0x7fffffff);
+    if (d < D) {
+      out[0] = from_f<QT>(acc.x * inv), out[1] = from_f<QT>(acc.y * inv);
+      out[2] = from_f<QT>(acc.z * inv), out[3] = from_f<QT>(acc.w * inv);
     }
   }
 }
@@ -273,7 +280,8 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
 template <typename QT, int N>
 cudaError_t launch_latent_join(const LatentAttnArgs& a, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(a.max_tokens) * a.group;
-  const int y = static_cast<int>((rows < N ? rows : N) + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+  const int units = static_cast<int>(rows < N ? rows : N) * ((a.item_dims + 127) / 128);
+  const int y = (units + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
   const int checks = (a.c.B + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
   return launch_pdl(latent_join_kernel<QT, N>, dim3(static_cast<unsigned>(a.parts + checks), static_cast<unsigned>(y)),
                     dim3(kJoinThreads), st, a);

@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     };
     int i = 0;
     uint32_t f = 0;  // pieces so far
-    int4 cut = make_int4(0, 0, 0, 0);  // the last item's
+    if (tid == 0) a.cut[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     bool more = it.t0 < it.t1 || next_item();
     if (more) load_queries();
     for (int seg = 0; more; ++seg) {
@@ -455,7 +455,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 
       // ---- the next item's queries, then this one's results or its share of them
       const bool whole = t0 == 0 && t1 == r.tiles;
-      cut = it.cut(a, runs);
+      if (tid == 0) it.cut(a, runs);
+      __syncwarp();
       more = next_item();
       if (more) load_queries();
       const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (t0 > 0 ? 0 : 1);
@@ -522,7 +523,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       fence_before();
     }
-    if (tid == 0) a.cut[blockIdx.x] = cut;
   }
 
   fence_before();
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   if (warp == kMmaWarp) tmem_free(tmem, 512);
   if (tid == 0) {
     a.gave_up[blockIdx.x] = (sm.gave_up ? kGaveUp : 0) | (sm.outside ? kOutside : 0);
-    if (!work || sm.gave_up) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);  // what was begun is not to be joined
+    if (!work || sm.gave_up) a.cut[2 * blockIdx.x] = make_int4(0, 0, 0, 0);  // what was begun is not to be joined
   }
   griddep_launch_dependents();
 }

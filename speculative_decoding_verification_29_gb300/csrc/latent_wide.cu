@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     Items<kRows, kCost> it(a, start, my_units);
     int i = 0;
     int seg = 0;
-    int4 cut = make_int4(0, 0, 0, 0);  // the last item's
+    if (tid == 0) a.cut[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     do {
       if (it.t0 >= it.t1) continue;
       const RowTile r = it.r;
@@ -511,10 +511,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       fence_before();
       __syncwarp();
-      cut = it.cut(a, runs);
+      if (tid == 0) it.cut(a, runs);
+      __syncwarp();
       ++seg;
     } while (it.next(a));
-    if (tid == 0) a.cut[blockIdx.x] = cut;
   }
 
   fence_before();
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   if (warp == kMmaWarp) tmem_free(tmem, 512);
   if (tid == 0) {
     a.gave_up[blockIdx.x] = (sm.gave_up ? kGaveUp : 0) | (sm.outside ? kOutside : 0);
-    if (!work || sm.gave_up) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);  // what was begun is not to be joined
+    if (!work || sm.gave_up) a.cut[2 * blockIdx.x] = make_int4(0, 0, 0, 0);  // what was begun is not to be joined
   }
   griddep_launch_dependents();
 }

@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kTakeThreads) pages_take_kernel(const __grid_c
   __shared__ int s_copies;
   griddep_launch_dependents();
   griddep_wait();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x;
   if (tid == 0) s_copies = 0;
   // The block that b's next token goes into, where that holds tokens already and b asks for room; -1: none. `more`: blocks
   // it needs behind its own; -1: they pass the table.
@@ -126,19 +126,21 @@ __global__ void __launch_bounds__(kTakeThreads) pages_take_kernel(const __grid_c
   int64_t want = 0;
   for (int base = 0; base < a.B; base += kTakeThreads) {
     const int b = base + tid;
-    int n = 0, copy = -1;
+    int n = 0, copy = -1, kept = 0, keep = 0, flags = 0;
     if (b < a.B) {
       const Ask k = ask_of(a, b);
       int more;
       const int id = writes(b, k, &more);
       n = max(more, 0);
+      kept = k.kept, keep = k.keep;
+      flags = (k.sound ? 0 : 1) | (k.need > 0 ? 2 : 0) | (more < 0 ? 4 : 0);
       if (id >= 0 && a.refs[id] >= 2 && !(a.sharers[id] >= a.refs[id] && a.last_sharer[id] == b)) copy = id, ++n;
     }
     int64_t total;
     const int64_t at = want + block_scan(n, &total, s_warp);
     if (b < a.B) {
-      a.take[b] = make_int2(static_cast<int>(min(at, static_cast<int64_t>(INT_MAX))), n);
-      a.copies[b] = make_int2(copy, -1);  // read again below, in b's order, before the list is written over it
+      a.take[2 * b] = make_int4(static_cast<int>(min(at, static_cast<int64_t>(INT_MAX))), n, kept - (copy >= 0), copy);
+      a.take[2 * b + 1] = make_int4(keep, flags & 1, flags & 2, flags & 4);
     }
     want += total;
   }
@@ -160,41 +162,28 @@ __global__ void __launch_bounds__(kTakeThreads) pages_take_kernel(const __grid_c
     found += total;
   }
   __syncthreads();
-  // a warp per sequence, 32 sequences at a time
-  for (int base = 0; base < a.B; base += kTakeThreads / 32) {
-    const int b = base + warp;
-    int2 take = make_int2(0, 0);
-    int copy = -1, dst = -1;
-    if (b < a.B) {
-      take = a.take[b];
-      copy = a.copies[b].x;
-    }
-    __syncthreads();  // the list of copies never passes the sequences that have been read
-    if (b < a.B) {
-      const Ask k = ask_of(a, b);
-      int more;
-      writes(b, k, &more);
-      const bool shorts = k.need > 0 && (more < 0 || static_cast<int64_t>(take.x) + take.y > found);
-      int32_t* row = a.new_table + static_cast<int64_t>(b) * a.M;
-      if (!shorts) {
-        const int first = k.kept - (copy >= 0);
-        for (int i = lane; i < take.y; i += 32) {
-          const int id = a.free_ids[take.x + i];
-          row[first + i] = id;
-          a.refs[id] = 1;
-          if (i == 0) dst = id;
-        }
+  // eight lanes per sequence
+  const int sub = tid & 7;
+  for (int b = tid >> 3; b < a.B; b += kTakeThreads / 8) {
+    const int4 t = a.take[2 * b], k = a.take[2 * b + 1];
+    const bool shorts = k.z && (k.w || static_cast<int64_t>(t.x) + t.y > found);
+    int32_t* row = a.new_table + static_cast<int64_t>(b) * a.M;
+    int dst = -1;
+    if (!shorts)
+      for (int i = sub; i < t.y; i += 8) {
+        const int id = a.free_ids[t.x + i];
+        row[t.z + i] = id;
+        a.refs[id] = 1;
+        if (i == 0) dst = id;
       }
-      bool bad = !k.sound || shorts;
-      for (int c = lane; c < a.chunks; c += 32) bad |= a.unsound[static_cast<int64_t>(b) * a.chunks + c] != 0;
-      bad = __any_sync(0xffffffffu, bad);
-      if (lane == 0) {
-        a.row_status[b] = bad ? SPEC_ROW_CACHE : 0;
-        a.new_len[b] = k.keep;
-        if (copy >= 0 && !shorts) {
-          atomicSub(&a.refs[copy], 1);
-          a.copies[atomicAdd(&s_copies, 1)] = make_int2(copy, dst);
-        }
+    if (sub == 0) {
+      bool bad = k.y || shorts;
+      for (int c = 0; c < a.chunks; ++c) bad |= a.unsound[static_cast<int64_t>(b) * a.chunks + c] != 0;
+      a.row_status[b] = bad ? SPEC_ROW_CACHE : 0;
+      a.new_len[b] = k.x;
+      if (t.w >= 0 && !shorts) {
+        atomicSub(&a.refs[t.w], 1);
+        a.copies[atomicAdd(&s_copies, 1)] = make_int2(t.w, dst);
       }
     }
   }
