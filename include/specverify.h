@@ -103,7 +103,7 @@ enum {
 #define SPEC_ROW_WARP 32  /* spec_tree_expand: more than 4096 tokens of one frontier node tie at its M-th
                              largest logit (never set by the chain calls) */
 
-#define SPEC_ROW_CACHE 64 /* spec_kv8_*: a sequence's lengths, or the id of a cache block it uses, are out of range */
+#define SPEC_ROW_CACHE 64 /* spec_kv8_*, spec_latent_*, spec_pages_update: a sequence's lengths, or the id of a cache block it uses, are out of range */
 #define SPEC_ROW_TIMEOUT 128 /* spec_kv8_attention: a wait inside the kernel ran out (never seen in a sound run) */
 
 /* Limits: 1 <= B <= 65535; 0 <= K <= 255; 2 <= V <= 2^24; for trees

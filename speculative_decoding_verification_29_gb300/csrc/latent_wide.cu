@@ -28,20 +28,20 @@ namespace {
 constexpr int kCost = 4;
 constexpr int kRows = 128, kSlots = 64;  // rows of an item, slots of a tile
 constexpr int kChunk = kSlots * 128, kQChunk = kRows * 128;  // bytes of 64 dimensions of a tile, of the queries
-constexpr int kPieces = 4, kShared = 2;  // ring: two tiles' pieces and shared dimensions
+constexpr int kPieces = 4;  // ring: pieces of two tiles (of four, where a piece is all values); a tile's first one brings the shared dimensions
 constexpr uint32_t kQAt = 256, kSAt = 384;  // tensor memory: results at 0, queries, scores
 constexpr int kWideThreads = 128 + 128 + 64;  // weights, queries, copies and products
 constexpr int kBudget = 232448;
 
 struct Small {
-  alignas(8) uint64_t full[kPieces], empty[kPieces], sh_full[kShared], sh_empty[kShared];
+  alignas(8) uint64_t full[kPieces], empty[kPieces];
   alignas(8) uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_free, drain;
   int tmp[64];
   int odd[2];  // item number + 1 where a value that not every row sees is not finite
   uint32_t tmem;
   int gave_up, outside;
 };
-static_assert(5 * kQChunk + kPieces * 4 * kChunk + kShared * kChunk + sizeof(Small) + 1024 <= kBudget, "shared memory");
+static_assert(5 * kQChunk + kPieces * 4 * kChunk + 2 * kChunk + sizeof(Small) + 1024 <= kBudget, "shared memory");
 
 // 64 columns of the warp's lanes.
 __device__ __forceinline__ void ld64(uint32_t addr, uint32_t* r) {
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   uint8_t* q_smem = dyn + ((1024u - (smem_addr(dyn) & 1023u)) & 1023u);  // dimensions that are no values of the item, shared ones
   uint8_t* ring = q_smem + ((halves - 1) * pc + 1) * kQChunk;
   uint8_t* sh = ring + kPieces * piece;
-  Small& sm = *reinterpret_cast<Small*>(sh + kShared * kChunk);
+  Small& sm = *reinterpret_cast<Small*>(sh + kPieces / halves * kChunk);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = uniform(tid >> 5);
   constexpr int kQueryWarp = 4, kLoadWarp = 8, kMmaWarp = 9;
@@ -82,9 +82,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       bar_init(smem_addr(&sm.full[i]), 1);
       bar_init(smem_addr(&sm.empty[i]), 1);
     }
-    for (int i = 0; i < kShared; ++i) {
-      bar_init(smem_addr(&sm.sh_full[i]), 1);
-      bar_init(smem_addr(&sm.sh_empty[i]), 1);
+    for (int i = 0; i < 2; ++i) {
       bar_init(smem_addr(&sm.s_full[i]), 1);
       bar_init(smem_addr(&sm.p_full[i]), 4);
       bar_init(smem_addr(&sm.pv_done[i]), 1);
@@ -110,9 +108,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   fence_after();
   const uint32_t tmem = uniform(sm.tmem);
 
-  uint32_t fill = 0, sh_fill = 0;  // ring slots that copies were begun into
+  uint32_t fill = 0;  // ring slots that copies were begun into
   if (work && warp == kLoadWarp) {
-    // ---- copies: a tile's piece that is no value of the item, its shared dimensions, its values
+    // ---- copies: a tile's piece that is no value of the item with its shared dimensions, then its values
     Items<kRows, kCost> it(a, start, my_units);
     const int bs = a.c.block, rows = min(bs, kSlots), ppt = kSlots / rows;  // slots of a copy, copies of 64 dimensions
     bool ok = true;
@@ -138,28 +136,21 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (__any_sync(0xffffffffu, id == -2)) sm.outside = 1;
         const uint32_t inside = __popc(__ballot_sync(0xffffffffu, id >= 0 && c == 0));
         const int y = a.order ? id : in_block, z = a.order ? in_block : id;
-        auto copy_piece = [&](int p) {  // value dimensions p * vd on
+        auto copy_piece = [&](int p, bool shared) {  // value dimensions p * vd on; the shared ones with them
           const uint32_t slot = fill % kPieces, bar = smem_addr(&sm.full[slot]);
           if (fill >= kPieces) ok = bar_wait(smem_addr(&sm.empty[slot]), (fill / kPieces - 1) & 1, gave_up);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) return;
-          if (lane == 0) bar_expect(bar, inside * rows * 128 * pc);
+          if (lane == 0) bar_expect(bar, inside * rows * 128 * (shared ? pc + 1 : pc));
           __syncwarp();
           if (id >= 0 && c < pc)
             load_3d(smem_addr(ring + slot * piece + c * kChunk + sub * rows * 128), &map, bar, p * vd + c * 64, y, z);
+          if (shared && id >= 0 && c == pc) load_3d(smem_addr(sh + slot / halves * kChunk + sub * rows * 128), &map, bar, dims, y, z);
           ++fill;
         };
-        if (halves == 2) copy_piece(1 - it.h);
+        if (halves == 2) copy_piece(1 - it.h, true);
         if (!ok) break;
-        const uint32_t slot = sh_fill % kShared, bar = smem_addr(&sm.sh_full[slot]);
-        if (sh_fill >= kShared) ok = bar_wait(smem_addr(&sm.sh_empty[slot]), (sh_fill / kShared - 1) & 1, gave_up);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (lane == 0) bar_expect(bar, inside * rows * 128);
-        __syncwarp();
-        if (id >= 0 && c == 0) load_3d(smem_addr(sh + slot * kChunk + sub * rows * 128), &map, bar, dims, y, z);
-        ++sh_fill;
-        copy_piece(it.h);
+        copy_piece(it.h, halves == 1);
       }
     } while (ok && it.next(a));
   } else if (work && warp == kMmaWarp) {
@@ -185,14 +176,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const int s0 = uniform(sp.s0), s1 = uniform(sp.s1);
       auto scores = [&](bool last) {  // S[i & 1] = queries x tile, the values last: they are given back last (by the results)
         const uint32_t to = uniform(tmem + kSAt + (i & 1) * kSlots);
-        auto ready = [&](uint64_t* full, uint32_t slot, uint32_t round) {
-          ok = __all_sync(0xffffffffu, bar_wait(smem_addr(full + slot), round & 1, gave_up));
+        auto ready = [&](uint32_t slot) {
+          ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.full[slot]), (f / kPieces) & 1, gave_up));
           if (ok) fence_after();
           return ok;
         };
+        uint32_t slot = uniform(f % kPieces);
+        if (!ready(slot)) return false;
+        const uint64_t sd = moved(s_desc, slot / halves * kChunk);
         if (halves == 2) {
-          const uint32_t slot = uniform(f % kPieces);
-          if (!ready(sm.full, slot, f / kPieces)) return false;
           const uint64_t ed = moved(e_desc, slot * piece);
           if (elect()) {
 #pragma unroll
@@ -200,23 +192,21 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mma_f16(to, q_desc + (c * kQChunk >> 4) + 2 * k, ed + (c * kChunk >> 4) + 2 * k, id_s, c > 0 || k > 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f16(to, r_desc + 2 * k, sd + 2 * k, id_s, true);
             commit(smem_addr(&sm.empty[slot]));
           }
           __syncwarp();
           ++f;
+          slot = uniform(f % kPieces);
+          if (!ready(slot)) return false;
         }
-        const uint32_t shared = uniform(i % kShared), slot = uniform(f % kPieces);
-        if (!ready(sm.sh_full, shared, i / kShared)) return false;
-        const uint64_t sd = moved(s_desc, shared * kChunk), ed = moved(e_desc, slot * piece);
-        if (elect()) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f16(to, r_desc + 2 * k, sd + 2 * k, id_s, halves == 2 || k > 0);
-          commit(smem_addr(&sm.sh_empty[shared]));
-        }
-        __syncwarp();
-        if (!ready(sm.full, slot, f / kPieces)) return false;
         ++f;
+        const uint64_t ed = moved(e_desc, slot * piece);
         if (elect()) {
+          if (halves == 1)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f16(to, r_desc + 2 * k, sd + 2 * k, id_s, k > 0);
 #pragma unroll
           for (int c = 0; c < pc; ++c)
 #pragma unroll
@@ -526,11 +516,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       for (uint32_t k = fill > kPieces ? fill - kPieces : 0; k < fill; ++k)
 #pragma unroll 1
         for (int n = 0; n < (1 << 16) && !bar_try(smem_addr(&sm.full[k % kPieces]), (k / kPieces) & 1); ++n) {
-        }
-#pragma unroll 1
-      for (uint32_t k = sh_fill > kShared ? sh_fill - kShared : 0; k < sh_fill; ++k)
-#pragma unroll 1
-        for (int n = 0; n < (1 << 16) && !bar_try(smem_addr(&sm.sh_full[k % kShared]), (k / kShared) & 1); ++n) {
         }
     }
     if (warp == kMmaWarp) {

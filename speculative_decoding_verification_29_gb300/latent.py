@@ -5,38 +5,51 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
 from typing import Dict, Optional
 
 import torch
 
 from . import _lib
 from ._lib import SPEC_BF16, SPEC_F16, SPEC_F32, check
-from .api import _here, _int32, _kv8_rows, _kv8_workspace, _on_stream, _ptr, _stream, alloc_workspace
+from .api import _here, _int32, _kv8_rows, _kv8_workspace, _on_stream, _ptr, _raw_stream, _stream, alloc_workspace
 
 _DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
 
 
+def _whole(t, name, dev, at, n=0):
+    """_int32, kept cheap: small calls are bound by this host path. at: the device's index."""
+    if t.dtype is not torch.int32 or t.get_device() != at or not t.is_contiguous() or n and t.numel() < n:
+        _int32(t, name, dev, n)
+
+
+def _queue(stream, at):
+    return _raw_stream(at) if stream is None and _raw_stream is not None else _stream(stream)
+
+
 def _cache(cache, block_table, cache_len, latent_dim: int, planes: bool = False):
     """The C record of a cache and its device, checked; the tensors stay the caller's."""
-    dev = cache.device
-    if dev.type != "cuda":
+    dev, at = cache.device, cache.get_device()
+    if at < 0:
         raise ValueError("cache must be a CUDA tensor (the cache lives there)")
-    _here(dev)
+    if at != torch.cuda.current_device():
+        _here(dev)
     shape, stride = cache.shape, cache.stride()
     if len(shape) != 3 + planes or stride[-1] != 1:
         raise ValueError("cache must be [blocks, block, latent_dim + rot_dim], an entry contiguous")
-    if cache.dtype not in (torch.bfloat16, torch.float16):
+    dtype = _DTYPES.get(cache.dtype, SPEC_F32)
+    if dtype == SPEC_F32:
         raise TypeError(f"cache must be bfloat16 or float16, got {cache.dtype}")
     nb, bs, W = shape[-3:]
     if not 0 < latent_dim < W:
         raise ValueError(f"an entry of {W} elements cannot hold a latent vector of {latent_dim} and rotated dimensions")
-    _int32(block_table, "block_table", dev)
-    _int32(cache_len, "cache_len", dev)
-    B = cache_len.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B or cache_len.dim() != 1:
+    _whole(block_table, "block_table", dev, at)
+    _whole(cache_len, "cache_len", dev, at)
+    rows, lens = block_table.shape, cache_len.shape
+    if len(rows) != 2 or len(lens) != 1 or rows[0] != lens[0]:
         raise ValueError("block_table must be [B, max_blocks] and cache_len [B]")
-    return _lib.LatentCache(cache.data_ptr(), block_table.data_ptr(), cache_len.data_ptr(), B, nb, block_table.shape[1], bs,
-                            latent_dim, W - latent_dim, _DTYPES[cache.dtype], 2 * stride[-3], 2 * stride[-2]), dev
+    return _lib.LatentCache(cache.data_ptr(), block_table.data_ptr(), cache_len.data_ptr(), rows[0], nb, rows[1], bs,
+                            latent_dim, W - latent_dim, dtype, 2 * stride[-3], 2 * stride[-2]), dev, at
 
 
 def _vectors(t, name, D, dev):
@@ -46,8 +59,8 @@ def _vectors(t, name, D, dev):
     return t.stride(0)
 
 
-def _cu(cu_tokens, B, dev):
-    _int32(cu_tokens, "cu_tokens", dev)
+def _cu(cu_tokens, B, dev, at):
+    _whole(cu_tokens, "cu_tokens", dev, at)
     if cu_tokens.numel() != B + 1:
         raise ValueError("cu_tokens must have B + 1 entries")
 
@@ -73,16 +86,16 @@ def spec_latent_append(latent, rope_key, cache, block_table, cache_len, cu_token
     lib = _lib.load()
     if latent.dim() != 2:
         raise ValueError("latent must be [tokens, latent_dim]")
-    rec, dev = _cache(cache, block_table, cache_len, latent.shape[1])
+    rec, dev, at = _cache(cache, block_table, cache_len, latent.shape[1])
     T, R = latent.shape[0], rec.rot_dim
     xst, rst = _vectors(latent, "latent", rec.latent_dim, dev), _vectors(rope_key, "rope_key", R, dev)
     if latent.dtype not in (cache.dtype, torch.float32) or rope_key.dtype != latent.dtype:
         raise TypeError("latent and rope_key must both be of the cache's type or float32")
     if rope_key.shape[0] != T:
         raise ValueError("latent and rope_key must have the same tokens")
-    _cu(cu_tokens, rec.B, dev)
+    _cu(cu_tokens, rec.B, dev, at)
     if positions is not None:
-        _int32(positions, "positions", dev)
+        _whole(positions, "positions", dev, at)
         if positions.numel() != T:
             raise ValueError("positions must have one entry per token")
     wcode = 0
@@ -96,7 +109,7 @@ def spec_latent_append(latent, rope_key, cache, block_table, cache_len, cu_token
     if q_rope is not None:
         qst, qsh = _kv8_rows(q_rope, "q_rope", R, dev)
         if q_out is None:
-            q_out = torch.empty(q_rope.shape, dtype=q_rope.dtype, device=dev)
+            q_out = q_rope.new_empty(q_rope.shape)
         ost, osh = _kv8_rows(q_out, "q_out", R, dev, True)
         if q_rope.dtype != latent.dtype or q_out.dtype != q_rope.dtype or q_rope.shape[0] != T or q_out.shape != q_rope.shape:
             raise ValueError("q_rope and q_out must be [tokens, q_heads, rot_dim] of latent's type")
@@ -110,23 +123,27 @@ def spec_latent_append(latent, rope_key, cache, block_table, cache_len, cu_token
     if 2 * n != R:
         raise ValueError(f"inv_freq must have {R // 2} entries for {R} rotated dimensions, not {n}")
     if out is None:
-        out = dict(row_status=torch.empty(rec.B, dtype=torch.int32, device=dev))
+        out = dict(row_status=cache_len.new_empty(rec.B))
     else:
-        _int32(out["row_status"], "row_status", dev, rec.B)
+        _whole(out["row_status"], "row_status", dev, at, rec.B)
     if q_rope is not None:
         out["q_out"] = q_out
     check("spec_latent_append", lib.spec_latent_append(
         ctypes.byref(rec), latent.data_ptr(), xst, rope_key.data_ptr(), rst, _DTYPES[latent.dtype], T, cu_tokens.data_ptr(),
         _ptr(positions), freq, int(bool(interleaved)), _ptr(norm_weight), wcode, eps, _ptr(q_rope), qst, qsh,
-        None if q_rope is None else q_out.data_ptr(), ost, osh, hq, out["row_status"].data_ptr(), _stream(stream)))
+        None if q_rope is None else q_out.data_ptr(), ost, osh, hq, out["row_status"].data_ptr(), _queue(stream, at)))
     return out
 
 
 def latent_workspace_bytes(cache, value_dim: int, q_heads: int, max_tokens: int) -> int:
     """Workspace of spec_latent_attention for a cache's sizes, the query heads and the longest step."""
-    nb, bs, W = cache.shape
-    rec = _lib.LatentCache(cache.data_ptr(), cache.data_ptr(), cache.data_ptr(), 1, nb, 1, bs, value_dim, W - value_dim,
-                           _DTYPES[cache.dtype], 2 * cache.stride(0), 2 * cache.stride(1))
+    return _attention_bytes(cache.shape[1], value_dim, cache.shape[2] - value_dim, q_heads, max_tokens)
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_bytes(block: int, value_dim: int, rot: int, q_heads: int, max_tokens: int) -> int:
+    W = 2 * (value_dim + rot)
+    rec = _lib.LatentCache(256, 256, 256, 1, 1, 1, block, value_dim, rot, SPEC_BF16, block * W, W)  # only sizes matter
     return int(_lib.load().spec_latent_workspace_bytes(ctypes.byref(rec), q_heads, max_tokens))
 
 
@@ -148,21 +165,21 @@ def spec_latent_attention(q, cache, block_table, cache_len, cu_tokens, *, max_to
     caller applies the values' up-projection, and row_status [B]; a caller's
     own out["out"] may have any token and head strides, but must not be q."""
     lib = _lib.load()
-    rec, dev = _cache(cache, block_table, cache_len, value_dim)
+    rec, dev, at = _cache(cache, block_table, cache_len, value_dim)
     qst, qsh = _kv8_rows(q, "q", cache.shape[2], dev)
     if q.dtype != cache.dtype:
         raise TypeError("q must have the cache's type")
     T, hq, _ = q.shape
-    _cu(cu_tokens, rec.B, dev)
+    _cu(cu_tokens, rec.B, dev, at)
     if tree_mask is not None:
         if tree_mask.device != dev or tree_mask.element_size() != 1 or not tree_mask.is_contiguous() or \
                 tree_mask.shape != (rec.B, max_tokens, max_tokens):
             raise ValueError("tree_mask must be a contiguous [B, max_tokens, max_tokens] tensor of bytes")
     if out is None:
-        out = dict(out=torch.empty(T, hq, value_dim, dtype=q.dtype, device=dev),
-                   row_status=torch.empty(rec.B, dtype=torch.int32, device=dev))
+        out = dict(out=q.new_empty((T, hq, value_dim)),
+                   row_status=cache_len.new_empty(rec.B))
     else:
-        _int32(out["row_status"], "row_status", dev, rec.B)
+        _whole(out["row_status"], "row_status", dev, at, rec.B)
     o = out["out"]
     ost, osh = _kv8_rows(o, "out", value_dim, dev, True)
     if o.shape != (T, hq, value_dim) or o.dtype != q.dtype:
@@ -170,7 +187,7 @@ def spec_latent_attention(q, cache, block_table, cache_len, cu_tokens, *, max_to
     if T and o.data_ptr() == q.data_ptr():
         raise ValueError("out must not be q: queries are read again after the first results were written")
     if workspace is None:
-        nbytes = lib.spec_latent_workspace_bytes(ctypes.byref(rec), hq, max_tokens)
+        nbytes = _attention_bytes(rec.block, value_dim, rec.rot_dim, hq, max_tokens)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         if workspace.data_ptr() % 256:
             workspace = alloc_workspace(nbytes, dev)
@@ -179,7 +196,7 @@ def spec_latent_attention(q, cache, block_table, cache_len, cu_tokens, *, max_to
     check("spec_latent_attention", lib.spec_latent_attention(
         ctypes.byref(rec), q.data_ptr(), qst, qsh, T, hq, cu_tokens.data_ptr(), max_tokens, _ptr(tree_mask), sm_scale,
         o.data_ptr(), ost, osh, out["row_status"].data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace.numel() * workspace.element_size(), _queue(stream, at)))
     return out
 
 
@@ -196,26 +213,26 @@ def spec_latent_compact(cache, block_table, cache_len, accept_len, path=None,
     lib = _lib.load()
     W = cache.shape[-1]
     C = (W - 1) // 128 * 128  # entries move whole: how they are divided does not matter here
-    rec, dev = _cache(cache, block_table, cache_len, C, cache.dim() == 4)
+    rec, dev, at = _cache(cache, block_table, cache_len, C, cache.dim() == 4)
     planes, sp = (cache.shape[0], 2 * cache.stride(0)) if cache.dim() == 4 else (1, 0)
-    _int32(accept_len, "accept_len", dev)
+    _whole(accept_len, "accept_len", dev, at)
     if accept_len.numel() != rec.B:
         raise ValueError("accept_len must have B entries")
     D = 0
     if path is not None:
-        _int32(path, "path", dev)
+        _whole(path, "path", dev, at)
         if path.dim() != 2 or path.shape[0] != rec.B:
             raise ValueError("path must be [B, D]")
         D = path.shape[1]
     if out is None:
-        out = dict(new_len=torch.empty(rec.B, dtype=torch.int32, device=dev),
-                   row_status=torch.empty(rec.B, dtype=torch.int32, device=dev))
+        out = dict(new_len=cache_len.new_empty(rec.B),
+                   row_status=cache_len.new_empty(rec.B))
     else:
-        _int32(out["new_len"], "new_len", dev, rec.B)
-        _int32(out["row_status"], "row_status", dev, rec.B)
+        _whole(out["new_len"], "new_len", dev, at, rec.B)
+        _whole(out["row_status"], "row_status", dev, at, rec.B)
     check("spec_latent_compact", lib.spec_latent_compact(ctypes.byref(rec), planes, sp, _ptr(path), D, accept_len.data_ptr(),
                                                          out["new_len"].data_ptr(), out["row_status"].data_ptr(),
-                                                         _stream(stream)))
+                                                         _queue(stream, at)))
     return out
 
 
@@ -256,19 +273,20 @@ def spec_pages_update(block_table, cache_len, refs, pools=(), *, planes: bool = 
     and out has none), cache_len [B] (the tokens kept), row_status [B], and refs. A
     sequence with SPEC_ROW_CACHE in row_status must not be appended to."""
     lib = _lib.load()
-    dev = block_table.device
-    if dev.type != "cuda":
+    dev, at = block_table.device, block_table.get_device()
+    if at < 0:
         raise ValueError("block_table must be a CUDA tensor")
-    _here(dev)
-    _int32(block_table, "block_table", dev)
-    _int32(cache_len, "cache_len", dev)
-    _int32(refs, "refs", dev)
+    if at != torch.cuda.current_device():
+        _here(dev)
+    _whole(block_table, "block_table", dev, at)
+    _whole(cache_len, "cache_len", dev, at)
+    _whole(refs, "refs", dev, at)
     if block_table.dim() != 2 or cache_len.dim() != 1 or refs.dim() != 1 or block_table.shape[0] != cache_len.numel():
         raise ValueError("block_table must be [B, max_blocks], cache_len [B] and refs [num_blocks]")
     B, M = block_table.shape
     for t, name in ((keep_len, "keep_len"), (source, "source"), (need, "need")):
         if t is not None:
-            _int32(t, name, dev)
+            _whole(t, name, dev, at)
             if t.numel() != B:
                 raise ValueError(f"{name} must have B entries")
     if block is None:
@@ -278,12 +296,12 @@ def spec_pages_update(block_table, cache_len, refs, pools=(), *, planes: bool = 
     n = refs.numel()
     recs = _pages_pools(pools, n, dev, planes)
     if out is None:
-        out = dict(cache_len=torch.empty_like(cache_len), row_status=torch.empty(B, dtype=torch.int32, device=dev))
+        out = dict(cache_len=cache_len.new_empty(B), row_status=cache_len.new_empty(B))
     else:
-        _int32(out["cache_len"], "out's cache_len", dev, B)
-        _int32(out["row_status"], "row_status", dev, B)
+        _whole(out["cache_len"], "out's cache_len", dev, at, B)
+        _whole(out["row_status"], "row_status", dev, at, B)
     table = out.setdefault("block_table", block_table if source is None else torch.empty_like(block_table))
-    _int32(table, "out's block_table", dev)
+    _whole(table, "out's block_table", dev, at)
     if table.shape != block_table.shape:
         raise ValueError("out's block_table must have block_table's shape")
     if source is not None and table.data_ptr() == block_table.data_ptr():
@@ -300,6 +318,6 @@ def spec_pages_update(block_table, cache_len, refs, pools=(), *, planes: bool = 
     check("spec_pages_update", lib.spec_pages_update(
         block_table.data_ptr(), table.data_ptr(), cache_len.data_ptr(), _ptr(keep_len), _ptr(source), _ptr(need),
         refs.data_ptr(), B, M, n, block, recs, len(pools), out["cache_len"].data_ptr(), out["row_status"].data_ptr(),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _queue(stream, at)))
     out["refs"] = refs
     return out
