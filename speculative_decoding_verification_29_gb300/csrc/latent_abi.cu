@@ -178,7 +178,7 @@ int spec_latent_attention(const spec_latent_cache* cache, const void* queries, i
   if (static_cast<int64_t>(a.row_tiles) * a.c.B >= (1LL << 31)) return SPEC_ERR_UNSUPPORTED;
   a.c.H = rows == 128 && a.c.D > 256 ? 2 : 1;
   a.item_dims = a.c.D / a.c.H;
-  // In gangs where all sequences have as many items and the gangs fill the SMs.
+  // In gangs (see latent_attn.cuh) where all sequences have as many items and whole gangs fill 7 of 8 SMs.
   a.gang = 0;
   const int64_t items = static_cast<int64_t>(a.row_tiles) * a.c.H;
   if (items > 1 && items <= kSms && static_cast<int64_t>(a.c.B) * max_tokens == T && kSms / items * items >= kSms * 7 / 8)

@@ -10,12 +10,21 @@
 // both compute its scores: (2 (C + R) + C) / (C + R + C) = 1.53 times the products.
 // That buys a first operand that lies in tensor memory in three of four
 // products: shared memory then only has to deliver the tile, which is what
-// bounds few rows on many slots (latent_attn.cu), and the scores of the next tile
+// bounds few rows on many slots (latent_rows.cuh), and the scores of the next tile
 // are computed while the weights of this one are made.
 //
 // Shared memory: the queries' other dimensions (80 KB) and two tiles of 64
 // slots (144 KB) in pieces of the value dimensions of an item, each given back when
-// its last product has read it.
+// its last product has read it. The piece that holds no values of the item comes
+// first in a tile's scores, so that the values, which their own product gives back
+// last, are asked for as late as possible (long contexts 966 -> 719 us).
+//
+// What bounds it. Two sequences of 110,000 to 131,072 tokens x 9 x 128 heads, bf16: 686
+// us, 910 TFLOP/s, 0.47 of a library product and 0.72 with the scores counted twice;
+// 2700 clocks a tile, of which the products take 1990, then waits for the values'
+// piece and those of the issuing warp. 16 trees of 61 tokens x 16 heads, fp16: 144
+// us, tensor pipe busy for 40%; an item's queries, first maximum, masked tiles and
+// results take a third. 256 dimensions (three prompts of 500 to 1500): 155 us.
 #include <string.h>
 
 #include "latent_attn.cuh"
@@ -337,7 +346,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         ld64(at, x);
         const bool masked = s >= sp.part;
         if (masked) {
-          // As in latent_attn.cu: slots behind the rows' last, and values that are not finite, are cleared. Two threads a slot.
+          // As in latent_rows.cuh: slots behind the rows' last, and values that are not finite, are cleared. Two threads a slot.
           const int in = own & 63, slot = s * kSlots + in;
           const uint32_t value = static_cast<uint32_t>(i) * halves + halves - 1;
           ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.full[value % kPieces]), (value / kPieces) & 1, gave_up));

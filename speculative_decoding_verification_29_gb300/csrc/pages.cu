@@ -12,6 +12,10 @@
 // Who copies: of the c sequences of a call that go on writing the same partly
 // filled block, held by r sequences in all, every one where c < r; where c = r,
 // all but the last, which keeps it.
+//
+// What bounds it. 64 sequences after a step: 8.9 us, the three launches' chain. Four
+// prompts forked to 64 sequences, 60 blocks of 74 KB copied in 32 planes: 27.5 us,
+// 142 MB of stores (the sources come from L2 after their first reader).
 #include <limits.h>
 
 #include "internal.h"

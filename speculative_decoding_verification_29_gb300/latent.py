@@ -243,12 +243,17 @@ def _pages_pools(pools, num_blocks, dev, planes):
     for rec, t in zip(recs, pools):
         if t.device != dev:
             raise ValueError(f"pools must be on {dev}")
-        if t.dim() < lead + 2 or t.shape[lead] != num_blocks or t.numel() == 0 or not t[(0,) * (lead + 1)].is_contiguous():
+        shape, stride, inner = t.shape, t.stride(), 1
+        for i in range(len(shape) - 1, lead, -1):
+            if shape[i] != 1 and stride[i] != inner:
+                inner = 0
+            inner *= shape[i]
+        if len(shape) < lead + 2 or shape[lead] != num_blocks or inner == 0:
             raise ValueError(f"pools must be [{'planes, ' * lead}{num_blocks}, ...], the elements of a block contiguous; got "
-                             f"{tuple(t.shape)} with strides {t.stride()}")
-        size, stride = t.element_size(), t.stride()
-        rec.data, rec.n_planes, rec.stride_plane = t.data_ptr(), t.shape[0] if lead else 1, stride[0] * size if lead else 0
-        rec.stride_block, rec.block_bytes = stride[lead] * size, t[(0,) * (lead + 1)].numel() * size
+                             f"{tuple(shape)} with strides {stride}")
+        size = t.element_size()
+        rec.data, rec.n_planes, rec.stride_plane = t.data_ptr(), shape[0] if lead else 1, stride[0] * size if lead else 0
+        rec.stride_block, rec.block_bytes = stride[lead] * size, inner * size
     return recs
 
 
