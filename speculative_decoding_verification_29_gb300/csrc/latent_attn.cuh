@@ -61,16 +61,17 @@ __device__ __forceinline__ void turn_units(uint4* u, int lane) {
 }
 
 // Clears a slot's chunks of 16 bytes in shared memory where the slot lies behind the rows' last; else only the elements that
-// are not finite. True where it met such a one. An exponent of ones carries into the sign's place.
+// are not finite. True where it met such a one. An exponent of ones carries into the sign's place. Neighbouring slots lie 128
+// bytes apart, so each begins at another chunk (`first`): else all would ask the same banks.
 template <typename B, int CHUNKS>
-__device__ __forceinline__ bool clean_chunks(uint4* row, bool behind) {
+__device__ __forceinline__ bool clean_chunks(uint4* row, int first, bool behind) {
   uint32_t hit = 0;
 #pragma unroll
   for (int k = 0; k < CHUNKS; ++k) {
     if (behind) {
-      row[k] = make_uint4(0, 0, 0, 0);
+      row[k ^ first] = make_uint4(0, 0, 0, 0);
     } else {
-      const uint4 u = row[k];
+      const uint4 u = row[k ^ first];
       hit |= ((u.x & B::kExp) + B::kStep) | ((u.y & B::kExp) + B::kStep) | ((u.z & B::kExp) + B::kStep) | ((u.w & B::kExp) + B::kStep);
     }
   }

@@ -56,7 +56,7 @@ struct LCfg {
   static constexpr uint32_t kO = 64;              // tensor memory: scores at 0, results of 128 dimensions every 64 columns
   static constexpr int kBudget = 232448 - 1024;
   struct Small {
-    alignas(16) float ref[N];
+    alignas(16) float ref[N], fac[N];  // references, and what sums and results are scaled by when they move
     alignas(16) float smax[G][4][HN];  // each warp's largest scores
     float sums[G][4][HN];
     alignas(16) float inv[4 * G][HN];
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               uint4* row = reinterpret_cast<uint4*>(ring + at * kPiece + c * (kTile * 128) + own * 128);
-              if (clean_chunks<B, 8>(row, slot >= r.end)) sm.odd[seg & 1] = seg + 1;
+              if (clean_chunks<B, 8>(row, own & 7, slot >= r.end)) sm.odd[seg & 1] = seg + 1;
             }
           }
           if (slot >= r.ctx) {
@@ -421,13 +421,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const float old = t == t0 ? kUnset : sm.ref[group * HN + col], now = fmaxf(old, m);
           const float by = t == t0 ? 0.f : ex2_fast(old - now);
           named_sync(bar_id, 128);  // references and maxima have been read
-          if (quarter == 0 && lane < HN) sm.ref[group * HN + lane] = now;
+          if (quarter == 0 && lane < HN) sm.ref[group * HN + lane] = now, sm.fac[group * HN + lane] = by;
+          named_sync(bar_id, 128);
           float fac[HN];
 #pragma unroll
-          for (int j = 0; j < HN; ++j) {
-            y[j] -= __shfl_sync(0xffffffffu, now, j);
-            fac[j] = __shfl_sync(0xffffffffu, by, j);
-            l[j] *= fac[j];
+          for (int j = 0; j < HN; j += 4) {
+            const float4 n4 = *reinterpret_cast<const float4*>(&sm.ref[group * HN + j]),
+                         f4 = *reinterpret_cast<const float4*>(&sm.fac[group * HN + j]);
+            y[j] -= n4.x, y[j + 1] -= n4.y, y[j + 2] -= n4.z, y[j + 3] -= n4.w;
+            fac[j] = f4.x, fac[j + 1] = f4.y, fac[j + 2] = f4.z, fac[j + 3] = f4.w;
+            l[j] *= f4.x, l[j + 1] *= f4.y, l[j + 2] *= f4.z, l[j + 3] *= f4.w;
           }
           if (t > t0) {
 #pragma unroll 1
@@ -442,7 +445,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             }
             wait_st();
           }
-          named_sync(bar_id, 128);  // the new references are there for the next tile
         }
         uint8_t* p_row = sh + (i % NS) * kShared + own * 128;
 #pragma unroll

@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (slot >= r.ctx) {  // every row sees those before
 #pragma unroll 1
             for (int c = own >> 6; c < pc; c += 2)
-              if (clean_chunks<B, 8>(reinterpret_cast<uint4*>(row + c * kChunk), slot >= r.end)) sm.odd[seg & 1] = seg + 1;
+              if (clean_chunks<B, 8>(reinterpret_cast<uint4*>(row + c * kChunk), in & 7, slot >= r.end)) sm.odd[seg & 1] = seg + 1;
           }
           __syncwarp();
         }
