@@ -60,6 +60,7 @@ struct LCfg {
     alignas(16) float smax[G][4][HN];  // each warp's largest scores
     float sums[G][4][HN];
     alignas(16) float inv[4 * G][HN];
+    int64_t to[G][HN];  // where an item's rows go (elements; -1: no such row)
     alignas(8) uint64_t full[kMaxPieces], empty[kMaxPieces], sh_full[kMaxShared], sh_empty[kMaxShared];
     alignas(8) uint64_t s_full, p_full, o_full, q_full, drain;
     int tmp[64];
@@ -90,18 +91,32 @@ __device__ __forceinline__ void st_cols(uint32_t addr, const uint32_t* r) {
   for (int k = 0; k < HN; k += 8) tmem_st8(addr + k, r + k);
 }
 
-// Sums of v[j] over the warp's lanes, j < HN <= 32: lane j gets the j-th. v is not kept.
+// Sums of v[j] over the warp's lanes, j < C = 8, 16 or 32: lane j (mod C) gets the j-th. v is not kept.
+template <int C>
+__device__ __forceinline__ float lane_sum(float* v, int lane) {
+#pragma unroll
+  for (int o = 16; o >= C; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < C; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+#pragma unroll
+  for (int o = C / 2; o >= 1; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int k = 0; k < o; ++k) {
+      const float send = up ? v[k] : v[k + o], keep = up ? v[k + o] : v[k];
+      v[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  return v[0];
+}
 template <int HN>
 __device__ __forceinline__ float sums_of(float* v, int lane) {
-  float r = 0.f;
-#pragma unroll
-  for (int j = 0; j < HN; ++j) {
-    float s = v[j];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == j) r = s;
+  if constexpr (HN == 24) {
+    const float a = lane_sum<16>(v, lane), b = lane_sum<8>(v + 16, lane);
+    return lane < 16 ? a : b;
+  } else {
+    return lane_sum<HN>(v, lane);
   }
-  return r;
 }
 
 // ----------------------------------------------------------------- kernel --
@@ -475,6 +490,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       {
         const float s = sums_of<HN>(l, lane);
         if (lane < HN) sm.sums[group][quarter][lane] = s;
+        if (quarter == 3 && lane < HN) {
+          const int flat = r0 + lane, tok = flat / a.group;
+          sm.to[group][lane] = group * HN + lane < r.rows
+                                   ? (r.first + static_cast<int64_t>(tok)) * a.ost + (flat - tok * a.group) * a.osh : -1;
+        }
       }
       ok = bar_wait(smem_addr(&sm.o_full), seg & 1, gave_up);
       if (!named_all(bar_id, 128, ok)) break;
@@ -508,7 +528,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         ld_cols<HN>(lanes + C::kO + 64 * p, x);
         wait_ld();
         settle<HN>(x);
-        int tok = r0 / a.group, sub = r0 - tok * a.group;
         if (!whole) {
           float* o = a.part_o + (part * N + group * HN) * dims + 128 * p + own;
 #pragma unroll
@@ -519,15 +538,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < HN; j += 2) {  // neighbours swap: a lane stores two dimensions of every other row
           const float u = __uint_as_float(x[j]) * sm.inv[warp][j], v = __uint_as_float(x[j + 1]) * sm.inv[warp][j + 1];
-          const int s0 = sub, k0 = tok;
-          if (++sub == a.group) sub = 0, ++tok;
-          const int s1 = sub, k1 = tok;
-          if (++sub == a.group) sub = 0, ++tok;
           const bool odd = lane & 1;
           const float got = __shfl_xor_sync(0xffffffffu, odd ? u : v, 1);
-          QT* o = static_cast<QT*>(a.out) + (r.first + static_cast<int64_t>(odd ? k1 : k0)) * a.ost + (odd ? s1 : s0) * a.osh +
-                  128 * p + (own & ~1);
-          if (group * HN + j + (odd ? 1 : 0) >= r.rows) continue;
+          const int64_t to = sm.to[group][j + (odd ? 1 : 0)];
+          if (to < 0) continue;
+          QT* o = static_cast<QT*>(a.out) + to + 128 * p + (own & ~1);
           const float lo = odd ? got : u, hi = odd ? v : got;
           if (vec_o) *reinterpret_cast<uint32_t*>(o) = B::pack(lo, hi);
           else o[0] = from_f<QT>(lo), o[1] = from_f<QT>(hi);
