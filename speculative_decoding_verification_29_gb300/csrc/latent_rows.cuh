@@ -24,12 +24,13 @@
 // What bounds it. A product of K = 16 takes 49 clocks at N = 64 (41 at 32), not the
 // 32 of its arithmetic: the first operand's 4 KB come from shared memory at 128
 // bytes a clock. 64 sequences x 9 tokens x 32 heads (1500 to 6500 tokens, bf16):
-// 271 us, 590 TFLOP/s, 0.31 of a library product; of some 5900 clocks a tile 3330 are
+// 256 us, 625 TFLOP/s, 0.32 of a library product; of some 5900 clocks a tile 3330 are
 // the products', 1400 the softmax step and its hand-overs, which nothing overlaps
-// because no second tile fits, the rest waits for pieces. 64 x 1 token: 71 us, 4.0
-// TB/s, 0.60 of a copy; a tile's pieces are given back one after the other during
-// its second product, so that about 2000 clocks a tile go by until the next one's are
-// there, and start and join take 15 us.
+// because no second tile fits, the rest waits for pieces; an item of 22 tiles has some
+// 20,000 clocks for its queries, first and masked tile and results. 64 x 1 token: 70
+// us, 4.1 TB/s, 0.62 of a copy; a tile's pieces are given back one after the other
+// during its second product, so that about 2000 clocks a tile go by until the next
+// one's are there, and start and join take 15 us.
 #pragma once
 
 #include <string.h>

@@ -19,12 +19,12 @@
 // first in a tile's scores, so that the values, which their own product gives back
 // last, are asked for as late as possible (long contexts 966 -> 719 us).
 //
-// What bounds it. Two sequences of 110,000 to 131,072 tokens x 9 x 128 heads, bf16: 686
-// us, 910 TFLOP/s, 0.47 of a library product and 0.72 with the scores counted twice;
+// What bounds it. Two sequences of 110,000 to 131,072 tokens x 9 x 128 heads, bf16: 685
+// us, 912 TFLOP/s, 0.47 of a library product and 0.72 with the scores counted twice;
 // 2700 clocks a tile, of which the products take 1990, then waits for the values'
-// piece and those of the issuing warp. 16 trees of 61 tokens x 16 heads, fp16: 144
+// piece and those of the issuing warp. 16 trees of 61 tokens x 16 heads, fp16: 143
 // us, tensor pipe busy for 40%; an item's queries, first maximum, masked tiles and
-// results take a third. 256 dimensions (three prompts of 500 to 1500): 155 us.
+// results take a third. 256 dimensions (three prompts of 500 to 1500): 150 us, 860 TFLOP/s.
 #include <string.h>
 
 #include "latent_attn.cuh"
