@@ -104,7 +104,7 @@ enum {
                              largest logit (never set by the chain calls) */
 
 #define SPEC_ROW_CACHE 64 /* spec_kv8_*, spec_latent_*, spec_pages_update: a sequence's lengths, or the id of a cache block it uses, are out of range */
-#define SPEC_ROW_TIMEOUT 128 /* spec_kv8_attention: a wait inside the kernel ran out (never seen in a sound run) */
+#define SPEC_ROW_TIMEOUT 128 /* spec_kv8_attention, spec_latent_attention: a wait inside the kernel ran out (never seen in a sound run) */
 
 /* Limits: 1 <= B <= 65535; 0 <= K <= 255; 2 <= V <= 2^24; for trees
  * 1 <= N <= 1024, 1 <= D <= 64, 1 <= R <= 4096. */

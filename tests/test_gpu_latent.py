@@ -391,3 +391,32 @@ def test_compact(planes, bs, C, R, dt):
     t[0, 0] = -1
     t[0, (30 + int(path[0, 11])) // bs] = c.num
     assert sv().spec_latent_compact(p, t, n, a, path.cuda())["row_status"].tolist()[0] == 64
+
+
+@pytest.mark.parametrize("heads", [16, 32])
+def test_uneven_steps_that_add_up(heads):
+    """As many tokens as B steps of max_tokens, but one sequence has fewer and one more than it may: its rows are NaN."""
+    c = plain.Cache([140, 300, 77], [9, 3, 15], 512, 64, 32, BF, seed=50).fill()
+    q = queries(c, heads, 51)
+    want, tol = plain.attention(c, q, SCALE)
+    r = attend(c, q.cuda(), most=9)
+    assert r["row_status"].tolist() == [0, 0, 64]
+    close(r["out"][:12], want[:12], tol[:12])
+    assert bool(torch.isnan(r["out"][12:]).all())
+
+
+def test_two_streams_at_once():
+    """Calls of both kernels in flight on two streams, each with memory of its own."""
+    c = plain.Cache([900, 40, 1500], [9, 9, 9], 512, 64, 32, BF, seed=52).fill()
+    args = c.to("cuda")
+    qs = [queries(c, h, 53).cuda() for h in (4, 24)]
+    first = [attend(c, q, args)["out"] for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, (q, s) in enumerate(zip(qs, streams)):
+            got[i].append(attend(c, q, args, stream=s)["out"])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, first[i]) for x in got[i])
