@@ -82,11 +82,9 @@ __device__ __forceinline__ bool clean_chunks(uint4* row, int first, bool behind)
   return true;
 }
 
-// A descriptor of smem_desc's, its address moved by `bytes`; the sum is known to be the warp's, so that it stays in uniform
-// registers and an issue takes few instructions (see tc.cuh).
-__device__ __forceinline__ uint64_t moved(uint64_t desc, uint32_t bytes) {
-  return (desc & 0xffffffff00000000ull) | uniform(static_cast<uint32_t>(desc) + (bytes >> 4));
-}
+// A descriptor of smem_desc's, its address moved by `bytes`. (Told to be uniform by a shuffle, as the roles' warp is, it costs 1
+// to 2% of the kernels' time.)
+__device__ __forceinline__ uint64_t moved(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 
 // What a tensor memory load has brought is used behind this only (after wait_ld).
 template <int C>

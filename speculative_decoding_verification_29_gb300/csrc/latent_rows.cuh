@@ -24,7 +24,7 @@
 // What bounds it. A product of K = 16 takes 49 clocks at N = 64 (41 at 32), not the
 // 32 of its arithmetic: the first operand's 4 KB come from shared memory at 128
 // bytes a clock. 64 sequences x 9 tokens x 32 heads (1500 to 6500 tokens, bf16):
-// 256 us, 625 TFLOP/s, 0.32 of a library product; of some 5900 clocks a tile 3330 are
+// 254 us, 630 TFLOP/s, 0.33 of a library product; of some 5900 clocks a tile 3330 are
 // the products', 1400 the softmax step and its hand-overs, which nothing overlaps
 // because no second tile fits, the rest waits for pieces; an item of 22 tiles has some
 // 20,000 clocks for its queries, first and masked tile and results. 64 x 1 token: 70
@@ -226,10 +226,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     // ---- products: the warp waits together, one lane issues
     constexpr uint32_t id_s = 1u << 4 | B::kFormat << 7 | B::kFormat << 10 | static_cast<uint32_t>(N >> 3) << 17 | 8u << 24;
     constexpr uint32_t id_o = id_s | 3u << 15;  // both operands lie with M (N) contiguous
-    const uint64_t e_desc = moved(smem_desc(smem_addr(ring), 16, 1024, 2), 0), s_desc = moved(smem_desc(smem_addr(sh), 16, 1024, 2), 0),
-                   q_desc = moved(smem_desc(smem_addr(q_smem), 16, 1024, 2), 0),
-                   c_desc = moved(smem_desc(smem_addr(ring), kTile * 128, 1024, 2), 0),
-                   p_desc = moved(smem_desc(smem_addr(sh), kTile * 128, 1024, 2), 0);
+    const uint64_t e_desc = smem_desc(smem_addr(ring), 16, 1024, 2), s_desc = smem_desc(smem_addr(sh), 16, 1024, 2),
+                   q_desc = smem_desc(smem_addr(q_smem), 16, 1024, 2),
+                   c_desc = smem_desc(smem_addr(ring), kTile * 128, 1024, 2),
+                   p_desc = smem_desc(smem_addr(sh), kTile * 128, 1024, 2);
     Items<N, kCost> it(a, start, my_units);
     bool ok = true;
     uint32_t f = 0;  // pieces so far
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       for (int t = t0; t < t1; ++t, ++i) {
 #pragma unroll
         for (int p = 0; p < pieces; ++p) {
-          const uint32_t slot = uniform((f + p) % NP);
+          const uint32_t slot = (f + p) % NP;
           ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.full[slot]), ((f + p) / NP) & 1, gave_up));
           if (!ok) break;
           fence_after();
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         fence_after();
 #pragma unroll
         for (int p = 0; p < pieces; ++p) {
-          const uint32_t from = uniform((f + p) % NP);
+          const uint32_t from = (f + p) % NP;
           const uint64_t cd = moved(c_desc, from * kPiece);
           const uint32_t to = tmem + C::kO + 64 * p;
           if (elect()) {

@@ -19,12 +19,12 @@
 // first in a tile's scores, so that the values, which their own product gives back
 // last, are asked for as late as possible (long contexts 966 -> 719 us).
 //
-// What bounds it. Two sequences of 110,000 to 131,072 tokens x 9 x 128 heads, bf16: 685
-// us, 912 TFLOP/s, 0.47 of a library product and 0.72 with the scores counted twice;
+// What bounds it. Two sequences of 110,000 to 131,072 tokens x 9 x 128 heads, bf16: 675
+// us, 926 TFLOP/s, 0.48 of a library product and 0.73 with the scores counted twice;
 // 2700 clocks a tile, of which the products take 1990, then waits for the values'
-// piece and those of the issuing warp. 16 trees of 61 tokens x 16 heads, fp16: 143
+// piece and those of the issuing warp. 16 trees of 61 tokens x 16 heads, fp16: 142
 // us, tensor pipe busy for 40%; an item's queries, first maximum, masked tiles and
-// results take a third. 256 dimensions (three prompts of 500 to 1500): 150 us, 860 TFLOP/s.
+// results take a third. 256 dimensions (three prompts of 500 to 1500): 146 us, 885 TFLOP/s.
 #include <string.h>
 
 #include "latent_attn.cuh"
@@ -167,10 +167,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     constexpr uint32_t format = 1u << 4 | B::kFormat << 7 | B::kFormat << 10 | static_cast<uint32_t>(kRows >> 4) << 24;
     constexpr uint32_t id_s = format | static_cast<uint32_t>(kSlots >> 3) << 17;
     constexpr uint32_t id_o = format | 1u << 16 | static_cast<uint32_t>(vd >> 3) << 17;  // the entries lie with N contiguous
-    const uint64_t e_desc = moved(smem_desc(smem_addr(ring), 16, 1024, 2), 0), s_desc = moved(smem_desc(smem_addr(sh), 16, 1024, 2), 0),
-                   q_desc = moved(smem_desc(smem_addr(q_smem), 16, 1024, 2), 0),
+    const uint64_t e_desc = smem_desc(smem_addr(ring), 16, 1024, 2), s_desc = smem_desc(smem_addr(sh), 16, 1024, 2),
+                   q_desc = smem_desc(smem_addr(q_smem), 16, 1024, 2),
                    r_desc = moved(q_desc, (halves - 1) * pc * kQChunk),
-                   c_desc = moved(smem_desc(smem_addr(ring), kChunk, 1024, 2), 0);
+                   c_desc = smem_desc(smem_addr(ring), kChunk, 1024, 2);
     Items<kRows, kCost> it(a, start, my_units);
     bool ok = true;
     uint32_t f = 0;  // pieces whose scores are begun
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (ok) fence_after();
           return ok;
         };
-        uint32_t slot = uniform(f % kPieces);
+        uint32_t slot = f % kPieces;
         if (!ready(slot)) return false;
         const uint64_t sd = moved(s_desc, slot / halves * kChunk);
         if (halves == 2) {
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
           __syncwarp();
           ++f;
-          slot = uniform(f % kPieces);
+          slot = f % kPieces;
           if (!ready(slot)) return false;
         }
         ++f;
