@@ -612,7 +612,8 @@ int spec_latent_attention(const spec_latent_cache* cache, const void* queries, i
 
 /* spec_kv8_compact for this cache, in every one of n_planes pools (layers) that
  * share the block table, stride_plane bytes apart (a multiple of 16). Entries keep
- * their bytes. D <= 256; n_planes < 2^24. */
+ * their bytes. new_len and row_status may each be cache_len or accept_len itself (in
+ * place); overlapping them otherwise is refused. D <= 256; n_planes < 2^24. */
 int spec_latent_compact(const spec_latent_cache* cache, int n_planes, int64_t stride_plane, const int32_t* path, int D,
                         const int32_t* accept_len, int32_t* new_len, int32_t* row_status, void* stream);
 

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "common.cuh"
 
 namespace specv {
@@ -261,6 +263,34 @@ inline cudaError_t launch_pdl(void (*kernel)(Args), dim3 grid, dim3 block, cudaS
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+// A compaction: its entries move and its lengths are written in one launch. Where the lengths are written over those that every
+// thread block of a sequence reads, they are left to a launch behind the moves (one thread block a sequence has none to race
+// with).
+constexpr int kMoveEntries = 1, kWriteLengths = 2;
+template <typename Args>
+inline cudaError_t launch_compaction(void (*kernel)(Args), dim3 grid, dim3 block, cudaStream_t st, Args a) {
+  const bool apart = a.in_place && grid.x > 1;
+  a.what = apart ? kMoveEntries : kMoveEntries | kWriteLengths;
+  const cudaError_t e = launch_pdl(kernel, grid, block, st, a);
+  if (e != cudaSuccess || !apart) return e;
+  a.what = kWriteLengths;
+  return launch_pdl(kernel, dim3(1, grid.y), block, st, a);
+}
+
+// Whether a compaction's outputs [B] may lie where they do: each is one of the arrays of lengths that the call reads, or meets
+// none of them.
+inline bool lengths_in_place(const int32_t* cache_len, const int32_t* accept_len, const int32_t* new_len,
+                             const int32_t* row_status, int B, bool* in_place) {
+  *in_place = false;
+  for (const int32_t* in : {cache_len, accept_len})
+    for (const int32_t* out : {new_len, row_status}) {
+      const uintptr_t i = reinterpret_cast<uintptr_t>(in), o = reinterpret_cast<uintptr_t>(out), n = 4 * static_cast<uintptr_t>(B);
+      if (i == o) *in_place = true;
+      else if (i < o + n && o < i + n) return false;
+    }
+  return true;
 }
 
 }  // namespace specv

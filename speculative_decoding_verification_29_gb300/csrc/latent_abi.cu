@@ -5,6 +5,7 @@
 
 #include <algorithm>
 
+#include "internal.h"
 #include "latent.h"
 #include "paged.h"
 
@@ -203,6 +204,7 @@ int spec_latent_compact(const spec_latent_cache* cache, int n_planes, int64_t st
   if (rc != SPEC_OK) return rc;
   if (!accept_len || !new_len || !row_status || n_planes < 1 || (path && D < 1)) return SPEC_ERR_ARG;
   if (stride_plane < 0 || (stride_plane & 15)) return SPEC_ERR_ARG;
+  if (!lengths_in_place(cache->cache_len, accept_len, new_len, row_status, cache->B, &a.in_place)) return SPEC_ERR_ARG;
   if (path && D > kLatentMaxPath) return SPEC_ERR_UNSUPPORTED;
   if (n_planes >= (1 << 24) || stride_plane >= (1LL << 46)) return SPEC_ERR_UNSUPPORTED;
   a.planes = n_planes;

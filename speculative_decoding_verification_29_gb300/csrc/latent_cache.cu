@@ -279,11 +279,11 @@ __global__ void __launch_bounds__(kCompactThreads) latent_compact_kernel(const _
   }
   __syncthreads();
   const int state = s_state;
-  if (blockIdx.x == 0 && tid == 0) {
+  if (blockIdx.x == 0 && tid == 0 && (a.what & kWriteLengths)) {
     a.new_len[b] = state >= 1 ? base + L + 1 : -1;
     a.row_status[b] = state < 0 ? -state : 0;
   }
-  if (state != 1) return;
+  if (state != 1 || !(a.what & kMoveEntries)) return;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kCompactThreads + tid;  // plane, column
   const int plane = static_cast<int>(item / a.cols), col = static_cast<int>(item - static_cast<int64_t>(plane) * a.cols);
   if (plane >= a.planes) return;
@@ -310,7 +310,7 @@ cudaError_t launch_latent_append(const LatentAppendArgs& a, int dtype, int cache
 cudaError_t launch_latent_compact(const LatentCompactArgs& a, cudaStream_t st) {
   const int64_t items = static_cast<int64_t>(a.planes) * a.cols;
   const dim3 grid(static_cast<unsigned>((items + kCompactThreads - 1) / kCompactThreads), static_cast<unsigned>(a.c.B));
-  return launch_pdl(latent_compact_kernel, grid, dim3(kCompactThreads), st, a);
+  return launch_compaction(latent_compact_kernel, grid, dim3(kCompactThreads), st, a);
 }
 
 }  // namespace specv

@@ -209,7 +209,8 @@ def spec_latent_compact(cache, block_table, cache_len, accept_len, path=None,
     [planes, ...] (any plane stride that is a multiple of 16 bytes). cache_len [B]:
     position of node 0; accept_len [B] and path [B, D] (None for chain
     verification) as returned by the verification call. Returns new_len [B]
-    and row_status [B]."""
+    and row_status [B]; a caller's own out["new_len"] may be cache_len, which
+    then is brought up to date in place."""
     lib = _lib.load()
     W = cache.shape[-1]
     C = (W - 1) // 128 * 128  # entries move whole: how they are divided does not matter here
