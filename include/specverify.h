@@ -392,7 +392,8 @@ int spec_tree_expand(const void* draft_logits, int dtype, float temperature, con
  *                 NULL for chain verification, where path[t] = t and nothing
  *                 moves (1 <= D <= 1024)
  *   accept_len    device [B] int32, the accepted length L of the same call
- * Outputs (device): new_len [B] int32; row_status [B] int32.
+ * Outputs (device): new_len [B] int32; row_status [B] int32. Each may be base_pos
+ * or accept_len itself (in place); overlapping them otherwise is refused.
  * A row with accept_len < 0 (flagged by verification) is left alone:
  * new_len -1, status 0. A row whose path does not start at 0, is not
  * strictly increasing, has L >= D or reaches position S or beyond (or whose
@@ -529,8 +530,9 @@ int spec_kv8_attention(const spec_kv8_cache* cache, const void* queries, int64_t
  * path NULL: chain verification, nothing moves. Rows are checked as by
  * spec_kv_compact (SPEC_ROW_TREE, new_len -1; accept_len < 0: new_len -1,
  * status 0), plus SPEC_ROW_CACHE (new_len -1, nothing moved) for an invalid
- * cache_len or block id. D <= 64. n_planes >= 1; 1 <= n_planes * B * kv_heads
- * < 2^30. */
+ * cache_len or block id. new_len and row_status may each be cache_len or
+ * accept_len itself (in place); overlapping them otherwise is refused. D <= 64.
+ * n_planes >= 1; 1 <= n_planes * B * kv_heads < 2^30. */
 int spec_kv8_compact(const spec_kv8_cache* cache, int n_planes, int64_t stride_plane, int64_t scale_stride_plane,
                      const int32_t* path, int D, const int32_t* accept_len, int32_t* new_len, int32_t* row_status,
                      void* stream);

@@ -629,6 +629,7 @@ int spec_kv_compact(void* kv, int elem_bytes, int n_planes, int B, int S, int W,
   const long long ncol = row_bytes / unit;
   if (ncol * n_planes > 0x7fffffffLL * 256LL || ncol > 0x7fffffffLL) return SPEC_ERR_UNSUPPORTED;
   KvArgs a{};
+  if (!lengths_in_place(base_pos, accept_len, new_len, row_status, B, &a.in_place)) return SPEC_ERR_ARG;
   a.kv = kv;
   a.es = elem_bytes;
   a.P = n_planes;

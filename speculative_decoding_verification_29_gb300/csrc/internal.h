@@ -233,6 +233,8 @@ struct KvArgs {
   const int32_t* acc;    // [B] accept lengths
   int32_t* new_len;      // [B]
   int32_t* row_status;   // [B]
+  int what;              // kMoveEntries, kWriteLengths
+  bool in_place;         // the lengths are written over those that are read
 };
 int kv_max_path();
 cudaError_t launch_kv_compact(const KvArgs& a, int unit, cudaStream_t st);

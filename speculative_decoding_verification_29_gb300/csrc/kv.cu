@@ -67,11 +67,11 @@ __global__ void __launch_bounds__(kKvThreads) kv_compact_kernel(KvArgs a) {
   }
   __syncthreads();
   const int ok = s_ok;
-  if (blockIdx.x == 0 && tid == 0) {
+  if (blockIdx.x == 0 && tid == 0 && (a.what & kWriteLengths)) {
     a.new_len[b] = ok == 1 ? b0 + L + 1 : -1;
     a.row_status[b] = ok == 0 ? SPEC_ROW_TREE : 0;
   }
-  if (ok != 1 || !a.path || L < 1) return;  // a chain moves nothing
+  if (ok != 1 || !a.path || L < 1 || !(a.what & kMoveEntries)) return;  // a chain moves nothing
   const long long item = static_cast<long long>(blockIdx.x) * kKvThreads + tid;
   if (item >= static_cast<long long>(a.P) * a.ncol) return;
   const int p = static_cast<int>(item / a.ncol);
@@ -103,9 +103,9 @@ cudaError_t launch_kv_compact(const KvArgs& a, int unit, cudaStream_t st) {
   const long long items = static_cast<long long>(a.P) * a.ncol;
   const dim3 grid(static_cast<unsigned>((items + kKvThreads - 1) / kKvThreads), static_cast<unsigned>(a.B));
   const dim3 block(kKvThreads);
-  if (unit == 16) return launch_pdl(kv_compact_kernel<uint4>, grid, block, st, a);
-  if (unit == 4) return launch_pdl(kv_compact_kernel<uint32_t>, grid, block, st, a);
-  return launch_pdl(kv_compact_kernel<uint8_t>, grid, block, st, a);
+  if (unit == 16) return launch_compaction(kv_compact_kernel<uint4>, grid, block, st, a);
+  if (unit == 4) return launch_compaction(kv_compact_kernel<uint32_t>, grid, block, st, a);
+  return launch_compaction(kv_compact_kernel<uint8_t>, grid, block, st, a);
 }
 
 }  // namespace specv

@@ -58,6 +58,8 @@ struct Kv8CompactArgs {
   const int32_t* acc;
   int32_t* new_len;
   int32_t* row_status;
+  int what;       // kMoveEntries, kWriteLengths
+  bool in_place;  // the lengths are written over those that are read
 };
 cudaError_t launch_kv8_compact(const Kv8CompactArgs& a, cudaStream_t st);
 

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 
+#include "internal.h"
 #include "kv8.h"
 #include "paged.h"
 
@@ -208,6 +209,7 @@ int spec_kv8_compact(const spec_kv8_cache* cache, int n_planes, int64_t stride_p
   if (rc != SPEC_OK) return rc;
   if (!accept_len || !new_len || !row_status || n_planes < 1 || (path && D < 1)) return SPEC_ERR_ARG;
   if (stride_plane < 0 || scale_stride_plane < 0 || (stride_plane & 15)) return SPEC_ERR_ARG;
+  if (!lengths_in_place(cache->cache_len, accept_len, new_len, row_status, cache->B, &a.in_place)) return SPEC_ERR_ARG;
   if (path && D > kKv8MaxPath) return SPEC_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(n_planes) * a.c.B * a.c.H >= (1LL << 30) || stride_plane >= (1LL << 46) ||
       scale_stride_plane >= (1LL << 46))

@@ -411,11 +411,11 @@ __global__ void __launch_bounds__(kCompWarps * 32) kv8_compact_kernel(const __gr
   }
   __syncthreads();
   const int state = s_state;
-  if (blockIdx.x == 0 && tid == 0) {
+  if (blockIdx.x == 0 && tid == 0 && (a.what & kWriteLengths)) {
     a.new_len[b] = state >= 1 ? base + L + 1 : -1;
     a.row_status[b] = state < 0 ? -state : 0;
   }
-  if (state != 1) return;
+  if (state != 1 || !(a.what & kMoveEntries)) return;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kCompWarps + warp;  // plane, keys or values, head
   if (item >= static_cast<int64_t>(a.planes) * 2 * a.c.H) return;
   const int h = static_cast<int>(item % a.c.H);
@@ -511,8 +511,8 @@ cudaError_t launch_kv8_compact(const Kv8CompactArgs& a, cudaStream_t st) {
   const int64_t items = static_cast<int64_t>(a.planes) * 2 * a.c.H;
   const dim3 grid(static_cast<unsigned>((items + kCompWarps - 1) / kCompWarps), static_cast<unsigned>(a.c.B));
   const dim3 block(kCompWarps * 32);
-  return a.c.D == 128 ? launch_pdl(kv8_compact_kernel<128>, grid, block, st, a)
-                      : launch_pdl(kv8_compact_kernel<64>, grid, block, st, a);
+  return a.c.D == 128 ? launch_compaction(kv8_compact_kernel<128>, grid, block, st, a)
+                      : launch_compaction(kv8_compact_kernel<64>, grid, block, st, a);
 }
 
 }  // namespace specv

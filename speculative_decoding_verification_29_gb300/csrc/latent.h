@@ -44,7 +44,7 @@ struct LatentCompactArgs {
   const int32_t* acc;
   int32_t* new_len;
   int32_t* row_status;
-  int what;  // kMoveEntries, kWriteLengths
+  int what;       // kMoveEntries, kWriteLengths
   bool in_place;  // the lengths are written over those that are read
 };
 cudaError_t launch_latent_compact(const LatentCompactArgs& a, cudaStream_t st);

@@ -28,7 +28,18 @@ def latent(lib, new_len=OUT, status=STATUS):
     return lib.spec_latent_compact(ctypes.byref(c), 32, 1 << 24, P, 8, ACC, new_len, status, None)
 
 
-CALLS = [latent]
+def kv8(lib, new_len=OUT, status=STATUS):
+    from speculative_decoding_verification_29_gb300 import _lib
+
+    c = _lib.Kv8Cache(P, P, P, P, P + (5 << 32), LEN, B, 100, 20, 32, 8, 128, 8 * 32 * 128, 32 * 128, 128)
+    return lib.spec_kv8_compact(ctypes.byref(c), 32, 1 << 24, 1 << 16, P, 8, ACC, new_len, status, None)
+
+
+def kv(lib, new_len=OUT, status=STATUS):
+    return lib.spec_kv_compact(P, 2, 64, B, 100, 1024, B * 102400, 102400, 1024, LEN, P, 8, ACC, new_len, status, None)
+
+
+CALLS = [latent, kv8, kv]
 
 
 @pytest.mark.parametrize("call", CALLS)

@@ -66,3 +66,33 @@ def test_latent(planes, chain):
         return sv().spec_latent_compact(caches[0], t, n, a, None if chain else p.cuda(), out=out)
 
     same_in_place(call, lambda: [pool.cuda()], lens, acc, path)
+
+
+@pytest.mark.parametrize("planes", [1, 24])
+@pytest.mark.parametrize("chain", [False, True])
+def test_kv8(planes, chain):
+    B, bs, H, D = 70, 16, 8, 128
+    lens, acc, path = steps(B, seed=6)
+    M = 7
+    g = torch.Generator().manual_seed(7)
+    table = torch.randperm(B * M, generator=g).to(I32).view(B, M).cuda()
+    codes = torch.randint(0, 127, (2, planes, B * M, H, bs, D), generator=g, dtype=torch.uint8)  # finite ones
+    scales = torch.randint(120, 134, (2, planes, B * M, H), generator=g, dtype=torch.uint8)
+
+    def call(caches, n, a, p, out):
+        return sv().spec_kv8_compact(*caches, table, n, a, None if chain else p.cuda(), out=out)
+
+    same_in_place(call, lambda: [codes[0].cuda(), codes[1].cuda(), scales[0].cuda(), scales[1].cuda()], lens, acc, path)
+
+
+@pytest.mark.parametrize("planes,W", [(1, 8), (64, 1024), (64, 1001)])
+@pytest.mark.parametrize("chain", [False, True])
+def test_kv(planes, W, chain):
+    B = 9
+    lens, acc, path = steps(B, seed=8)
+    kv = torch.randn(planes, B, 110, W, generator=torch.Generator().manual_seed(9)).to(torch.bfloat16)
+
+    def call(caches, n, a, p, out):
+        return sv().spec_kv_compact(caches[0], n, a, None if chain else p.cuda(), out=out)
+
+    same_in_place(call, lambda: [kv.cuda()], lens, acc, path)
