@@ -275,8 +275,9 @@ def spec_pages_update(block_table, cache_len, refs, pools=(), *, planes: bool = 
     or, with ``planes``, [planes, num_blocks, ...] of layers that share the table
     (a latent cache; codes and scales of an 8-bit cache), the elements of a block
     contiguous. block: tokens of a block (None: the second last dimension of the
-    first pool, as all caches here have it). Returns block_table (the given one where source is None
-    and out has none), cache_len [B] (the tokens kept), row_status [B], and refs. A
+    first pool, as all caches here have it). out: cache_len, row_status and, where the
+    rows are to go elsewhere, block_table; it is not changed. Returns block_table (without one in out: the
+    given one, or with source a new one), cache_len [B] (the tokens kept), row_status [B], and refs. A
     sequence with SPEC_ROW_CACHE in row_status must not be appended to."""
     lib = _lib.load()
     dev, at = block_table.device, block_table.get_device()
@@ -306,7 +307,9 @@ def spec_pages_update(block_table, cache_len, refs, pools=(), *, planes: bool = 
     else:
         _whole(out["cache_len"], "out's cache_len", dev, at, B)
         _whole(out["row_status"], "row_status", dev, at, B)
-    table = out.setdefault("block_table", block_table if source is None else torch.empty_like(block_table))
+    table = out.get("block_table")  # the caller's dict is left as it is: no call's rows become the next one's destination
+    if table is None:
+        table = block_table if source is None else torch.empty_like(block_table)
     _whole(table, "out's block_table", dev, at)
     if table.shape != block_table.shape:
         raise ValueError("out's block_table must have block_table's shape")
@@ -325,5 +328,4 @@ def spec_pages_update(block_table, cache_len, refs, pools=(), *, planes: bool = 
         block_table.data_ptr(), table.data_ptr(), cache_len.data_ptr(), _ptr(keep_len), _ptr(source), _ptr(need),
         refs.data_ptr(), B, M, n, block, recs, len(pools), out["cache_len"].data_ptr(), out["row_status"].data_ptr(),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _queue(stream, at)))
-    out["refs"] = refs
-    return out
+    return dict(out, block_table=table, refs=refs)

@@ -1,0 +1,51 @@
+"""The pages' calls made again: one dict of outputs for several tables."""
+
+import pytest
+import torch
+
+import latent_plain as plain
+from gpu_helpers import need_gpu
+
+pytestmark = pytest.mark.gpu
+I32 = torch.int32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def sv():
+    import speculative_decoding_verification_29_gb300 as m
+
+    return m
+
+
+def i32(*x):
+    return torch.tensor(x, dtype=I32)
+
+
+def test_one_out_for_several_tables():
+    """Each call's rows go into the table that it was given, or with source into a new one, whatever the last call did."""
+    bs = 16
+    tables = [i32([0, 1, -1], [2, -1, -1]), i32([5, -1, -1], [3, 4, -1])]
+    lens = [i32(20, 16), i32(9, 30)]
+    out = dict(cache_len=torch.zeros(2, dtype=I32, device="cuda"), row_status=torch.zeros(2, dtype=I32, device="cuda"))
+    keys = set(out)
+    need = i32(20, 3)
+    for source in (None, i32(1, 1)):
+        for table, length in zip(tables, lens):
+            refs = torch.zeros(12, dtype=I32)
+            for i in table[table >= 0].tolist():
+                refs[i] += 1
+            rows, kept, counts, status, _ = plain.pages(table, length, refs, bs, source=source, need=need)
+            t, r = table.cuda(), refs.cuda()
+            got = sv().spec_pages_update(t, length.cuda(), r, block=bs, need=need.cuda(), out=out,
+                                         source=None if source is None else source.cuda())
+            assert got["block_table"].tolist() == rows and r.tolist() == counts and got["refs"] is r
+            assert got["cache_len"] is out["cache_len"] and out["cache_len"].tolist() == kept
+            assert out["row_status"].tolist() == status
+            assert (got["block_table"] is t) == (source is None)
+            if source is not None:
+                assert torch.equal(t.cpu(), table)
+            assert set(out) == keys
