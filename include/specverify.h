@@ -592,9 +592,10 @@ int spec_latent_append(const spec_latent_cache* cache, const void* latents, int6
  * over the context and those of the step's tokens (appended before) that token i
  * sees, as in spec_kv8_attention. The keys' up-projection is absorbed into q by
  * the caller, the values' is applied to out. A row that sees nothing is 0.
- * Entries that a row does not see do not reach it, finite or not; a row that sees
- * an entry with an infinite or NaN element is NaN, or (an entry of the context
- * whose score is -infinity) NaN in that entry's infinite dimensions only.
+ * Entries that a row does not see do not reach it, finite or not. A row that sees
+ * an entry whose score is NaN or +infinity is NaN. One whose score is -infinity has
+ * no weight: it makes the row NaN in the dimensions in which its latent vector is
+ * infinite, and nowhere else; a row whose entries all have none is 0 otherwise.
  *   queries       device, the cache's type: [T][q_heads] rows of latent_dim +
  *       rot_dim contiguous elements, any strides (elements)
  *   out           device, the cache's type: [T][q_heads] rows of latent_dim

@@ -359,7 +359,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         uint32_t vis = 0xffffffffu;
         if (t >= r.part) {
           // Slots behind the rows' last hold no values, and a value that is not finite must not reach the rows that do not see
-          // it through a weight of 0: both are cleared here, and the rows that see such a one are made NaN at the item's end.
+          // it through a weight of 0: both are cleared here. The scores had it: of the rows that see it, those whose score is
+          // NaN or infinity are NaN, and those whose score is -infinity get a NaN in its dimension at the item's end.
           const int slot = t * kTile + own;
 #pragma unroll 1
           for (int p = group; p < pieces && ok; p += C::G) {
@@ -502,19 +503,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       fence_after();
       {
         const int col = lane < HN ? lane : 0;
-        float s = (sm.sums[group][0][col] + sm.sums[group][1][col]) + (sm.sums[group][2][col] + sm.sums[group][3][col]);
-        if (sm.odd[seg & 1] == seg + 1) {  // set before the weights of its tile were ready
-#pragma unroll 1
-          for (int slot = max(t0, r.part) * kTile; slot < min(r.end, t1 * kTile); ++slot) {
-            const int id = a.c.table[static_cast<int64_t>(r.b) * a.c.max_blocks + slot / a.c.block];
-            if (id < 0 || id >= a.c.num_blocks) continue;
-            const uint16_t* e = reinterpret_cast<const uint16_t*>(a.c.k + id * a.c.sb + (slot % a.c.block) * a.c.ss);
-            bool bad = false;
-            for (int d = lane; d < dims; d += 32) bad |= (e[d] & (B::kExp & 0xffffu)) == (B::kExp & 0xffffu);
-            if (!__any_sync(0xffffffffu, bad)) continue;
-            if (slot < r.ctx || sees(a, r.b, min(r.n - 1, (r0 + col) / a.group), slot - r.ctx)) s = __int_as_float(0x7fffffff);
-          }
-        }
+        const float s = (sm.sums[group][0][col] + sm.sums[group][1][col]) + (sm.sums[group][2][col] + sm.sums[group][3][col]);
         if (lane < HN) {
           sm.inv[warp][lane] = s == 0.f ? 0.f : 1.f / s;
           if (!whole && quarter == 0 && group * HN + lane < r.rows)
@@ -522,6 +511,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
       }
       __syncwarp();
+      const bool cleared = sm.odd[seg & 1] == seg + 1;  // set before the weights of its tile were ready
 #pragma unroll 1
       for (int p = 0; p < pieces; ++p) {
         __syncwarp();
@@ -529,6 +519,21 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         ld_cols<HN>(lanes + C::kO + 64 * p, x);
         wait_ld();
         settle<HN>(x);
+        if (cleared) {  // what it was, times a weight of 0
+#pragma unroll 1
+          for (int slot = max(max(t0, r.part) * kTile, r.ctx); slot < min(r.end, t1 * kTile); ++slot) {
+            const int id = a.c.table[static_cast<int64_t>(r.b) * a.c.max_blocks + slot / a.c.block];
+            if (id < 0 || id >= a.c.num_blocks) continue;
+            const uint16_t* e = reinterpret_cast<const uint16_t*>(a.c.k + id * a.c.sb + (slot % a.c.block) * a.c.ss);
+            const bool bad = (e[128 * p + own] & (B::kExp & 0xffffu)) == (B::kExp & 0xffffu);
+            if (!__any_sync(0xffffffffu, bad)) continue;
+            const bool saw = sees(a, r.b, min(r.n - 1, (r0 + lane) / a.group), slot - r.ctx);  // the group's row `lane`
+            const uint32_t rows = __ballot_sync(0xffffffffu, saw);
+#pragma unroll
+            for (int j = 0; j < HN; ++j)
+              if (bad && (rows >> j) & 1) x[j] = 0x7fffffffu;
+          }
+        }
         if (!whole) {
           float* o = a.part_o + (part * N + group * HN) * dims + 128 * p + own;
 #pragma unroll
