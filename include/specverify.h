@@ -603,8 +603,11 @@ int spec_latent_append(const spec_latent_cache* cache, const void* latents, int6
  *   q_heads       at most 1024
  * Scores, maxima, sums and the accumulated output are fp32. The weights enter the
  * second product rounded to the cache's type, and the sum that divides is that of
- * the rounded weights; a weight is relative to a reference that the row's largest
- * score passes by at most 2^8.
+ * the rounded weights. A weight is relative to a reference, and a row's largest
+ * lies between 1 and 2^8 in bf16, 2^7 and 2^15 in fp16, whose weights below 2^-14
+ * are off by up to 2^-25. The second product's terms are cut at 2^-25 of the running
+ * sum (the tensor cores' addition), so entries further below one that leads do not
+ * reach the result, however many they are.
  * Outputs, workspace (spec_latent_workspace_bytes(...) bytes, 256-byte aligned,
  * no initialisation) and errors as in spec_kv8_attention. */
 size_t spec_latent_workspace_bytes(const spec_latent_cache* cache, int q_heads, int max_tokens);

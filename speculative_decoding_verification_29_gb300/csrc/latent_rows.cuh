@@ -4,8 +4,8 @@
 // Mathematics. out = sum_t 2^(y_t - ref) c_t / sum_t 2^(y_t - ref) with y_t = s
 // log2(e) (q . e_t), e_t the entry (latent vector c_t and shared dimensions).
 // All heads read the same entries, so an item's rows are any 16 to 64 of a
-// sequence's rows (token, head). A row's reference moves only when a tile's
-// largest y passes it by more than 2^8; the accumulators are scaled then, and
+// sequence's rows (token, head). A row's reference is set to its largest y (in
+// fp16 7 below it) and moves only when one passes that by more than 2^8; the accumulators are scaled then, and
 // otherwise a tile needs no maximum at all, only a vote that none is passed.
 //
 // Orientation. Slots are the 128 rows of both products' first operand: scores
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
 #pragma unroll
         for (int j = 0; j < HN; ++j) top = fmaxf(top, y[j]);
-        pass |= top > kPass;
+        pass |= top > kPass + B::kBelow;
         if (!named_all(bar_id, 128, ok && !pass)) {
           if (!named_all(bar_id, 128, ok)) {
             ok = false;
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           named_sync(bar_id, 128);
           const int col = lane < HN ? lane : 0;
           const float m = fmaxf(fmaxf(sm.smax[group][0][col], sm.smax[group][1][col]), fmaxf(sm.smax[group][2][col], sm.smax[group][3][col]));
-          const float old = t == t0 ? kUnset : sm.ref[group * HN + col], now = fmaxf(old, m);
+          const float old = t == t0 ? kUnset : sm.ref[group * HN + col], now = fmaxf(old, m - B::kBelow);
           const float by = t == t0 ? 0.f : ex2_fast(old - now);
           named_sync(bar_id, 128);  // references and maxima have been read
           if (quarter == 0 && lane < HN) sm.ref[group * HN + lane] = now, sm.fac[group * HN + lane] = by;

@@ -391,9 +391,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           top2 = fmaxf(top2, __uint_as_float(x[k + 1]));
         }
         top = fmaxf(top, top2) * a.scale;
-        const bool pass = top > ref + kPass;
+        const bool pass = top > ref + (kPass + B::kBelow);
         if (__any_sync(0xffffffffu, pass)) {
-          const float now = pass ? top : ref, by = pass ? ex2_fast(ref - now) : 1.f;
+          const float now = pass ? top - B::kBelow : ref, by = pass ? ex2_fast(ref - now) : 1.f;
           ref = now;
           sum *= by;
           if (s > s0) {
