@@ -477,6 +477,34 @@ def _kv8_rows(t, name, D, dev, written=False):
     return stride[0], stride[1]
 
 
+def _rows_meet(x, y):
+    """Whether rows of two [tokens, heads, D] activations of the same tokens and heads share memory."""
+    T, H, D = x.shape
+    if T == 0 or H == 0:
+        return False
+    size, (xt, xh, _), (yt, yh, _) = x.element_size(), x.stride(), y.stride()
+    off, V = y.data_ptr() - x.data_ptr(), y.shape[2]
+    if off >= ((T - 1) * xt + (H - 1) * xh + D) * size or -off >= ((T - 1) * yt + (H - 1) * yh + V) * size:
+        return False  # the common case, kept cheap
+    return _meet(T, H, off, xt * size, xh * size, D * size, yt * size, yh * size, V * size)
+
+
+@functools.lru_cache(maxsize=64)
+def _meet(T: int, H: int, off: int, xt: int, xh: int, W: int, yt: int, yh: int, V: int) -> bool:
+    """Whether rows of W bytes at t * xt + h * xh and of V bytes at off + t * yt + h * yh, t < T, h < H, share a byte."""
+    xs, ys = (H - 1) * xh + W, (H - 1) * yh + V
+    if xt == yt and max(xs, ys) <= xt and xs <= off % xt <= xt - ys:
+        return False  # side by side in every token
+    if (xt, xh) == (yt, yh) and xh > 0 and xt % xh == 0 and W <= off % xh <= xh - V:
+        return False  # side by side in every head
+    if T * H > 1 << 24:
+        return True  # not looked at row by row
+    t, h = torch.arange(T, device="cpu")[:, None], torch.arange(H, device="cpu")
+    x, y = (t * xt + h * xh).flatten().sort().values, (off + t * yt + h * yh).flatten()
+    before = torch.searchsorted(x, y + V) - 1  # the last row of x that begins before y's ends
+    return bool(((before >= 0) & (x[before.clamp(min=0)] + W > y)).any())
+
+
 def _kv8_workspace(t, dev):
     if t.device != dev or not t.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
@@ -571,7 +599,7 @@ def spec_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cache
     those with tree_mask[b, i, j] != 0. max_tokens: no sequence has more step
     tokens. sm_scale: head_dim ** -0.5 when None. Returns out (like q) and
     row_status [B]; a caller's own out["out"] may have any token and head
-    strides, but must not be q."""
+    strides, but must not overlap q."""
     lib = _lib.load()
     cache, dev = _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len)
     qst, qsh = _kv8_rows(q, "q", cache.head_dim, dev)
@@ -594,8 +622,8 @@ def spec_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cache
     ost, osh = _kv8_rows(o, "out", cache.head_dim, dev, True)
     if o.shape != q.shape or o.dtype != q.dtype:
         raise ValueError("out must have q's shape and type")
-    if T and o.data_ptr() == q.data_ptr():
-        raise ValueError("out must not be q: queries are read again after the first results were written")
+    if _rows_meet(q, o):
+        raise ValueError("out must not overlap q: queries are read again after the first results were written")
     if workspace is None:
         nbytes = lib.spec_kv8_workspace_bytes(ctypes.byref(cache), hq, max_tokens, code)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)

@@ -12,7 +12,7 @@ import torch
 
 from . import _lib
 from ._lib import SPEC_BF16, SPEC_F16, SPEC_F32, check
-from .api import _here, _int32, _kv8_rows, _kv8_workspace, _on_stream, _ptr, _raw_stream, _stream, alloc_workspace
+from .api import _here, _int32, _kv8_rows, _kv8_workspace, _on_stream, _ptr, _raw_stream, _rows_meet, _stream, alloc_workspace
 
 _DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
 
@@ -163,7 +163,7 @@ def spec_latent_attention(q, cache, block_table, cache_len, cu_tokens, *, max_to
     sm_scale: of the scores; the heads' own key dimension decides it, which the
     cache does not know. Returns out [T, q_heads, value_dim], to which the
     caller applies the values' up-projection, and row_status [B]; a caller's
-    own out["out"] may have any token and head strides, but must not be q."""
+    own out["out"] may have any token and head strides, but must not overlap q."""
     lib = _lib.load()
     rec, dev, at = _cache(cache, block_table, cache_len, value_dim)
     qst, qsh = _kv8_rows(q, "q", cache.shape[2], dev)
@@ -184,8 +184,8 @@ def spec_latent_attention(q, cache, block_table, cache_len, cu_tokens, *, max_to
     ost, osh = _kv8_rows(o, "out", value_dim, dev, True)
     if o.shape != (T, hq, value_dim) or o.dtype != q.dtype:
         raise ValueError(f"out must be [{T}, {hq}, {value_dim}] of q's type")
-    if T and o.data_ptr() == q.data_ptr():
-        raise ValueError("out must not be q: queries are read again after the first results were written")
+    if _rows_meet(q, o):
+        raise ValueError("out must not overlap q: queries are read again after the first results were written")
     if workspace is None:
         nbytes = _attention_bytes(rec.block, value_dim, rec.rot_dim, hq, max_tokens)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
