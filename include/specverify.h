@@ -459,7 +459,8 @@ typedef struct {
  *       at position 2^31 as at 1. rot_dim: a multiple of 16 up to head_dim.
  *   interleaved   0: pair i is (i, i + rot_dim / 2); 1: (2 i, 2 i + 1)
  *   queries, queries_out  device or NULL: [T][q_heads] rows of the same dtype
- *       and strides of their own, rotated alike (queries_out may be queries).
+ *       and strides of their own, rotated alike (queries_out may be queries with
+ *       the same strides, and must not overlap them otherwise).
  * Scales: a token needs the least 2^e in range with max |x| <= 448 * 2^e over
  * its finite entries. A block whose first slot this call writes gets the
  * largest need of its tokens; a block that already holds tokens keeps its
@@ -574,7 +575,8 @@ typedef struct {
  *       weight (eps >= 0, finite)
  *   queries, queries_out  device or NULL: [T][q_heads] rows of rot_dim elements
  *       of type `dtype` with strides of their own, for example the tails of the
- *       rows that spec_latent_attention reads (queries_out may be queries)
+ *       rows that spec_latent_attention reads (queries_out may be queries with the
+ *       same strides, and must not overlap them otherwise)
  * Computed in fp32 and rounded once. Output: row_status [B] int32 as by
  * spec_kv8_append. Two sequences must not write the same slot.
  * Errors: SPEC_ERR_ARG for NULL pointers, sizes, types or strides outside the

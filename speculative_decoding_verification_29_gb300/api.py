@@ -489,6 +489,12 @@ def _rows_meet(x, y):
     return _meet(T, H, off, xt * size, xh * size, D * size, yt * size, yh * size, V * size)
 
 
+def _meets_itself(x, y):
+    """Whether y, of x's shape, is written over other rows of x than its own."""
+    same = x.data_ptr() == y.data_ptr() and all(n < 2 or a == b for n, a, b in zip(x.shape, x.stride(), y.stride()))
+    return not same and _rows_meet(x, y)
+
+
 @functools.lru_cache(maxsize=64)
 def _meet(T: int, H: int, off: int, xt: int, xh: int, W: int, yt: int, yh: int, V: int) -> bool:
     """Whether rows of W bytes at t * xt + h * xh and of V bytes at off + t * yt + h * yh, t < T, h < H, share a byte."""
@@ -547,11 +553,14 @@ def spec_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache
     qst = qsh = ost = osh = hq = 0
     if q is not None:
         qst, qsh = _kv8_rows(q, "q", D, dev)
-        if q_out is None:
+        given = q_out is not None
+        if not given:
             q_out = torch.empty_like(q)
         ost, osh = _kv8_rows(q_out, "q_out", D, dev, True)
         if q.dtype != k.dtype or q_out.dtype != q.dtype or q.shape[0] != T or q_out.shape != q.shape:
             raise ValueError("q and q_out must be [tokens, q_heads, head_dim] of the keys' type")
+        if given and _meets_itself(q, q_out):
+            raise ValueError("q_out must be q or not overlap it")
         hq = q.shape[1]
     rot, freq, held = 0, None, None
     if inv_freq is not None:

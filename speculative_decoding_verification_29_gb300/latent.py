@@ -12,7 +12,7 @@ import torch
 
 from . import _lib
 from ._lib import SPEC_BF16, SPEC_F16, SPEC_F32, check
-from .api import _here, _int32, _kv8_rows, _kv8_workspace, _on_stream, _ptr, _raw_stream, _rows_meet, _stream, alloc_workspace
+from .api import _here, _int32, _kv8_rows, _kv8_workspace, _meets_itself, _on_stream, _ptr, _raw_stream, _rows_meet, _stream, alloc_workspace
 
 _DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
 
@@ -108,11 +108,14 @@ def spec_latent_append(latent, rope_key, cache, block_table, cache_len, cu_token
     qst = qsh = ost = osh = hq = 0
     if q_rope is not None:
         qst, qsh = _kv8_rows(q_rope, "q_rope", R, dev)
-        if q_out is None:
+        given = q_out is not None
+        if not given:
             q_out = q_rope.new_empty(q_rope.shape)
         ost, osh = _kv8_rows(q_out, "q_out", R, dev, True)
         if q_rope.dtype != latent.dtype or q_out.dtype != q_rope.dtype or q_rope.shape[0] != T or q_out.shape != q_rope.shape:
             raise ValueError("q_rope and q_out must be [tokens, q_heads, rot_dim] of latent's type")
+        if given and _meets_itself(q_rope, q_out):
+            raise ValueError("q_out must be q_rope or not overlap it")
         hq = q_rope.shape[1]
     if isinstance(inv_freq, torch.Tensor):
         held = inv_freq.detach().to("cpu", torch.float64).contiguous()

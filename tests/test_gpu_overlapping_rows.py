@@ -66,3 +66,30 @@ def test_overlaps(make, heads):
         with pytest.raises(ValueError, match="overlap"):
             call(rows, out=dict(out=o, row_status=status))
     assert torch.equal(q, keep)
+
+
+@pytest.mark.parametrize("kv", [False, True])
+def test_rotated_queries(kv):
+    """In place and side by side with the queries, but not over other rows of them."""
+    freq = [0.5 ** i for i in range(16)]
+    if kv:
+        c = kv8_plain.Cache([40, 7], [3, 2], 2, 64, 16, seed=4).fill()
+        args, cu, D = c.to("cuda"), c.cu.cuda(), 64
+        x = torch.randn(5, 2, 64, generator=torch.Generator().manual_seed(5)).to(BF).cuda()
+        call = lambda q, o: sv().spec_kv8_append(x, x, *args, cu, inv_freq=freq, q=q, q_out=o)["q_out"]  # noqa: E731
+    else:
+        c = latent_plain.Cache([40, 7], [3, 2], 128, 32, 16, BF, seed=4).fill()
+        args, cu, D = c.to("cuda"), c.cu.cuda(), 32
+        x = torch.randn(5, 160, generator=torch.Generator().manual_seed(5)).to(BF).cuda()
+        call = lambda q, o: sv().spec_latent_append(x[:, :128], x[:, 128:], *args, cu, inv_freq=freq, q_rope=q, q_out=o)["q_out"]  # noqa: E731
+    wide = torch.randn(6, 4, 2 * D, generator=torch.Generator().manual_seed(6)).to(BF).cuda()
+    q = wide[:5, :, :D]
+    want, keep = call(q, None).clone(), wide.clone()
+    with pytest.raises(ValueError, match="overlap"):
+        call(q, wide[1:, :, :D])
+    with pytest.raises(ValueError, match="overlap"):
+        call(q, wide[:5, :, D // 2: D // 2 + D])
+    assert torch.equal(wide, keep)
+    assert torch.equal(call(q, wide[:5, :, D:]), want)
+    assert torch.equal(wide[:5, :, :D], keep[:5, :, :D])
+    assert torch.equal(call(q, q), want)
