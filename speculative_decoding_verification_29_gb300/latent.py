@@ -278,7 +278,7 @@ def spec_pages_update(block_table, cache_len, refs, pools=(), *, planes: bool = 
     or, with ``planes``, [planes, num_blocks, ...] of layers that share the table
     (a latent cache; codes and scales of an 8-bit cache), the elements of a block
     contiguous. block: tokens of a block (None: the second last dimension of the
-    first pool, as all caches here have it). out: cache_len, row_status and, where the
+    first pool, as the latent cache and the codes of an 8-bit one have it; a pool of scales does not tell it). out: cache_len, row_status and, where the
     rows are to go elsewhere, block_table; it is not changed. Returns block_table (without one in out: the
     given one, or with source a new one), cache_len [B] (the tokens kept), row_status [B], and refs. A
     sequence with SPEC_ROW_CACHE in row_status must not be appended to."""
@@ -300,8 +300,8 @@ def spec_pages_update(block_table, cache_len, refs, pools=(), *, planes: bool = 
             if t.numel() != B:
                 raise ValueError(f"{name} must have B entries")
     if block is None:
-        if not len(pools):
-            raise ValueError("block is needed where no pool tells it")
+        if not len(pools) or pools[0].dim() < 3 + planes:
+            raise ValueError("block is needed where the first pool does not tell it: [..., block, elements of a token]")
         block = pools[0].shape[-2]
     n = refs.numel()
     recs = _pages_pools(pools, n, dev, planes)

@@ -1,4 +1,4 @@
-"""The pages' calls made again: one dict of outputs for several tables."""
+"""The pages' calls made again: one dict of outputs for several tables, and what of the pools a call may not guess."""
 
 import pytest
 import torch
@@ -49,3 +49,18 @@ def test_one_out_for_several_tables():
             if source is not None:
                 assert torch.equal(t.cpu(), table)
             assert set(out) == keys
+
+
+def test_a_block_that_no_pool_tells():
+    """The scales of an 8-bit cache, [blocks, heads], have no dimension of tokens: block is asked for."""
+    table, length, refs, need = i32([0, 1, -1], [2, -1, -1]).cuda(), i32(20, 16).cuda(), i32(1, 1, 1, 0, 0, 0).cuda(), i32(1, 1).cuda()
+    scales = torch.zeros(6, 4, dtype=torch.uint8, device="cuda")
+    codes = torch.zeros(6, 4, 16, 64, dtype=torch.uint8, device="cuda")
+    for pools, planes in (((scales, codes), False), ((scales[None], codes[None]), True), ((torch.zeros(6, 16, device="cuda"),), False)):
+        with pytest.raises(ValueError, match="block is needed"):
+            sv().spec_pages_update(table, length, refs, pools, planes=planes, need=need)
+    assert table.tolist() == [[0, 1, -1], [2, -1, -1]] and refs.tolist() == [1, 1, 1, 0, 0, 0]
+    r = sv().spec_pages_update(table, length, refs, (codes, scales), need=need)
+    assert r["block_table"].tolist() == [[0, 1, -1], [2, 3, -1]]
+    r = sv().spec_pages_update(table, length, refs, (scales, codes), block=16, keep_len=i32(20, 17 - 1).cuda())
+    assert r["block_table"].tolist() == [[0, 1, -1], [2, -1, -1]]
