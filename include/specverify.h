@@ -662,7 +662,8 @@ int spec_latent_compact(const spec_latent_cache* cache, int n_planes, int64_t st
  *   workspace     spec_pages_workspace_bytes(...) bytes, 256-byte aligned, needing
  *       no initialisation
  * Errors: SPEC_ERR_ARG, SPEC_ERR_WORKSPACE as usual; SPEC_ERR_UNSUPPORTED for B >
- * 65535, max_blocks > 2^27, max_blocks * block > 2^31 - 128 or n_pools > 8. */
+ * 65535, max_blocks > 2^27, max_blocks * block > 2^31 - 128, num_blocks > 2^30 or
+ * n_pools > 8. */
 typedef struct {
   void* data; /* device */
   int32_t n_planes;

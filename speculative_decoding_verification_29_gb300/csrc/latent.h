@@ -86,6 +86,7 @@ struct PagesArgs {
   int chunks;
 };
 constexpr int kPagesChunk = 1024;
+constexpr int kPagesMaxBlocks = 1 << 30;  // a search that adds 4096 at a time stays below 2^31
 cudaError_t launch_pages_update(const PagesArgs& a, cudaStream_t st);
 
 }  // namespace specv

@@ -219,7 +219,7 @@ int spec_latent_compact(const spec_latent_cache* cache, int n_planes, int64_t st
 }
 
 size_t spec_pages_workspace_bytes(int B, int max_blocks, int num_blocks) {
-  if (B < 1 || max_blocks < 1 || num_blocks < 1 || B > kMaxB || max_blocks > (1 << 27)) return 0;
+  if (B < 1 || max_blocks < 1 || num_blocks < 1 || B > kMaxB || max_blocks > (1 << 27) || num_blocks > kPagesMaxBlocks) return 0;
   const size_t chunks = (max_blocks + kPagesChunk - 1) / kPagesChunk, n = num_blocks;
   return 3 * up256(n * 4) + up256(B * chunks * 4) + up256(2 * B * sizeof(int4)) + up256(B * sizeof(int2)) + 256;
 }
@@ -231,7 +231,8 @@ int spec_pages_update(const int32_t* block_table, int32_t* new_table, const int3
   if (!block_table || !new_table || !cache_len || !refs || !new_len || !row_status) return SPEC_ERR_ARG;
   if (B < 1 || max_blocks < 1 || num_blocks < 1 || block < 1 || n_pools < 0 || (n_pools > 0 && !pools)) return SPEC_ERR_ARG;
   if ((source && new_table == block_table) || new_len == cache_len) return SPEC_ERR_ARG;
-  if (B > kMaxB || max_blocks > (1 << 27) || static_cast<int64_t>(max_blocks) * block > kMaxTokens || n_pools > kMaxPools)
+  if (B > kMaxB || max_blocks > (1 << 27) || static_cast<int64_t>(max_blocks) * block > kMaxTokens || n_pools > kMaxPools ||
+      num_blocks > kPagesMaxBlocks)
     return SPEC_ERR_UNSUPPORTED;
   PagesArgs a{};
   for (int i = 0; i < n_pools; ++i) {
