@@ -234,6 +234,9 @@ int spec_pages_update(const int32_t* block_table, int32_t* new_table, const int3
   if (B > kMaxB || max_blocks > (1 << 27) || static_cast<int64_t>(max_blocks) * block > kMaxTokens || n_pools > kMaxPools ||
       num_blocks > kPagesMaxBlocks)
     return SPEC_ERR_UNSUPPORTED;
+  const uintptr_t rows = 4 * static_cast<uintptr_t>(B) * max_blocks, before = reinterpret_cast<uintptr_t>(block_table),
+                  after = reinterpret_cast<uintptr_t>(new_table);
+  if (before != after && before < after + rows && after < before + rows) return SPEC_ERR_ARG;
   PagesArgs a{};
   for (int i = 0; i < n_pools; ++i) {
     const spec_pages_pool& p = pools[i];

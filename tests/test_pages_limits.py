@@ -29,3 +29,14 @@ def test_pools_of_very_many_blocks(lib):
     assert lib.spec_pages_workspace_bytes(4, 20, 1 << 30) > 3 << 32
     for nb in ((1 << 30) + 1, (1 << 31) - 4096, (1 << 31) - 1):
         assert pages(lib, nb=nb) == LIMIT and lib.spec_pages_workspace_bytes(4, 20, nb) == 0
+
+
+def test_new_rows_over_old_ones(lib):
+    """The rows after the call lie where the old ones do, or in memory of their own: rows of other sequences are read."""
+    B, M = 4, 20
+    assert pages(lib) == CUDA and pages(lib, source=P + (6 << 32)) == ARG
+    for source in (None, P + (6 << 32)):
+        for off in (4, -4, 4 * M, -4 * M, 4 * (B * M - 1), 4 - 4 * B * M):
+            assert pages(lib, new=P + off, source=source) == ARG
+        for off in (4 * B * M, -4 * B * M):
+            assert pages(lib, new=P + off, source=source) == CUDA
