@@ -645,7 +645,10 @@ int spec_latent_compact(const spec_latent_cache* cache, int n_planes, int64_t st
  *      are all that hold it, the last keeps it.
  * Blocks are taken lowest id first, in the order of the sequences; blocks freed in
  * step 1 can be taken in step 2. Where they do not suffice, that sequence and all
- * later ones that need room take none.
+ * later ones with need > 0 take none and are marked in row_status, also those whose
+ * tokens would fit in the block that they hold last (a sequence that found no copy
+ * of it may hold it still). All keep their tokens: a further call with need 0 for
+ * sequences that have to wait serves the others.
  *   block_table   device [B][max_blocks] int32
  *   new_table     device, the rows after the call: block_table itself, unless
  *       source is given, or memory that does not overlap it
@@ -658,7 +661,7 @@ int spec_latent_compact(const spec_latent_cache* cache, int n_planes, int64_t st
  *   row_status    device [B] int32: SPEC_ROW_CACHE where source, keep_len (below 0
  *       or above cache_len[s]) or need (below 0) is unsound, which leaves b without
  *       blocks, where a kept entry is no block's id, or where room was asked for
- *       and not had: such a sequence must not be appended to.
+ *       and not had, by it or by a sequence before it (see above): such a sequence must not be appended to.
  *   workspace     spec_pages_workspace_bytes(...) bytes, 256-byte aligned, needing
  *       no initialisation
  * Errors: SPEC_ERR_ARG, SPEC_ERR_WORKSPACE as usual; SPEC_ERR_UNSUPPORTED for B >

@@ -281,7 +281,9 @@ def spec_pages_update(block_table, cache_len, refs, pools=(), *, planes: bool = 
     first pool, as the latent cache and the codes of an 8-bit one have it; a pool of scales does not tell it). out: cache_len, row_status and, where the
     rows are to go elsewhere, block_table; it is not changed. Returns block_table (without one in out: the
     given one, or with source a new one), cache_len [B] (the tokens kept), row_status [B], and refs. A
-    sequence with SPEC_ROW_CACHE in row_status must not be appended to."""
+    sequence with SPEC_ROW_CACHE in row_status must not be appended to. Where blocks do not suffice, that sequence and all later
+    ones with need > 0 are marked so and take none; they keep their tokens, and a further call with need 0 for those that have
+    to wait serves the others."""
     lib = _lib.load()
     dev, at = block_table.device, block_table.get_device()
     if at < 0:

@@ -64,3 +64,14 @@ def test_a_block_that_no_pool_tells():
     assert r["block_table"].tolist() == [[0, 1, -1], [2, 3, -1]]
     r = sv().spec_pages_update(table, length, refs, (scales, codes), block=16, keep_len=i32(20, 17 - 1).cuda())
     assert r["block_table"].tolist() == [[0, 1, -1], [2, -1, -1]]
+
+
+def test_room_after_a_request_that_failed():
+    """Later sequences that ask are refused with it, those too that have their room, and all keep their tokens; asked again without
+    it, they are served. One that asks nothing is not marked."""
+    r = sv().spec_pages_update(i32([0, -1, -1], [3, -1, -1], [4, -1, -1], [5, -1, -1]).cuda(), i32(15, 10, 16, 9).cuda(),
+                               i32(1, 0, 1, 1, 1, 1).cuda(), block=16, need=i32(33, 6, 1, 0).cuda())
+    assert r["row_status"].tolist() == [64, 64, 64, 0] and r["cache_len"].tolist() == [15, 10, 16, 9]
+    assert r["block_table"].tolist() == [[0, -1, -1], [3, -1, -1], [4, -1, -1], [5, -1, -1]] and r["refs"].tolist() == [1, 0, 1, 1, 1, 1]
+    r = sv().spec_pages_update(r["block_table"], r["cache_len"], r["refs"], block=16, need=i32(0, 6, 1, 0).cuda())
+    assert r["row_status"].tolist() == [0, 0, 0, 0] and r["block_table"].tolist() == [[0, -1, -1], [3, -1, -1], [4, 1, -1], [5, -1, -1]]
