@@ -9,6 +9,7 @@ import torch
 
 import latent_plain as plain
 from gpu_helpers import need_gpu
+from latent_dispatch import item_rows
 
 pytestmark = pytest.mark.gpu
 BF, HF = torch.bfloat16, torch.float16
@@ -24,18 +25,6 @@ def sv():
     import speculative_decoding_verification_29_gb300 as m
 
     return m
-
-
-def kernel_rows(c, heads, most):
-    """Rows of an item that the call's dispatch takes, told by its workspace: flags, cut items and two shares a part."""
-    W = c.C + c.R
-    need = sv().latent_workspace_bytes(torch.empty(1, c.bs, W, dtype=c.dt), c.C, heads, most)
-    up = lambda x: -(-x // 256) * 256  # noqa: E731
-    for rows in (16, 32, 48, 64, 128):
-        dims = c.C // 2 if rows == 128 and c.C > 256 else c.C
-        if need == up(152 * 4) + up(304 * 16) + up(304 * rows * 8) + up(304 * rows * dims * 4):
-            return rows
-    raise AssertionError(need)
 
 
 class Without:
@@ -73,7 +62,7 @@ def test_one_infinite_element(heads, n, C, R, rows, dt, masked, where):
     mask = tree(2, n) if masked else None
     for dim in (5, C - 3, C + 7):  # the first half of the values, the second, a shared one
         c = plain.Cache(ctx, [n, n], C, R, 32, dt, seed=C + dim).fill()
-        assert kernel_rows(c, heads, n) == rows
+        assert item_rows(c, heads, n) == rows
         t = at.get(where, 300)
         g = torch.Generator().manual_seed(dim)
         q = (torch.randn(2 * n, heads, C + R, generator=g) * 0.7).to(dt)
@@ -112,7 +101,7 @@ def test_whole_items(heads, rows):
     """Items of one tile: results that no join touches. Every sequence's last step token is infinite somewhere."""
     B, n, C = 90, 3, 512
     c = plain.Cache([i % 40 for i in range(B)], [n] * B, C, 64, 16, BF, seed=70).fill()
-    assert kernel_rows(c, heads, n) == rows
+    assert item_rows(c, heads, n) == rows
     q = (torch.randn(B * n, heads, C + 64, generator=torch.Generator().manual_seed(71)) * 0.7).to(BF)
     q[..., 400] = -1.0
     see = torch.ones(B, n, n, dtype=torch.uint8).tril()
