@@ -111,7 +111,10 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const void* map, uint32_t 
 // Two orders of the items' tiles over the thread blocks. In a row (Runs of kv8_attn.cuh): every block an equal run of all
 // items' tiles. In gangs: `gang` blocks, one for each item of a sequence, walk the same tiles at the same time, so that the
 // cache is read from memory once; a gang takes an equal run of the sequences' tiles.
-// Two long sequences of 36 items each: 1137 us in a row, 1028 in gangs; 64 x 6 items: 446, 406.
+// In a row and in gangs, us: two sequences of 110,001 to 131,072 tokens, 18 items each: 794, 675; 68 items, which leave 16 SMs
+// idle: 2673, 2471; 64 sequences of 1500 to 6500, 6 items each: 370, 299; 16 trees of 500 to 3500, 16 items: 143, 142. Where L2
+// holds the cache there is less to gain: two of 20,000 to 30,000, 76 items: 554, 539; 68 items: 487, 534; 62 items, whose 28 idle
+// SMs are more than an eighth: 448, 530.
 
 constexpr int kWhole = 1 << 30;  // rows of a row tile that is all of a sequence
 

@@ -43,7 +43,8 @@ namespace {
 
 // ---------------------------------------------------------- configuration --
 
-// Units of an item beside its tiles (see Runs): its queries, first maximum and results.
+// Units of an item beside its tiles (see Runs): its queries, first maximum and results. 64 sequences x 9 tokens x 32 heads: 258 us
+// with 0, 256 with 1, 254 with 3, 261 with 6; one token each 71, 70, 70, 74.
 constexpr int kCost = 3;
 constexpr int kPiece = kTile * 256, kShared = kTile * 128;  // bytes: 128 dimensions of a tile, its shared dimensions
 constexpr int kMaxPieces = 6, kMaxShared = 2;

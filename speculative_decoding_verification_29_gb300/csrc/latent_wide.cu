@@ -33,7 +33,8 @@ namespace specv {
 
 namespace {
 
-// Units of an item beside its tiles (see Runs): its queries and results.
+// Units of an item beside its tiles (see Runs): its queries and results. Three prompts of 500 to 1500 tokens: 175 us with 0, 156
+// with 2, 146 with 4 and 8; 16 trees of 61 tokens: 148, 147, 142, 144.
 constexpr int kCost = 4;
 constexpr int kRows = 128, kSlots = 64;  // rows of an item, slots of a tile
 constexpr int kChunk = kSlots * 128, kQChunk = kRows * 128;  // bytes of 64 dimensions of a tile, of the queries
