@@ -534,7 +534,7 @@ def spec_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache
     ``interleaved``, (2 i, 2 i + 1); positions [T] int32 where a token is rotated
     by another position than it is stored at (tree nodes: cache_len + depth).
     q [T, q_heads, head_dim]: queries, rotated alike into q_out (allocated when
-    None; may be q). Returns row_status [B] and, with q, q_out."""
+    None; may be q, must not overlap it otherwise). Returns row_status [B] and, with q, q_out."""
     lib = _lib.load()
     cache, dev = _kv8_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_len)
     D = cache.head_dim

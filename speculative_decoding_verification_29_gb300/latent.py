@@ -82,7 +82,7 @@ def spec_latent_append(latent, rope_key, cache, block_table, cache_len, cu_token
     spec_kv8_append, over all rot_dim dimensions. q_rope [T, q_heads, rot_dim]
     of latent's type (any strides, for example the last dimensions of the
     attention's queries): rotated alike into q_out (allocated when None; may be
-    q_rope). Returns row_status [B] and, with q_rope, q_out."""
+    q_rope, must not overlap it otherwise). Returns row_status [B] and, with q_rope, q_out."""
     lib = _lib.load()
     if latent.dim() != 2:
         raise ValueError("latent must be [tokens, latent_dim]")
