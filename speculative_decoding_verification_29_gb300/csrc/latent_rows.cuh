@@ -512,7 +512,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
       }
       __syncwarp();
-      const bool cleared = sm.odd[seg & 1] == seg + 1;  // set before the weights of its tile were ready
 #pragma unroll 1
       for (int p = 0; p < pieces; ++p) {
         __syncwarp();
@@ -520,21 +519,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         ld_cols<HN>(lanes + C::kO + 64 * p, x);
         wait_ld();
         settle<HN>(x);
-        if (cleared) {  // what it was, times a weight of 0
-#pragma unroll 1
-          for (int slot = max(max(t0, r.part) * kTile, r.ctx); slot < min(r.end, t1 * kTile); ++slot) {
-            const int id = a.c.table[static_cast<int64_t>(r.b) * a.c.max_blocks + slot / a.c.block];
-            if (id < 0 || id >= a.c.num_blocks) continue;
-            const uint16_t* e = reinterpret_cast<const uint16_t*>(a.c.k + id * a.c.sb + (slot % a.c.block) * a.c.ss);
-            const bool bad = (e[128 * p + own] & (B::kExp & 0xffffu)) == (B::kExp & 0xffffu);
-            if (!__any_sync(0xffffffffu, bad)) continue;
-            const bool saw = sees(a, r.b, min(r.n - 1, (r0 + lane) / a.group), slot - r.ctx);  // the group's row `lane`
-            const uint32_t rows = __ballot_sync(0xffffffffu, saw);
-#pragma unroll
-            for (int j = 0; j < HN; ++j)
-              if (bad && (rows >> j) & 1) x[j] = 0x7fffffffu;
-          }
-        }
         if (!whole) {
           float* o = a.part_o + (part * N + group * HN) * dims + 128 * p + own;
 #pragma unroll
@@ -554,6 +538,26 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           if (vec_o) *reinterpret_cast<uint32_t*>(o) = B::pack(lo, hi);
           else o[0] = from_f<QT>(lo), o[1] = from_f<QT>(hi);
         }
+      }
+      __syncwarp();
+      if (sm.odd[seg & 1] == seg + 1) {  // set before the weights of its tile were ready: what was cleared, times a weight of 0
+#pragma unroll 1
+        for (int slot = max(max(t0, r.part) * kTile, r.ctx); slot < min(r.end, t1 * kTile); ++slot) {
+          const int id = a.c.table[static_cast<int64_t>(r.b) * a.c.max_blocks + slot / a.c.block];
+          if (id < 0 || id >= a.c.num_blocks) continue;
+          const uint16_t* e = reinterpret_cast<const uint16_t*>(a.c.k + id * a.c.sb + (slot % a.c.block) * a.c.ss);
+#pragma unroll 1
+          for (int d = own; d < dims; d += kTile) {
+            if ((e[d] & (B::kExp & 0xffffu)) != (B::kExp & 0xffffu)) continue;
+#pragma unroll 1
+            for (int j = 0; j < HN && group * HN + j < r.rows; ++j) {
+              if (!sees(a, r.b, (r0 + j) / a.group, slot - r.ctx)) continue;
+              if (whole) static_cast<QT*>(a.out)[sm.to[group][j] + d] = from_f<QT>(__int_as_float(0x7fffffff));
+              else a.part_o[(part * N + group * HN + j) * dims + d] = __int_as_float(0x7fffffff);
+            }
+          }
+        }
+        __syncwarp();
       }
       fence_before();
     }

@@ -441,7 +441,30 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // ---- the item's results, or its share of them
       const bool whole = t0 == 0 && t1 == r.tiles;
       const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (t0 > 0 ? 0 : 1);
-      const bool cleared = sm.odd[seg & 1] == seg + 1;  // set before the weights of its tile were ready
+      if (sm.odd[seg & 1] == seg + 1) {  // set before the weights of its tile were ready: what was cleared, times a weight of 0
+#pragma unroll 1
+        for (int slot = max(max(s0, sp.part) * kSlots, r.ctx); slot < min(r.end, s1 * kSlots); ++slot) {
+          const int id = a.c.table[static_cast<int64_t>(r.b) * a.c.max_blocks + slot / a.c.block];
+          if (id < 0 || id >= a.c.num_blocks) continue;
+          const uint16_t* e = reinterpret_cast<const uint16_t*>(a.c.k + id * a.c.sb + (slot % a.c.block) * a.c.ss) + h * vd;
+          const bool saw = tok < r.n && sees(a, r.b, tok, slot - r.ctx);
+#pragma unroll 1
+          for (int c = 0; c < vd; c += 32) {
+            const uint32_t bad = __ballot_sync(0xffffffffu, (e[c + lane] & (B::kExp & 0xffffu)) == (B::kExp & 0xffffu));
+            if (bad == 0) continue;
+            uint32_t x[32];
+            tmem_ld<32>(lanes + c, x);
+            wait_ld();
+            settle<32>(x);
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (saw && (bad >> k) & 1) x[k] = 0x7fffffffu;
+            tmem_st16(lanes + c, x);
+            tmem_st16(lanes + c + 16, x + 16);
+            wait_st();
+          }
+        }
+      }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       if (!whole && own < r.rows) a.part_ml[part * kRows + own] = make_float2(ref, sum);
       int64_t at[4];  // of the rows that the lane stores a part of: results, or shares in the workspace
@@ -460,20 +483,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         tmem_ld<32>(lanes + c, x);
         wait_ld();
         settle<32>(x);
-        if (cleared) {  // what it was, times a weight of 0
-#pragma unroll 1
-          for (int slot = max(max(s0, sp.part) * kSlots, r.ctx); slot < min(r.end, s1 * kSlots); ++slot) {
-            const int id = a.c.table[static_cast<int64_t>(r.b) * a.c.max_blocks + slot / a.c.block];
-            if (id < 0 || id >= a.c.num_blocks) continue;
-            const uint16_t* e = reinterpret_cast<const uint16_t*>(a.c.k + id * a.c.sb + (slot % a.c.block) * a.c.ss);
-            const uint32_t bad = __ballot_sync(0xffffffffu, (e[h * vd + c + lane] & (B::kExp & 0xffffu)) == (B::kExp & 0xffffu));
-            if (bad == 0 || tok >= r.n || !sees(a, r.b, tok, slot - r.ctx)) continue;
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if ((bad >> k) & 1) x[k] = 0x7fffffffu;
-          }
-          __syncwarp();
-        }
         if (!whole) {
 #pragma unroll
           for (int g = 0; g < 32; g += 16) {
